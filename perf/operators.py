@@ -1,0 +1,348 @@
+"""What is measured of the paged FP8 KV cache: writing and reading it, and the
+attention over it for a batch of sequences that share a prefix.
+
+Two operators:
+
+* ``cache`` -- keys and values of new tokens go into the pages (E4M3 codes, one
+  power-of-two scale per token and head), and a set of cached tokens is read
+  back as dense rows.
+* ``attention`` -- queries of a batch attend to a prefix that all sequences
+  share and to each sequence's own pages (causal among the last q_len tokens).
+
+The page layout (a block is 16 tokens of one head): token o of the block and
+dimension d sit at byte (o // 4) * 4 * D + (d // 16) * 64 + (o % 4) * 16 + d % 16
+of a key block and at byte d * 16 + o of a value block.
+"""
+import math
+
+import torch
+
+own = False
+
+_DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------------ cases
+
+def listed():
+    """Each case says what it stands for."""
+    def cache(name, seqs, new, old, heads, dim, page, dtype):
+        return dict(name=name, op="cache", seqs=seqs, new=new, old=old, heads=heads, dim=dim, page=page, dtype=dtype)
+
+    def attn(name, batch, q_len, prefix, max_len, q_heads, kv_heads, dim, page, dtype, ragged=True, empty=False):
+        return dict(name=name, op="attention", batch=batch, q_len=q_len, prefix=prefix, max_len=max_len,
+                    q_heads=q_heads, kv_heads=kv_heads, dim=dim, page=page, dtype=dtype, ragged=ragged, empty=empty)
+
+    return [
+        # one decode step of 64 sequences: a row each, at whatever slot the sequence has reached
+        cache("cache step 64x1", 64, 1, 0, 8, 128, 16, "bf16"),
+        # a chunk of a long prompt that follows 4099 cached tokens; the whole context comes back for a dense pass
+        cache("cache chunk 2041 after 4099", 1, 2041, 4099, 4, 256, 64, "bf16"),
+        # a whole prompt of 32768 tokens
+        cache("cache prompt 32768", 1, 32768, 0, 8, 128, 64, "bf16"),
+        # float32 keys and values of three short prompts, an odd number of heads
+        cache("cache f32 3x777", 3, 777, 0, 5, 64, 32, "f32"),
+        # the first steps of one conversation: latency
+        attn("decode 1x127", 1, 1, 0, 127, 32, 8, 128, 64, "bf16", ragged=False),
+        # an ordinary decode batch of unequal contexts, one of them empty
+        attn("decode 64 to 4096", 64, 1, 0, 4096, 32, 8, 128, 16, "bf16", empty=True),
+        # one very long context, the head shape of wide-head models
+        attn("decode 1x131073", 1, 1, 0, 131073, 24, 4, 256, 64, "bf16", ragged=False),
+        # a system prompt shared by a few conversations
+        attn("prefix 2000, 16 to 300", 16, 1, 2000, 300, 32, 8, 128, 32, "bf16"),
+        # a long document shared by many questions, wide heads
+        attn("prefix 16384, 64 to 1024", 64, 1, 16384, 1024, 24, 4, 256, 64, "bf16"),
+        # the same at the largest: many samples of one long prompt
+        attn("prefix 32768, 256 to 512", 256, 1, 32768, 512, 32, 8, 128, 64, "bf16"),
+        # five drafted tokens a sequence, in float32
+        attn("drafts 24x5 f32", 24, 5, 1531, 777, 12, 4, 64, 16, "f32"),
+        # 512-token chunks of four prompts behind a shared system prompt
+        attn("chunk 4x512, prefix 4096", 4, 512, 4096, 1536, 32, 8, 128, 64, "bf16"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.49)))))))
+
+
+def draw(rng):
+    while True:
+        dtype = "f32" if rng.random() < 0.25 else "bf16"
+        dim, page = rng.choice([64, 128, 128, 256]), rng.choice([16, 32, 64, 128])
+        if rng.random() < 0.35:
+            c = dict(op="cache", seqs=_log(rng, 1, 256), new=_log(rng, 1, 32768), old=rng.choice([0, _log(rng, 1, 16384)]),
+                     heads=rng.randint(1, 8), dim=dim, page=page, dtype=dtype)
+            if c["seqs"] * (2 * c["new"] + c["old"]) * c["heads"] * dim * _DT[dtype].itemsize <= 2 * 32768 * 1024 * 2:
+                return c
+            continue
+        kv, batch = rng.randint(1, 8), _log(rng, 1, 256)
+        q_len = rng.choice([1, 1, 1, rng.randint(2, 8), _log(rng, 16, 512)])
+        prefix = rng.choice([0, _log(rng, 1, 32768), _log(rng, 256, 32768)])
+        c = dict(op="attention", batch=batch, q_len=q_len, prefix=prefix, max_len=max(q_len, _log(rng, 1, 131072)),
+                 q_heads=kv * rng.randint(1, 8), kv_heads=kv, dim=dim, page=page, dtype=dtype,
+                 ragged=rng.random() < 0.7, empty=rng.random() < 0.3)
+        w = work(c)
+        scores = c["q_heads"] * batch * q_len * (prefix + c["max_len"])
+        gathered = (batch * c["max_len"] + prefix) * kv * dim
+        if w["flops"] <= (30e9 if dtype == "f32" else 130e9) and w["bytes"] <= 2.6e8 and scores <= 3e8 and gathered <= 1.4e8:
+            return c
+
+
+def _lens(c):
+    """The sequences' own lengths: full, or spread over (0, max_len] in an order that is not sorted."""
+    n, top = c["batch"], c["max_len"]
+    step = next(s for s in range(max(1, n * 5 // 8), 2 * n + 2) if math.gcd(s, n) == 1)
+    lens = [max(c["q_len"], -(-top * (1 + b * step % n) // n)) if c["ragged"] else top for b in range(n)]
+    if c["empty"]:
+        lens[n // 2] = 0  # a place of the batch that holds no tokens yet
+    return lens
+
+
+def work(case):
+    c = case
+    size = _DT[c["dtype"]].itemsize
+    if c["op"] == "cache":
+        width, new, out = c["heads"] * c["dim"], c["seqs"] * c["new"], c["seqs"] * (c["new"] + c["old"])
+        per = width + c["heads"]  # codes and scales of a token, keys or values
+        return {"bytes": 2 * (new * (width * size + per) + out * (per + width * size)), "flops": 2 * 2 * (new + out) * width}
+    lens, q = _lens(c), c["q_len"]
+    seen = sum(c["prefix"] + max(0, n - q + 1 + j) for n in lens for j in range(q))
+    tokens = c["prefix"] + sum(lens)
+    return {"bytes": 2 * tokens * c["kv_heads"] * (c["dim"] + 1) + 2 * c["batch"] * q * c["q_heads"] * c["dim"] * size,
+            "flops": 4 * c["dim"] * c["q_heads"] * seen}
+
+
+# ----------------------------------------------------------------- inputs
+
+def _key_view(t, heads, dim, page):
+    return t.view(-1, heads, page // 16, 4, dim // 16, 4, 16)
+
+
+def _value_view(t, heads, dim, page):
+    return t.view(-1, heads, page // 16, dim, 16)
+
+
+def _scale_byte(x):
+    """e + 127 with e the least integer (not below -126) such that max|x| <= 448 * 2^e, over the last dimension."""
+    frac, e = torch.frexp(x.abs().amax(-1))  # max = frac * 2^e, frac in [0.5, 1); 448 = 0.875 * 2^9
+    return (e - 9 + (frac > 0.875) + 127).clamp(min=1)
+
+
+def _power(b):
+    """2^(b - 127) as float32, 1 <= b <= 254."""
+    return (b.int() << 23).view(torch.float32)
+
+
+def _encode(x):
+    """E4M3 codes and scale bytes of x [..., D] in float32."""
+    b = _scale_byte(x)
+    y = x * _power(254 - b)[..., None]
+    return y.to(torch.float8_e4m3fn).view(torch.uint8), b.to(torch.uint8)
+
+
+def _store(s, slots, kc, ks, vc, vs):
+    """Codes [rows, H, D] and scale bytes [rows, H] to their places in the pages."""
+    heads, dim, page = s["heads"], s["dim"], s["page"]
+    p, o = slots // page, slots % page
+    _key_view(s["k_codes"], heads, dim, page)[p, :, o // 16, o % 16 // 4, :, o % 4, :] = kc.view(-1, heads, dim // 16, 16)
+    _value_view(s["v_codes"], heads, dim, page)[p, :, o // 16, :, o % 16] = vc
+    s["k_scales"].view(-1, heads, page)[p, :, o] = ks
+    s["v_scales"].view(-1, heads, page)[p, :, o] = vs
+
+
+def _load(s, slots):
+    """Keys and values [rows, H, D] of the slots as float32."""
+    heads, dim, page = s["heads"], s["dim"], s["page"]
+    p, o = slots // page, slots % page
+    kc = _key_view(s["k_codes"], heads, dim, page)[p, :, o // 16, o % 16 // 4, :, o % 4, :].reshape(-1, heads, dim)
+    vc = _value_view(s["v_codes"], heads, dim, page)[p, :, o // 16, :, o % 16]
+    ks = _power(s["k_scales"].view(-1, heads, page)[p, :, o])
+    vs = _power(s["v_scales"].view(-1, heads, page)[p, :, o])
+    return kc.view(torch.float8_e4m3fn).float() * ks[..., None], vc.view(torch.float8_e4m3fn).float() * vs[..., None]
+
+
+def _rows(gen, n, heads, dim):
+    """Keys or values as a projection gives them: a few channels of every head are large."""
+    x = torch.randn(n, heads, dim, generator=gen, device="cuda")
+    loud = 1 + 5 * (torch.rand(heads, dim, generator=gen, device="cuda") > 0.97)
+    return x * loud
+
+
+def _pages(c, heads, dim, n_pages):
+    page = c["page"]
+    new = lambda width: torch.zeros(n_pages, width, dtype=torch.uint8, device="cuda")  # noqa: E731
+    return dict(heads=heads, dim=dim, page=page, k_codes=new(heads * page * dim), v_codes=new(heads * page * dim),
+                k_scales=new(heads * page), v_scales=new(heads * page))
+
+
+def _fill(s, gen, slots):
+    for part in slots.split(1 << 16):
+        kc, ks = _encode(_rows(gen, len(part), s["heads"], s["dim"]))
+        vc, vs = _encode(_rows(gen, len(part), s["heads"], s["dim"]))
+        _store(s, part, kc, ks, vc, vs)
+
+
+def prepare(case, seed):
+    c = case
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    page, dtype = c["page"], _DT[c["dtype"]]
+    if c["op"] == "cache":
+        total = c["old"] + c["new"]
+        per = -(-total // page)
+        s = _pages(c, c["heads"], c["dim"], c["seqs"] * per + 1)
+        ids = torch.randperm(c["seqs"] * per + 1, generator=gen, device="cuda")[: c["seqs"] * per].view(c["seqs"], per)
+        at = torch.arange(total, device="cuda")
+        slots = ids[:, at // page] * page + at % page  # [seqs, total]
+        if c["old"]:
+            _fill(s, gen, slots[:, : c["old"]].reshape(-1))
+        n = c["seqs"] * c["new"]
+        s.update(op="cache", dtype=dtype, slots=slots[:, c["old"]:].reshape(-1).contiguous(), wanted=slots.reshape(-1).contiguous(),
+                 k=_rows(gen, n, c["heads"], c["dim"]).to(dtype).view(n, -1), v=_rows(gen, n, c["heads"], c["dim"]).to(dtype).view(n, -1))
+        return s
+    lens, q = _lens(c), c["q_len"]
+    per, shared = -(-c["max_len"] // page), -(-c["prefix"] // page)
+    n_pages = c["batch"] * per + shared + 1
+    s = _pages(c, c["kv_heads"], c["dim"], n_pages)
+    ids = torch.randperm(n_pages, generator=gen, device="cuda").int()
+    table, prefix_pages = ids[: c["batch"] * per].view(c["batch"], per).contiguous(), ids[c["batch"] * per: n_pages - 1].contiguous()
+    at = torch.arange(c["max_len"], device="cuda")
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    slots = table.long()[:, at // page] * page + at % page
+    _fill(s, gen, slots[at[None] < lens_t[:, None]])
+    if c["prefix"]:
+        at = torch.arange(c["prefix"], device="cuda")
+        _fill(s, gen, prefix_pages.long()[at // page] * page + at % page)
+    x = torch.randn(c["batch"] * q, c["q_heads"] * c["dim"], generator=gen, device="cuda") * 1.5
+    s.update(op="attention", dtype=dtype, q=x.to(dtype), table=table, lens=lens_t, prefix_pages=prefix_pages, prefix=c["prefix"],
+             q_len=q, q_heads=c["q_heads"], max_len=c["max_len"], work=None)
+    return s
+
+
+# -------------------------------------------------------------- one pass
+
+def run(state):
+    s = state
+    if own:
+        return _own(s)
+    if s["op"] == "cache":
+        heads, dim = s["heads"], s["dim"]
+        kc, ks = _encode(s["k"].float().view(-1, heads, dim))
+        vc, vs = _encode(s["v"].float().view(-1, heads, dim))
+        _store(s, s["slots"], kc, ks, vc, vs)
+        k, v = _load(s, s["wanted"])
+        return k.reshape(len(k), -1).to(s["dtype"]), v.reshape(len(v), -1).to(s["dtype"])
+    heads, dim, page, q_len, prefix = s["heads"], s["dim"], s["page"], s["q_len"], s["prefix"]
+    batch, group = len(s["lens"]), s["q_heads"] // heads
+    q = s["q"].float().view(batch, q_len, heads, group, dim).permute(2, 0, 1, 3, 4) * dim ** -0.5  # [H, B, q_len, group, D]
+    # each sequence's own tokens, padded to the longest and masked
+    at = torch.arange(s["max_len"], device=q.device)
+    ks, vs = _load(s, (s["table"].long()[:, at // page] * page + at % page).reshape(-1))
+    ks, vs = (x.view(batch, -1, heads, dim).permute(2, 0, 1, 3) for x in (ks, vs))  # [H, B, S, D]
+    limit = s["lens"][:, None] - q_len + 1 + torch.arange(q_len, device=q.device)  # [B, q_len]
+    seen = (at < limit[:, :, None])[:, :, None, :]  # [B, q_len, 1, S]
+    own_scores = torch.matmul(q.reshape(heads, batch, q_len * group, dim), ks.transpose(2, 3).contiguous())
+    own_scores = own_scores.view(heads, batch, q_len, group, -1).masked_fill(~seen, -math.inf)
+    top = own_scores.amax(-1, keepdim=True)
+    if prefix:
+        at = torch.arange(prefix, device=q.device)
+        kp, vp = _load(s, s["prefix_pages"].long()[at // page] * page + at % page)
+        kp, vp = kp.permute(1, 2, 0).contiguous(), vp.permute(1, 0, 2).contiguous()
+        scores = torch.matmul(q.reshape(heads, -1, dim), kp).view(heads, batch, q_len, group, prefix)
+        top = torch.maximum(top, scores.amax(-1, keepdim=True))
+    top = top.masked_fill(top == -math.inf, 0.0)
+    p = torch.exp(own_scores - top)
+    total = p.sum(-1, keepdim=True)
+    o = torch.matmul(p.view(heads, batch, q_len * group, -1), vs.contiguous()).view(heads, batch, q_len, group, dim)
+    if prefix:
+        p = torch.exp(scores - top)
+        total = total + p.sum(-1, keepdim=True)
+        o = o + torch.matmul(p.view(heads, -1, prefix), vp).view(heads, batch, q_len, group, dim)
+    o = torch.where(total > 0, o / total, 0.0)
+    return o.permute(1, 2, 0, 3, 4).reshape(batch * q_len, -1).to(s["dtype"])
+
+
+def _own(s):
+    import bit_linear_layer_amd as nv
+
+    pages = nv.KVPages(s["k_codes"], s["v_codes"], s["k_scales"], s["v_scales"], s["heads"], s["dim"], s["page"])
+    if s["op"] == "cache":
+        nv.kv_pages_write(pages, s["k"], s["v"], s["slots"])
+        return nv.kv_pages_read(pages, s["wanted"], out_dtype=s["dtype"])
+    if s["work"] is None:  # a server keeps its workspace
+        s["work"] = nv.kv_pages_attention_workspace(s["q"], pages, len(s["lens"]), q_len=s["q_len"], prefix_len=s["prefix"])
+    return nv.kv_pages_attention(s["q"], pages, s["table"], s["lens"], q_len=s["q_len"], prefix_pages=s["prefix_pages"],
+                                 prefix_len=s["prefix"], max_len=s["max_len"], workspace=s["work"])
+
+
+# ------------------------------------------------------ the definition, in 64 bits
+
+def _e4m3_values():
+    """The 256 values of a byte: sign, four exponent bits (bias 7), three mantissa bits."""
+    out = []
+    for b in range(256):
+        e, m = b >> 3 & 15, b & 7
+        mag = m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10)
+        out.append(-mag if b & 128 else mag)
+    return torch.tensor(out, dtype=torch.float64, device="cuda")
+
+
+def _nearest(x):
+    """x [..., D] in 64 bits through the cache: the nearest E4M3 multiple of the row's scale, ties to even."""
+    top = x.abs().amax(-1, keepdim=True)
+    e = torch.ceil(torch.log2(top.clamp(min=1e-300) / 448)).clamp(min=-126)
+    e = torch.where(top > 448 * torch.exp2(e), e + 1, e)
+    e = torch.where((top <= 448 * torch.exp2(e - 1)) & (e > -126), e - 1, e)
+    y = x / torch.exp2(e)
+    lead = torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -20)))
+    lead = torch.where(y.abs() < torch.exp2(lead), lead - 1, torch.where(y.abs() >= torch.exp2(lead + 1), lead + 1, lead))
+    step = torch.exp2(lead.clamp(min=-6) - 3)
+    return torch.round(y / step) * step * torch.exp2(e)
+
+
+def _tokens(s, slots, h, table):
+    """Keys and values [n, D] of head h at the slots, byte by byte from the layout's formula."""
+    dim, page = s["dim"], s["page"]
+    o, d = (slots % 16)[:, None], torch.arange(dim, device="cuda")[None]
+    row = (slots // page)[:, None] * (s["heads"] * page * dim) + (h * page + slots % page // 16 * 16)[:, None] * dim
+    kb = s["k_codes"].view(-1)[row + o // 4 * 4 * dim + d // 16 * 64 + o % 4 * 16 + d % 16]
+    vb = s["v_codes"].view(-1)[row + d * 16 + o]
+    at = slots // page * (s["heads"] * page) + h * page + slots % page
+    ks, vs = (torch.exp2(s[x].view(-1)[at].double() - 127)[:, None] for x in ("k_scales", "v_scales"))
+    return table[kb.long()] * ks, table[vb.long()] * vs
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    table = _e4m3_values()
+    heads, dim, page = s["heads"], s["dim"], s["page"]
+    if s["op"] == "cache":
+        out = []
+        for name, part in (("k", 0), ("v", 1)):
+            whole = torch.empty(len(s["wanted"]), heads, dim, dtype=torch.float64, device="cuda")
+            for h in range(heads):
+                whole[:, h] = _tokens(s, s["wanted"], h, table)[part]
+            new = _nearest(s[name].double().view(-1, heads, dim))
+            whole.view(case["seqs"], -1, heads, dim)[:, case["old"]:] = new.view(case["seqs"], case["new"], heads, dim)
+            out.append(whole.view(len(whole), -1))
+        return tuple(out)
+    batch, q_len, group = case["batch"], s["q_len"], s["q_heads"] // heads
+    q = s["q"].double().view(batch, q_len, s["q_heads"], dim)
+    out = torch.zeros(batch, q_len, s["q_heads"], dim, dtype=torch.float64, device="cuda")
+    at = torch.arange(s["prefix"], device="cuda")
+    first = s["prefix_pages"].long()[at // page] * page + at % page
+    lens = s["lens"].tolist()
+    for h in range(heads):
+        kp, vp = _tokens(s, first, h, table)
+        for b in range(batch):
+            at = torch.arange(lens[b], device="cuda")
+            k, v = _tokens(s, s["table"].long()[b][at // page] * page + at % page, h, table)
+            k, v = torch.cat([kp, k]), torch.cat([vp, v])
+            if not len(k):
+                continue
+            x = q[b, :, h * group:(h + 1) * group].reshape(-1, dim) @ k.T / math.sqrt(dim)
+            last = s["prefix"] + lens[b] - q_len + torch.arange(q_len, device="cuda").repeat_interleave(group)
+            x = x.masked_fill(torch.arange(len(k), device="cuda")[None] > last[:, None], -math.inf)
+            p = torch.exp(x - x.amax(-1, keepdim=True).clamp(min=-1e300))
+            y = p @ v / p.sum(-1, keepdim=True).clamp(min=1e-300)
+            out[b, :, h * group:(h + 1) * group] = y.view(q_len, group, dim)
+    return out.view(batch * q_len, -1)
