@@ -269,7 +269,8 @@ def _own(s):
         nv.kv_pages_write(pages, s["k"], s["v"], s["slots"])
         return nv.kv_pages_read(pages, s["wanted"], out_dtype=s["dtype"])
     if s["work"] is None:  # a server keeps its workspace
-        s["work"] = nv.kv_pages_attention_workspace(s["q"], pages, len(s["lens"]), q_len=s["q_len"], prefix_len=s["prefix"])
+        s["work"] = nv.kv_pages_attention_workspace(s["q"], pages, len(s["lens"]), q_len=s["q_len"], max_len=s["max_len"],
+                                                    prefix_len=s["prefix"])
     return nv.kv_pages_attention(s["q"], pages, s["table"], s["lens"], q_len=s["q_len"], prefix_pages=s["prefix_pages"],
                                  prefix_len=s["prefix"], max_len=s["max_len"], workspace=s["work"])
 
