@@ -22,6 +22,9 @@ __all__ = [
     "DecodeWeight", "nvfp4_decode_weight_bytes", "nvfp4_decode_weight_pack", "nvfp4_gemm_decode",
     "nvfp4_linear_decode", "pack_decode", "gemm_decode", "linear_decode",
     "empty_nvfp4", "quantize", "gemm", "gemm_fused_segments", "silu_mul", "workspace_for",
+    "KVPages", "empty_kv_pages", "nvfp4_kv_pages_write", "nvfp4_kv_pages_read", "nvfp4_kv_pages_attention",
+    "nvfp4_kv_pages_attention_workspace_bytes", "kv_pages_write", "kv_pages_read", "kv_pages_attention",
+    "kv_pages_attention_workspace",
     "DTYPE_BF16", "DTYPE_F32", "SCALE_DYNAMIC", "SCALE_STATIC", "AMAX_PRECOMPUTED", "MAX_SEGMENTS",
 ]
 
@@ -56,6 +59,19 @@ class _GdnInputs(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("ld_q", ctypes.c_int64), ("k", ctypes.c_void_p), ("ld_k", ctypes.c_int64),
                 ("v", ctypes.c_void_p), ("ld_v", ctypes.c_int64), ("beta", ctypes.c_void_p),
                 ("ld_beta", ctypes.c_int64), ("g", ctypes.c_void_p), ("ld_g", ctypes.c_int64)]
+
+
+class _KVPages(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("ld_codes", ctypes.c_int64),
+                ("ld_scales", ctypes.c_int64), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("q_len", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("max_len", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_cols", ctypes.c_int64),
+                ("ld_table", ctypes.c_int64), ("prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int64)]
 
 
 _lib = None
@@ -117,6 +133,16 @@ def load() -> ctypes.CDLL:
         lib.nvfp4_gdn_recurrence.argtypes = [ctypes.POINTER(_GdnInputs), ctypes.c_int, _I64, ctypes.c_int, ctypes.c_int,
                                              ctypes.c_int, _P, _P, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
         lib.nvfp4_gdn_recurrence.restype = ctypes.c_int
+        pages, batch = ctypes.POINTER(_KVPages), ctypes.POINTER(_KVBatch)
+        lib.nvfp4_kv_pages_write.argtypes = [pages, _P, _I64, _P, _I64, ctypes.c_int, _I64, _P, _P]
+        lib.nvfp4_kv_pages_write.restype = ctypes.c_int
+        lib.nvfp4_kv_pages_read.argtypes = [pages, _I64, _P, _P, _I64, _P, _I64, ctypes.c_int, _P]
+        lib.nvfp4_kv_pages_read.restype = ctypes.c_int
+        lib.nvfp4_kv_pages_attention_workspace_bytes.argtypes = [pages, batch, ctypes.c_int, ctypes.c_int]
+        lib.nvfp4_kv_pages_attention_workspace_bytes.restype = ctypes.c_size_t
+        lib.nvfp4_kv_pages_attention.argtypes = [pages, batch, _P, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_float, _P,
+                                                 _I64, _P, ctypes.c_size_t, _P]
+        lib.nvfp4_kv_pages_attention.restype = ctypes.c_int
         lib.nvfp4_status_string.argtypes = [ctypes.c_int]
         lib.nvfp4_status_string.restype = ctypes.c_char_p
         lib.nvfp4_version.argtypes = []
@@ -441,6 +467,183 @@ def nvfp4_gdn_recurrence(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta
     _check(st, "nvfp4_gdn_recurrence")
 
 
+@dataclass
+class KVPages:
+    """A paged FP8 KV cache in device memory (layout in include/nvfp4.h):
+    codes uint8 [n_pages, >= kv_heads * page_size * head_dim], scales uint8
+    [n_pages, >= kv_heads * page_size], one row stride for both codes and one
+    for both scales."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    kv_heads: int
+    head_dim: int
+    page_size: int
+
+    @property
+    def n_pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def device(self) -> torch.device:
+        return self.k_codes.device
+
+    def descriptor(self) -> _KVPages:
+        kc, vc, ks, vs = self.k_codes, self.v_codes, self.k_scales, self.v_scales
+        per = self.kv_heads * self.page_size
+        for t, width, like in ((kc, per * self.head_dim, kc), (vc, per * self.head_dim, kc), (ks, per, ks), (vs, per, ks)):
+            if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != kc.shape[0] or t.shape[1] < width or t.stride(1) != 1:
+                raise NVFP4Error(f"cache tensors must be uint8 [n_pages, >= {width}] with contiguous rows")
+            if t.stride(0) != like.stride(0):
+                raise NVFP4Error("key and value tensors of a cache must share their row stride")
+            if t.device != kc.device or not t.is_cuda:
+                raise NVFP4Error("cache tensors must live on one GPU")
+        return _KVPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), kc.shape[0],
+                        max(kc.stride(0), kc.shape[1]), max(ks.stride(0), ks.shape[1]), self.kv_heads, self.head_dim,
+                        self.page_size)
+
+
+def empty_kv_pages(n_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> KVPages:
+    """An uninitialized paged KV cache of n_pages * page_size slots."""
+    def new(width):
+        return torch.empty((n_pages, width), dtype=torch.uint8, device=device)
+    per = kv_heads * page_size
+    return KVPages(new(per * head_dim), new(per * head_dim), new(per), new(per), kv_heads, head_dim, page_size)
+
+
+def _on(t: torch.Tensor, device: torch.device, what: str) -> None:
+    if t.device != device:
+        raise NVFP4Error(f"{what} must live on {device}, got {t.device}")
+
+
+def _kv_rows(t: torch.Tensor, rows: int, pages: KVPages, what: str) -> None:
+    _on(t, pages.device, what)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != pages.kv_heads * pages.head_dim or t.stride(1) != 1:
+        raise NVFP4Error(f"{what} must be [{rows}, {pages.kv_heads * pages.head_dim}] with contiguous rows, got {tuple(t.shape)}")
+
+
+def _kv_slots(slots: torch.Tensor, pages: KVPages) -> None:
+    _on(slots, pages.device, "slots")
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        raise NVFP4Error("slots must be a contiguous 1-D int64 tensor")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows; a single row may carry any stride."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+class _device_of:
+    """Makes a tensor's GPU the current one for a call on one of its streams."""
+
+    def __init__(self, device: torch.device):
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def nvfp4_kv_pages_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """C ``nvfp4_kv_pages_write``: rows of k and v [rows, kv_heads * head_dim]
+    to the cache slots ``slots`` (int64 device tensor, distinct; a row whose
+    slot is outside the cache is dropped)."""
+    d = pages.descriptor()
+    _kv_slots(slots, pages)
+    _kv_rows(k, slots.shape[0], pages, "k")
+    _kv_rows(v, slots.shape[0], pages, "v")
+    if k.dtype != v.dtype:
+        raise NVFP4Error("k and v must share one dtype")
+    with _device_of(pages.device):
+        st = load().nvfp4_kv_pages_write(ctypes.byref(d), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
+                                         _dtype_code(k), slots.shape[0], slots.data_ptr(), _stream(pages.device, stream))
+    _check(st, "nvfp4_kv_pages_write")
+
+
+def nvfp4_kv_pages_read(pages: KVPages, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+                        stream=None) -> None:
+    """C ``nvfp4_kv_pages_read``: the cached rows at ``slots`` as dense keys
+    and values (rows whose slot is outside the cache stay as they were)."""
+    d = pages.descriptor()
+    _kv_slots(slots, pages)
+    _kv_rows(k_out, slots.shape[0], pages, "k_out")
+    _kv_rows(v_out, slots.shape[0], pages, "v_out")
+    if k_out.dtype != v_out.dtype:
+        raise NVFP4Error("k_out and v_out must share one dtype")
+    with _device_of(pages.device):
+        st = load().nvfp4_kv_pages_read(ctypes.byref(d), slots.shape[0], slots.data_ptr(), k_out.data_ptr(),
+                                        _row_stride(k_out), v_out.data_ptr(), _row_stride(v_out), _dtype_code(k_out),
+                                        _stream(pages.device, stream))
+    _check(st, "nvfp4_kv_pages_read")
+
+
+def nvfp4_kv_pages_attention_workspace_bytes(pages: KVPages, batch: int, q_heads: int, dtype: torch.dtype,
+                                             q_len: int = 1, max_len: int = 0, prefix_len: int = 0) -> int:
+    """C ``nvfp4_kv_pages_attention_workspace_bytes``; 0 for a shape that the
+    attention does not take."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise NVFP4Error(f"unsupported dtype {dtype}")
+    d = pages.descriptor()
+    b = _KVBatch(batch, q_len, None, max_len, None, 0, 0, None, prefix_len)
+    return int(load().nvfp4_kv_pages_attention_workspace_bytes(
+        ctypes.byref(d), ctypes.byref(b), q_heads, DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32))
+
+
+def nvfp4_kv_pages_attention(q: torch.Tensor, pages: KVPages, out: torch.Tensor, workspace: torch.Tensor, scale: float,
+                             batch: int, q_len: int = 1, table: torch.Tensor | None = None,
+                             lens: torch.Tensor | None = None, max_len: int | None = None,
+                             prefix_pages: torch.Tensor | None = None, prefix_len: int = 0, stream=None) -> None:
+    """C ``nvfp4_kv_pages_attention``: q and out [batch * q_len, q_heads *
+    head_dim]; table int32 [batch, cols], lens int32 [batch] (device);
+    max_len a host bound of lens (default: what the table can hold);
+    prefix_pages int32 (device) with the prefix_len shared tokens."""
+    d = pages.descriptor()
+    device = pages.device
+    width = q.shape[1] if q.dim() == 2 else 0
+    if width == 0 or width % pages.head_dim != 0 or q.shape[0] != batch * q_len or q.stride(1) != 1:
+        raise NVFP4Error(f"q must be [{batch * q_len}, q_heads * {pages.head_dim}] with contiguous rows")
+    if out.shape != q.shape or out.stride(1) != 1 or out.dtype != q.dtype:
+        raise NVFP4Error("out must have q's shape and dtype and contiguous rows")
+    _on(q, device, "q")
+    _on(out, device, "out")
+    _on(workspace, device, "workspace")
+    if not workspace.is_contiguous():
+        raise NVFP4Error("workspace must be contiguous")
+    b = _KVBatch(batch, q_len, None, 0, None, 0, 0, None, prefix_len)
+    if lens is not None:
+        _on(lens, device, "lens")
+        if lens.dtype != torch.int32 or tuple(lens.shape) != (batch,) or not lens.is_contiguous():
+            raise NVFP4Error(f"lens must be a contiguous int32 [{batch}] tensor")
+        b.lens = lens.data_ptr()
+    if table is not None:
+        _on(table, device, "table")
+        if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch or table.stride(1) != 1:
+            raise NVFP4Error(f"table must be int32 [{batch}, pages] with contiguous rows")
+        if lens is None:
+            raise NVFP4Error("a table needs lens")
+        b.table, b.table_cols, b.ld_table = table.data_ptr(), table.shape[1], _row_stride(table)
+        b.max_len = table.shape[1] * pages.page_size if max_len is None else max_len
+    elif max_len:
+        raise NVFP4Error("max_len needs a table")
+    if prefix_len:
+        if prefix_pages is None or prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1 \
+                or not prefix_pages.is_contiguous() or prefix_pages.shape[0] * pages.page_size < prefix_len:
+            raise NVFP4Error(f"prefix_pages must be a contiguous 1-D int32 tensor that holds {prefix_len} tokens")
+        _on(prefix_pages, device, "prefix_pages")
+        b.prefix_pages = prefix_pages.data_ptr()
+    with _device_of(device):
+        st = load().nvfp4_kv_pages_attention(
+            ctypes.byref(d), ctypes.byref(b), q.data_ptr(), _row_stride(q), _dtype_code(q), width // pages.head_dim, scale,
+            out.data_ptr(), _row_stride(out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream(device, stream))
+    _check(st, "nvfp4_kv_pages_attention")
+
+
 # ----------------------------------------------------------- conveniences
 
 def quantize(x: torch.Tensor, static_scale: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -562,3 +765,46 @@ def gdn_recurrence(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torc
     sf = torch.empty((v_heads, 128, 128), dtype=torch.float32, device=q.device) if return_state else None
     nvfp4_gdn_recurrence(q, k, v, beta, g, o, k_heads, v_heads, ws, normalize_qk, s0, sf)
     return (o, sf) if return_state else o
+
+
+def kv_pages_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantize k and v into the cache slots (see ``nvfp4_kv_pages_write``)."""
+    nvfp4_kv_pages_write(pages, k, v, slots)
+
+
+def kv_pages_read(pages: KVPages, slots: torch.Tensor, out_dtype=torch.bfloat16):
+    """(keys, values) [len(slots), kv_heads * head_dim] of the cache slots;
+    unspecified for slots outside the cache."""
+    shape = (slots.shape[0], pages.kv_heads * pages.head_dim)
+    k = torch.empty(shape, dtype=out_dtype, device=pages.device)
+    v = torch.empty(shape, dtype=out_dtype, device=pages.device)
+    nvfp4_kv_pages_read(pages, slots, k, v)
+    return k, v
+
+
+def kv_pages_attention_workspace(q: torch.Tensor, pages: KVPages, batch: int, q_len: int = 1, max_len: int = 0,
+                                 prefix_len: int = 0) -> torch.Tensor:
+    """A workspace for ``kv_pages_attention`` calls of this shape."""
+    n = nvfp4_kv_pages_attention_workspace_bytes(pages, batch, q.shape[1] // pages.head_dim, q.dtype, q_len, max_len,
+                                                 prefix_len)
+    if n == 0:
+        raise NVFP4Error("the attention does not take this shape")
+    return torch.empty((n + 3) // 4, dtype=torch.float32, device=q.device)
+
+
+def kv_pages_attention(q: torch.Tensor, pages: KVPages, table: torch.Tensor | None = None,
+                       lens: torch.Tensor | None = None, q_len: int = 1, prefix_pages: torch.Tensor | None = None,
+                       prefix_len: int = 0, scale: float | None = None, max_len: int | None = None,
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [batch * q_len, q_heads * head_dim] over the cache (see
+    ``nvfp4_kv_pages_attention``); scale head_dim^-1/2 unless given.  Without
+    ``out``, rows of places that hold no sequence are unspecified."""
+    batch = q.shape[0] // q_len
+    if max_len is None:
+        max_len = 0 if table is None else table.shape[1] * pages.page_size
+    if workspace is None:
+        workspace = kv_pages_attention_workspace(q, pages, batch, q_len, max_len, prefix_len)
+    o = out if out is not None else torch.empty_like(q, memory_format=torch.contiguous_format)
+    nvfp4_kv_pages_attention(q, pages, o, workspace, pages.head_dim ** -0.5 if scale is None else scale, batch, q_len, table,
+                             lens, max_len, prefix_pages, prefix_len)
+    return o

@@ -498,6 +498,7 @@ const char* nvfp4_status_string(int status) {
     case NVFP4_ERR_FLAGS: return "unknown flags";
     case NVFP4_ERR_HIP: return g_hip_msg[0] ? g_hip_msg : "HIP error";
     case NVFP4_ERR_RANGE: return "size beyond 2^31";
+    case NVFP4_ERR_VALUE: return "a number outside its range";
     default: return "unknown status";
   }
 }

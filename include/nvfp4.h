@@ -67,7 +67,8 @@ typedef enum {
   NVFP4_ERR_WORKSPACE = -8, /* workspace missing or too small */
   NVFP4_ERR_FLAGS = -9,     /* unknown flag bits */
   NVFP4_ERR_HIP = -10,      /* a HIP launch failed */
-  NVFP4_ERR_RANGE = -11     /* a size beyond what the kernels index (2^31) */
+  NVFP4_ERR_RANGE = -11,    /* a size beyond what the kernels index (2^31) */
+  NVFP4_ERR_VALUE = -12     /* a number outside its range */
 } nvfp4_status;
 
 /* Element types of dense (non-NVFP4) operands. */
@@ -413,6 +414,134 @@ int nvfp4_gdn_recurrence(const nvfp4_gdn_inputs* in, int in_dtype, int64_t token
                          int v_heads, int normalize_qk, const float* s0, float* s_final, void* o,
                          int o_dtype, int64_t ld_o, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/*
+ * Paged FP8 KV cache with a scale for each token and head, and the attention
+ * over it.  This is the serving form of the FP8 KV cache above: keys and
+ * values of any tokens are written into pages, every (token, kv head) row
+ * gets its own scale when it is written (no calibration), and
+ * nvfp4_kv_pages_attention reads the pages as they are.
+ *
+ * A page holds page_size tokens of every kv head; cache slot
+ * page * page_size + i is token i of the page.  For the row x of one token
+ * and head, with a = max|x|:
+ *   scale byte  B = e + 127, e the least integer >= -126 with a <= 448 * 2^e;
+ *   codes       the E4M3 byte nearest to the exact x / 2^e, ties to the even
+ *               code, sign = IEEE sign bit (nothing saturates);
+ *   value read  code * 2^e.
+ * A power of two keeps E4M3's relative precision and makes the decoded value
+ * exact in bf16 (for e >= -117, below which the smallest codes are bf16
+ * subnormals).
+ *
+ * Layout, per page p, head h and block b = i / 16 of 16 tokens, o = i % 16,
+ * D = head_dim (all uint8):
+ *   k_codes[p * ld_codes + (h * page_size + 16 b) * D
+ *           + (o / 4) * 4 D + (d / 16) * 64 + (o % 4) * 16 + d % 16]
+ *   v_codes[p * ld_codes + (h * page_size + 16 b) * D + d * 16 + o]
+ *   k_scales, v_scales[p * ld_scales + h * page_size + i]
+ * so that 16 bytes of a key block are 16 dimensions of one token and 16 bytes
+ * of a value block are 16 tokens of one dimension: what one lane feeds to the
+ * matrix instructions.
+ *   head_dim 64, 128 or 256; page_size a power of two, 16 <= page_size <=
+ *   4096; 1 <= kv_heads <= 4096; n_pages * page_size < 2^31.
+ *   ld_codes >= kv_heads * page_size * head_dim, ld_scales >= kv_heads *
+ *   page_size (bytes between pages), both multiples of 16; all four pointers
+ *   16-byte aligned.
+ */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t n_pages;
+  int64_t ld_codes, ld_scales;
+  int kv_heads, head_dim, page_size;
+} nvfp4_kv_pages;
+
+/*
+ * nvfp4_kv_pages_write -- rows of k and v [rows, kv_heads * head_dim] (bf16
+ * or float32, one dtype) into the cache, row i at slots[i] (DEVICE int64
+ * [rows]).  A row whose slot lies outside [0, n_pages * page_size) is not
+ * written.  Two rows of one call must not share a slot (the slot would hold
+ * a mixture of them).  Runs of 16 rows that fill one aligned block of slots
+ * are written whole; others byte by byte.
+ *   ld_k, ld_v  elements, >= kv_heads * head_dim, rows 16-byte aligned.
+ * One launch.  rows = 0 is a valid call that does nothing; rows < 2^28.
+ */
+int nvfp4_kv_pages_write(const nvfp4_kv_pages* cache, const void* k, int64_t ld_k, const void* v,
+                         int64_t ld_v, int x_dtype, int64_t rows, const int64_t* slots, void* stream);
+
+/*
+ * nvfp4_kv_pages_read -- rows of the cache as dense matrices: k_out and v_out
+ * [rows, kv_heads * head_dim] row i = the values at slots[i], as float32
+ * (exact within float32's normal range) or rounded to bf16 (nearest even; exact for
+ * e >= -117).  A row whose slot lies outside the cache is left as it was.
+ * Slots may repeat.  rows as for the write.
+ */
+int nvfp4_kv_pages_read(const nvfp4_kv_pages* cache, int64_t rows, const int64_t* slots, void* k_out,
+                        int64_t ld_k, void* v_out, int64_t ld_v, int out_dtype, void* stream);
+
+/*
+ * A batch of sequences over the pages.  Sequence b holds lens[b] cached
+ * tokens of its own -- the q_len tokens of this call among them, at its end
+ * -- in the pages table[b * ld_table + 0 ..], after prefix_len tokens that
+ * all sequences share, in the pages prefix_pages[0 ..].
+ *   lens          DEVICE int32 [batch], or NULL (all zero).  0 is a sequence
+ *                 without tokens of its own; a negative length marks a place
+ *                 of a padded batch that holds no sequence.  A length above
+ *                 max_len counts as max_len.
+ *   max_len       HOST bound of lens, 0 <= max_len <= table_cols * page_size;
+ *                 the launch is planned for it, so it should be near.
+ *   table         DEVICE int32 [batch, table_cols], row stride ld_table; may
+ *                 be NULL when max_len is 0.
+ *   prefix_pages  DEVICE int32 [ceil(prefix_len / page_size)]; may be NULL
+ *                 when prefix_len is 0.
+ * A page id outside [0, n_pages) is not read: its tokens count as masked.
+ */
+typedef struct {
+  int64_t batch;
+  int64_t q_len;
+  const int32_t* lens;
+  int64_t max_len;
+  const int32_t* table;
+  int64_t table_cols, ld_table;
+  const int32_t* prefix_pages;
+  int64_t prefix_len;
+} nvfp4_kv_batch;
+
+/* Bytes of device workspace that nvfp4_kv_pages_attention needs for a batch
+ * (of its shape only: batch, q_len, max_len and prefix_len are used, not the
+ * pointers), q_heads query heads and this cache's heads; 0 for a shape that
+ * it does not take. */
+size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, const nvfp4_kv_batch* batch,
+                                                int q_heads, int dtype);
+
+/*
+ * nvfp4_kv_pages_attention -- query row b * q_len + j (token j of sequence
+ * b), head h, attends with kv head h / (q_heads / kv_heads) to the prefix and
+ * to the first lens[b] - q_len + 1 + j tokens of its sequence:
+ *   out = sum_t softmax_t(scale * q . k_t) v_t.
+ * A row that sees no token gets zeros.  Rows of a sequence of negative length
+ * are left as they were.
+ *   q, out     DEVICE [batch * q_len, q_heads * head_dim], row strides ld_q,
+ *              ld_out in elements, rows 16-byte aligned; both of `dtype`.
+ *   scale      finite and > 0 (head_dim^-1/2 as a rule).
+ *   workspace  DEVICE, >= nvfp4_kv_pages_attention_workspace_bytes bytes,
+ *              16-byte aligned, contents arbitrary; calls that may overlap in
+ *              time need one each.
+ * The prefix is read once for all sequences, not once for each.  Products of
+ * bf16 queries are exact, sums and the softmax are float32; with NVFP4_DTYPE_
+ * BF16 each softmax weight enters its product with the values rounded to
+ * bf16, with NVFP4_DTYPE_F32 queries and weights enter as three bf16 terms
+ * (24 bits).  The result does not depend on timing: the same call on the same
+ * data gives the same bits.  1 <= q_len, batch * q_len < 2^31 / q_heads,
+ * batch * kv_heads * ceil(q_len * q_heads / kv_heads / 16) < 2^24; q_heads a
+ * multiple of kv_heads.  At most three launches.  batch = 0 is a
+ * valid call that does nothing.
+ */
+int nvfp4_kv_pages_attention(const nvfp4_kv_pages* cache, const nvfp4_kv_batch* batch, const void* q,
+                             int64_t ld_q, int dtype, int q_heads, float scale, void* out, int64_t ld_out,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable text of a status (and of the last HIP error, for NVFP4_ERR_HIP). */
 const char* nvfp4_status_string(int status);
