@@ -491,17 +491,21 @@ class KVPages:
 
     def descriptor(self) -> _KVPages:
         kc, vc, ks, vs = self.k_codes, self.v_codes, self.k_scales, self.v_scales
+        cs, ss, device, u8 = kc.shape, ks.shape, kc.device, torch.uint8
         per = self.kv_heads * self.page_size
-        for t, width, like in ((kc, per * self.head_dim, kc), (vc, per * self.head_dim, kc), (ks, per, ks), (vs, per, ks)):
-            if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != kc.shape[0] or t.shape[1] < width or t.stride(1) != 1:
-                raise NVFP4Error(f"cache tensors must be uint8 [n_pages, >= {width}] with contiguous rows")
-            if t.stride(0) != like.stride(0):
-                raise NVFP4Error("key and value tensors of a cache must share their row stride")
-            if t.device != kc.device or not t.is_cuda:
-                raise NVFP4Error("cache tensors must live on one GPU")
-        return _KVPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), kc.shape[0],
-                        max(kc.stride(0), kc.shape[1]), max(ks.stride(0), ks.shape[1]), self.kv_heads, self.head_dim,
-                        self.page_size)
+        if len(cs) != 2 or len(ss) != 2 or vc.shape != cs or vs.shape != ss or ss[0] != cs[0] or cs[1] < per * self.head_dim \
+                or ss[1] < per or kc.dtype is not u8 or vc.dtype is not u8 or ks.dtype is not u8 or vs.dtype is not u8:
+            raise NVFP4Error(f"cache tensors must be uint8 [n_pages, >= {per * self.head_dim}] (codes) and "
+                             f"[n_pages, >= {per}] (scales)")
+        (ldc, one), (lds, one_s) = kc.stride(), ks.stride()
+        if one != 1 or one_s != 1 or vc.stride() != (ldc, 1) or vs.stride() != (lds, 1):
+            raise NVFP4Error("cache tensors must have contiguous rows, keys and values with one row stride")
+        if device.type != "cuda" or vc.device != device or ks.device != device or vs.device != device:
+            raise NVFP4Error("cache tensors must live on one GPU")
+        if cs[0] == 1:  # a single row may carry any stride
+            ldc, lds = max(ldc, cs[1]), max(lds, ss[1])
+        return _KVPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), cs[0], ldc, lds, self.kv_heads,
+                        self.head_dim, self.page_size)
 
 
 def empty_kv_pages(n_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> KVPages:
@@ -517,69 +521,59 @@ def _on(t: torch.Tensor, device: torch.device, what: str) -> None:
         raise NVFP4Error(f"{what} must live on {device}, got {t.device}")
 
 
-def _kv_rows(t: torch.Tensor, rows: int, pages: KVPages, what: str) -> None:
-    _on(t, pages.device, what)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != pages.kv_heads * pages.head_dim or t.stride(1) != 1:
-        raise NVFP4Error(f"{what} must be [{rows}, {pages.kv_heads * pages.head_dim}] with contiguous rows, got {tuple(t.shape)}")
+def _row_stride(t: torch.Tensor, rows: int, cols: int, device: torch.device, what: str) -> int:
+    """Row stride (elements) of a [rows, cols] matrix with contiguous rows on
+    ``device``; a single row may carry any stride."""
+    if t.shape != (rows, cols):
+        raise NVFP4Error(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise NVFP4Error(f"{what} must have contiguous rows")
+    if t.device != device:
+        raise NVFP4Error(f"{what} must live on {device}, got {t.device}")
+    return ld if rows > 1 else max(ld, cols)
 
 
-def _kv_slots(slots: torch.Tensor, pages: KVPages) -> None:
-    _on(slots, pages.device, "slots")
-    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+def _kv_slots(slots: torch.Tensor, device: torch.device) -> int:
+    if slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
         raise NVFP4Error("slots must be a contiguous 1-D int64 tensor")
+    _on(slots, device, "slots")
+    return slots.shape[0]
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements between rows; a single row may carry any stride."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-class _device_of:
-    """Makes a tensor's GPU the current one for a call on one of its streams."""
-
-    def __init__(self, device: torch.device):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call_on(device: torch.device, stream, f, *args) -> int:
+    """f(*args, stream) with ``device`` as the current GPU, on ``stream`` or
+    the device's current one."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call_on(device, stream, f, *args)
+    return f(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(device, stream))
 
 
 def nvfp4_kv_pages_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """C ``nvfp4_kv_pages_write``: rows of k and v [rows, kv_heads * head_dim]
     to the cache slots ``slots`` (int64 device tensor, distinct; a row whose
     slot is outside the cache is dropped)."""
-    d = pages.descriptor()
-    _kv_slots(slots, pages)
-    _kv_rows(k, slots.shape[0], pages, "k")
-    _kv_rows(v, slots.shape[0], pages, "v")
+    d, device, width = pages.descriptor(), pages.k_codes.device, pages.kv_heads * pages.head_dim
+    rows = _kv_slots(slots, device)
+    ld_k, ld_v = _row_stride(k, rows, width, device, "k"), _row_stride(v, rows, width, device, "v")
     if k.dtype != v.dtype:
         raise NVFP4Error("k and v must share one dtype")
-    with _device_of(pages.device):
-        st = load().nvfp4_kv_pages_write(ctypes.byref(d), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
-                                         _dtype_code(k), slots.shape[0], slots.data_ptr(), _stream(pages.device, stream))
-    _check(st, "nvfp4_kv_pages_write")
+    _check(_call_on(device, stream, load().nvfp4_kv_pages_write, ctypes.byref(d), k.data_ptr(), ld_k, v.data_ptr(), ld_v,
+                    _dtype_code(k), rows, slots.data_ptr()), "nvfp4_kv_pages_write")
 
 
 def nvfp4_kv_pages_read(pages: KVPages, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
                         stream=None) -> None:
     """C ``nvfp4_kv_pages_read``: the cached rows at ``slots`` as dense keys
     and values (rows whose slot is outside the cache stay as they were)."""
-    d = pages.descriptor()
-    _kv_slots(slots, pages)
-    _kv_rows(k_out, slots.shape[0], pages, "k_out")
-    _kv_rows(v_out, slots.shape[0], pages, "v_out")
+    d, device, width = pages.descriptor(), pages.k_codes.device, pages.kv_heads * pages.head_dim
+    rows = _kv_slots(slots, device)
+    ld_k, ld_v = _row_stride(k_out, rows, width, device, "k_out"), _row_stride(v_out, rows, width, device, "v_out")
     if k_out.dtype != v_out.dtype:
         raise NVFP4Error("k_out and v_out must share one dtype")
-    with _device_of(pages.device):
-        st = load().nvfp4_kv_pages_read(ctypes.byref(d), slots.shape[0], slots.data_ptr(), k_out.data_ptr(),
-                                        _row_stride(k_out), v_out.data_ptr(), _row_stride(v_out), _dtype_code(k_out),
-                                        _stream(pages.device, stream))
-    _check(st, "nvfp4_kv_pages_read")
+    _check(_call_on(device, stream, load().nvfp4_kv_pages_read, ctypes.byref(d), rows, slots.data_ptr(), k_out.data_ptr(),
+                    ld_k, v_out.data_ptr(), ld_v, _dtype_code(k_out)), "nvfp4_kv_pages_read")
 
 
 def nvfp4_kv_pages_attention_workspace_bytes(pages: KVPages, batch: int, q_heads: int, dtype: torch.dtype,
@@ -602,46 +596,45 @@ def nvfp4_kv_pages_attention(q: torch.Tensor, pages: KVPages, out: torch.Tensor,
     head_dim]; table int32 [batch, cols], lens int32 [batch] (device);
     max_len a host bound of lens (default: what the table can hold);
     prefix_pages int32 (device) with the prefix_len shared tokens."""
-    d = pages.descriptor()
-    device = pages.device
-    width = q.shape[1] if q.dim() == 2 else 0
-    if width == 0 or width % pages.head_dim != 0 or q.shape[0] != batch * q_len or q.stride(1) != 1:
-        raise NVFP4Error(f"q must be [{batch * q_len}, q_heads * {pages.head_dim}] with contiguous rows")
-    if out.shape != q.shape or out.stride(1) != 1 or out.dtype != q.dtype:
-        raise NVFP4Error("out must have q's shape and dtype and contiguous rows")
-    _on(q, device, "q")
-    _on(out, device, "out")
-    _on(workspace, device, "workspace")
+    d, device, i32 = pages.descriptor(), pages.k_codes.device, torch.int32
+    if q.dim() != 2 or q.shape[1] == 0 or q.shape[1] % pages.head_dim != 0:
+        raise NVFP4Error(f"q must be [{batch * q_len}, q_heads * {pages.head_dim}], got {list(q.shape)}")
+    width = q.shape[1]
+    ld_q, ld_o = _row_stride(q, batch * q_len, width, device, "q"), _row_stride(out, batch * q_len, width, device, "out")
+    if out.dtype != q.dtype:
+        raise NVFP4Error("out must have q's dtype")
     if not workspace.is_contiguous():
         raise NVFP4Error("workspace must be contiguous")
-    b = _KVBatch(batch, q_len, None, 0, None, 0, 0, None, prefix_len)
+    _on(workspace, device, "workspace")
+    lens_p = table_p = prefix_p = None
+    cols = ld_table = 0
     if lens is not None:
-        _on(lens, device, "lens")
-        if lens.dtype != torch.int32 or tuple(lens.shape) != (batch,) or not lens.is_contiguous():
+        if lens.dtype is not i32 or lens.shape != (batch,) or not lens.is_contiguous():
             raise NVFP4Error(f"lens must be a contiguous int32 [{batch}] tensor")
-        b.lens = lens.data_ptr()
+        _on(lens, device, "lens")
+        lens_p = lens.data_ptr()
     if table is not None:
-        _on(table, device, "table")
-        if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch or table.stride(1) != 1:
-            raise NVFP4Error(f"table must be int32 [{batch}, pages] with contiguous rows")
         if lens is None:
             raise NVFP4Error("a table needs lens")
-        b.table, b.table_cols, b.ld_table = table.data_ptr(), table.shape[1], _row_stride(table)
-        b.max_len = table.shape[1] * pages.page_size if max_len is None else max_len
+        if table.dtype is not i32 or table.dim() != 2:
+            raise NVFP4Error(f"table must be int32 [{batch}, pages]")
+        cols = table.shape[1]
+        ld_table = _row_stride(table, batch, cols, device, "table")
+        table_p = table.data_ptr()
+        if max_len is None:
+            max_len = cols * pages.page_size
     elif max_len:
         raise NVFP4Error("max_len needs a table")
     if prefix_len:
-        if prefix_pages is None or prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1 \
+        if prefix_pages is None or prefix_pages.dtype is not i32 or prefix_pages.dim() != 1 \
                 or not prefix_pages.is_contiguous() or prefix_pages.shape[0] * pages.page_size < prefix_len:
             raise NVFP4Error(f"prefix_pages must be a contiguous 1-D int32 tensor that holds {prefix_len} tokens")
         _on(prefix_pages, device, "prefix_pages")
-        b.prefix_pages = prefix_pages.data_ptr()
-    with _device_of(device):
-        st = load().nvfp4_kv_pages_attention(
-            ctypes.byref(d), ctypes.byref(b), q.data_ptr(), _row_stride(q), _dtype_code(q), width // pages.head_dim, scale,
-            out.data_ptr(), _row_stride(out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream(device, stream))
-    _check(st, "nvfp4_kv_pages_attention")
+        prefix_p = prefix_pages.data_ptr()
+    b = _KVBatch(batch, q_len, lens_p, max_len or 0, table_p, cols, ld_table, prefix_p, prefix_len)
+    _check(_call_on(device, stream, load().nvfp4_kv_pages_attention, ctypes.byref(d), ctypes.byref(b), q.data_ptr(), ld_q,
+                    _dtype_code(q), width // pages.head_dim, scale, out.data_ptr(), ld_o, workspace.data_ptr(),
+                    workspace.nbytes), "nvfp4_kv_pages_attention")
 
 
 # ----------------------------------------------------------- conveniences
@@ -775,9 +768,7 @@ def kv_pages_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, slots: torc
 def kv_pages_read(pages: KVPages, slots: torch.Tensor, out_dtype=torch.bfloat16):
     """(keys, values) [len(slots), kv_heads * head_dim] of the cache slots;
     unspecified for slots outside the cache."""
-    shape = (slots.shape[0], pages.kv_heads * pages.head_dim)
-    k = torch.empty(shape, dtype=out_dtype, device=pages.device)
-    v = torch.empty(shape, dtype=out_dtype, device=pages.device)
+    k, v = torch.empty((2, slots.shape[0], pages.kv_heads * pages.head_dim), dtype=out_dtype, device=pages.device).unbind()
     nvfp4_kv_pages_read(pages, slots, k, v)
     return k, v
 
@@ -804,7 +795,7 @@ def kv_pages_attention(q: torch.Tensor, pages: KVPages, table: torch.Tensor | No
         max_len = 0 if table is None else table.shape[1] * pages.page_size
     if workspace is None:
         workspace = kv_pages_attention_workspace(q, pages, batch, q_len, max_len, prefix_len)
-    o = out if out is not None else torch.empty_like(q, memory_format=torch.contiguous_format)
+    o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
     nvfp4_kv_pages_attention(q, pages, o, workspace, pages.head_dim ** -0.5 if scale is None else scale, batch, q_len, table,
                              lens, max_len, prefix_pages, prefix_len)
     return o

@@ -48,7 +48,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kWaves = 4;
-constexpr int kStep = 64;       // tokens of one wave's step
+constexpr int kStep = 64;       // tokens of one wave's step (16-row tiles)
 constexpr int kTileRows = 16;
 constexpr float kLowest = -3.0e38f;  // stands for "no token yet"; finite, so differences are never NaN
 
@@ -57,14 +57,18 @@ struct Pass {
   int batch;      // sequences (1 where the rows of all share their tokens)
   int rows;       // query rows of a sequence and kv head: q_len * group
   int q_len, group;
-  int row_tiles;  // ceil(rows / kTileRows)
+  int tile_rows;  // query rows of a tile
+  int step;       // tokens of a wave's step
+  int step_waves; // waves of a workgroup that take different steps
+  int row_tiles;  // ceil(rows / tile_rows)
   int prefix_len; // shared tokens this pass reads for every tile
   const int* lens;  // null: no tokens of the sequences' own
   int max_len;
   int workgroups;
   int direct;     // every tile is whole in one workgroup and nothing joins it: write the output
-  float* ml;      // partials: [slot][16][2], then [slot][16][D]
+  float* ml;      // partials: [slot][tile_rows][2] and [slot][tile_rows][D]
   float* o;
+  int2* head;     // [tile]: the workgroup with its first unit, and the number of its pieces
 };
 
 __device__ __host__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -73,8 +77,8 @@ __device__ inline int own_len(const Pass& p, int b) {
   return p.lens == nullptr ? 0 : max(min(p.lens[b], p.max_len), -1);
 }
 __device__ inline int tile_units(const Pass& p, int len) {
-  const int steps = ceil_div(p.prefix_len, kStep) + ceil_div(max(len, 0), kStep);
-  return max(1, ceil_div(steps, kWaves));  // a tile without tokens is one empty unit
+  const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(max(len, 0), p.step);
+  return max(1, ceil_div(steps, p.step_waves));  // a tile without tokens is one empty unit
 }
 
 // Units of the sequences before `b` (sum over one tile each), and where a
@@ -168,6 +172,16 @@ __device__ inline bf16x8 take_term(float f[8]) {
   return r;
 }
 
+// The bytes of a dword that hold one of the first n tokens.
+__device__ inline uint32_t keep_bytes(int n) {
+  const int c = min(max(n, 0), 4);
+  return c == 4 ? 0xFFFFFFFFu : (1u << (8 * c)) - 1u;
+}
+
+__device__ inline void put_head(const Pass& p, int tile, int wg, int pieces) {
+  if (p.head != nullptr && threadIdx.x == 0) p.head[tile] = make_int2(wg, pieces);
+}
+
 // 1 / l, 0 for a row without tokens.
 __device__ inline float inverse_sum(float l) { return l > 0.0f ? 1.0f / l : 0.0f; }
 
@@ -183,17 +197,29 @@ __device__ inline void store_out4(const KvAttnArgs& a, int token, int head, int 
 }
 
 // T = bf16 terms of a query element and of a softmax weight: 1 for bf16
-// queries (exact; the weights are rounded to 8 bits, relative 2^-9 each), 3
-// for float32 (24 bits).
+// queries (exact; the weights are rounded to 8 bits, at most 2^-8 of each),
+// 3 for float32 (24 bits).
+template <int DT>
+constexpr int kTerms = DT == NVFP4_DTYPE_BF16 ? 1 : 3;
+
+// LDS of a stream workgroup.  The queries' fragments lie there because all
+// four waves use the same ones and their registers are wanted for bytes in
+// flight (D = 256: 32 of 256).
 template <int DT, int D>
-__global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pass p) {
-  constexpr int T = DT == NVFP4_DTYPE_BF16 ? 1 : 3;
+struct StreamLds {
+  float *part_a, *part_b;  // a wave's accumulators each: 16 * D
+  uint4* q;                // [kTerms][D / 32][64]
+  float (*ml)[32][2];
+  int64_t* line;
+};
+
+// PAIR: two workgroups share a CU, i.e. 256 registers a wave.
+template <int DT, int D, bool PAIR>
+__device__ __attribute__((always_inline)) inline void stream_body(const KvAttnArgs& a, const Pass& p, const int wg,
+                                                                  const StreamLds<DT, D>& lds) {
+  constexpr int T = kTerms<DT>;
   constexpr int KJ = D / 64;   // 16-byte pieces of a token that a lane holds
   constexpr int DT16 = D / 16; // output tiles of 16 dimensions
-  constexpr int kPad = D + 4;
-  __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kTileRows][kPad];
-  __shared__ float lds_ml[kWaves][kTileRows][2];
-  __shared__ int64_t lds_line[kWaves + 2];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -201,8 +227,8 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
   const int prefix_steps = ceil_div(p.prefix_len, kStep);
   const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
 
-  Line line(p, tiles_per_seq, lds_line);
-  int64_t unit = (int64_t)blockIdx.x * line.share;
+  Line line(p, tiles_per_seq, lds.line);
+  int64_t unit = (int64_t)wg * line.share;
   const int64_t last_unit = min(unit + line.share, line.total * tiles_per_seq);
   if (unit >= last_unit) return;
   int seq;
@@ -218,6 +244,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
     const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * kTileRows;
     const int steps = prefix_steps + ceil_div(max(len, 0), kStep);
     const int tile = seq * tiles_per_seq + x;
+    if (u0 == 0) put_head(p, tile, wg, (int)((unit + units - 1) / line.share - wg) + 1);
 
     // This lane's query row and the first own token that it does not see.
     const int row = min(row0 + i, p.rows - 1);
@@ -227,21 +254,17 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
     const int tile_last = min(row0 + kTileRows, p.rows) - 1;
     const int limit_first = len - p.q_len + 1 + row0 / p.group, limit_last = len - p.q_len + 1 + tile_last / p.group;
 
-    bf16x8 qf[T][2 * KJ];
-    {
-      const int head = kvh * p.group + row - row_token * p.group;
+    const int head = kvh * p.group + row - row_token * p.group;
+    for (int j = wave; j < 2 * KJ; j += kWaves) {
+      const int64_t at = token * a.ld_q + (int64_t)head * D + (4 * (j >> 1) + g) * 16 + 8 * (j & 1);
+      if constexpr (T == 1) {
+        lds.q[j * 64 + lane] = *reinterpret_cast<const uint4*>((const uint16_t*)a.q + at);
+      } else {
+        const float* s = (const float*)a.q + at;
+        const float4 lo = *reinterpret_cast<const float4*>(s), hi = *reinterpret_cast<const float4*>(s + 4);
+        float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-      for (int j = 0; j < 2 * KJ; ++j) {
-        const int64_t at = token * a.ld_q + (int64_t)head * D + (4 * (j >> 1) + g) * 16 + 8 * (j & 1);
-        if constexpr (T == 1) {
-          qf[0][j] = *reinterpret_cast<const bf16x8*>((const uint16_t*)a.q + at);
-        } else {
-          const float* s = (const float*)a.q + at;
-          const float4 lo = *reinterpret_cast<const float4*>(s), hi = *reinterpret_cast<const float4*>(s + 4);
-          float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int t = 0; t < T; ++t) qf[t][j] = take_term(f);
-        }
+        for (int t = 0; t < T; ++t) lds.q[(t * 2 * KJ + j) * 64 + lane] = __builtin_bit_cast(uint4, take_term(f));
       }
     }
 
@@ -250,18 +273,15 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
 #pragma unroll
     for (int d = 0; d < DT16; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // Where a step's tokens are: `list` of pages, first token `base`, tokens
-    // of the list `n` (those that any row of the tile sees).
-    auto step_list = [&](int s, const int*& list, int& base, int& n) {
-      if (s < prefix_steps) {
-        list = a.prefix_pages;
-        base = s * kStep;
-        n = p.prefix_len;
-      } else {
-        list = a.table + seq * a.ld_table;
-        base = (s - prefix_steps) * kStep;
-        n = limit_last;
-      }
+    // Where a step's tokens are: a list of pages, the first token `base`, and
+    // the tokens of the list that any row of the tile sees.
+    struct Where {
+      const int* list;
+      int base, n;
+    };
+    auto where = [&](int s) __attribute__((always_inline)) {
+      if (s < prefix_steps) return Where{a.prefix_pages, s * kStep, p.prefix_len};
+      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * kStep, limit_last};
     };
     // A wave's next step from s on that holds a visible token, or -1.
     auto next_step = [&](int s) {
@@ -270,32 +290,34 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
       if (s >= prefix_steps && (s - prefix_steps) * kStep >= limit_last) return -1;  // later ones neither
       return s;
     };
-    // Page ids of the lane's key block (i / 4) and value block (g); blocks
-    // past the last token take the last one's page and are masked below.
-    auto page_ids = [&](int s, int& pk, int& pv) {
-      const int* list;
-      int base, n;
-      step_list(s, list, base, n);
-      const int last = (n - 1) >> 4;
-      pk = list[min((base >> 4) + (i >> 2), last) >> page_blocks_shift];
-      pv = list[min((base >> 4) + g, last) >> page_blocks_shift];
+    // Blocks past the last token take the last one's page and are masked below.
+    auto block_of = [&](const Where& w, int b) { return min((w.base >> 4) + b, (w.n - 1) >> 4); };
+    auto slot_of = [&](int blk) { return (kvh << a.c.page_shift) + (blk & page_blocks_mask) * 16; };
+    auto row_of = [&](int id, int64_t ld) {
+      return (uint64_t)((unsigned)id < (unsigned)a.c.n_pages ? (unsigned)id : 0u) * (uint64_t)(uint32_t)ld;
     };
-    // Byte offset of token block `blk` (of its page) in codes; scales are at / D.
-    auto block_at = [&](int blk) { return (kvh << a.c.page_shift) + (blk & page_blocks_mask) * 16; };
+    // Page ids of the lane's key block (i / 4) and value block (g).
+    auto page_ids = [&](int s, int& pk, int& pv) __attribute__((always_inline)) {
+      const Where w = where(s);
+      pk = w.list[block_of(w, i >> 2) >> page_blocks_shift];
+      pv = w.list[block_of(w, g) >> page_blocks_shift];
+    };
 
+    // With D = 256 a step's keys and values together do not fit the registers
+    // of two waves per SIMD beside the accumulators: half of the values are
+    // asked for when the keys are used up, and the next keys when the first
+    // half of the values is.
+    constexpr bool kLate = D == 256 && PAIR;
+    constexpr int kFirst = kLate ? DT16 / 2 : DT16;
     uint4 kq[4][KJ], ksc;
-    auto load_keys = [&](int s, int pk) {
-      const int* list;
-      int base, n;
-      step_list(s, list, base, n);
-      const int page = (unsigned)pk < (unsigned)a.c.n_pages ? pk : 0;
-      const int at = block_at(min((base >> 4) + (i >> 2), (n - 1) >> 4));
-      const uint8_t* src = a.c.kc + page * a.c.ld_codes + (int64_t)at * D + g * 64 + (i & 3) * 16;
+    auto load_keys = [&](int s, int pk) __attribute__((always_inline)) {
+      const int at = slot_of(block_of(where(s), i >> 2));
+      const uint8_t* src = a.c.kc + row_of(pk, a.c.ld_codes) + (uint32_t)(at * D + g * 64 + (i & 3) * 16);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int j = 0; j < KJ; ++j) kq[t][j] = *reinterpret_cast<const uint4*>(src + t * (4 * D) + j * 256);
-      ksc = *reinterpret_cast<const uint4*>(a.c.ks + page * a.c.ld_scales + at);
+      ksc = *reinterpret_cast<const uint4*>(a.c.ks + row_of(pk, a.c.ld_scales) + (uint32_t)at);
     };
 
     int s = next_step(u0 * kWaves + wave);
@@ -304,10 +326,9 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
       page_ids(s, pk, pv);
       load_keys(s, pk);
     }
+    __syncthreads();  // the queries are in LDS
     while (s >= 0) {
-      const int* list;
-      int base, n;
-      step_list(s, list, base, n);
+      const Where w = where(s);
       const bool prefix = s < prefix_steps;
       const bool bad = (unsigned)pv >= (unsigned)a.c.n_pages;
       const int sn = next_step(s + kWaves);
@@ -316,62 +337,65 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
 
       // values of this step
       uint4 vq[DT16], vsc;
+      const uint8_t* vsrc;
       {
-        const int page = bad ? 0 : pv;
-        const int at = block_at(min((base >> 4) + g, (n - 1) >> 4));
-        const uint8_t* src = a.c.vc + page * a.c.ld_codes + (int64_t)at * D + i * 16;
+        const int at = slot_of(block_of(w, g));
+        vsrc = a.c.vc + row_of(pv, a.c.ld_codes) + (uint32_t)(at * D + i * 16);
 #pragma unroll
-        for (int d = 0; d < DT16; ++d) vq[d] = *reinterpret_cast<const uint4*>(src + d * 256);
-        vsc = *reinterpret_cast<const uint4*>(a.c.vs + page * a.c.ld_scales + at);
+        for (int d = 0; d < kFirst; ++d) vq[d] = *reinterpret_cast<const uint4*>(vsrc + d * 256);
+        vsc = *reinterpret_cast<const uint4*>(a.c.vs + row_of(pv, a.c.ld_scales) + (uint32_t)at);
       }
 
       // scores: sc[t][r] is token 4 t + r of block g
       f32x4 sc[4];
-      const uint32_t kw[4] = {ksc.x, ksc.y, ksc.z, ksc.w};
+      float ks[4];
+      {
+        const uint32_t kw[4] = {ksc.x, ksc.y, ksc.z, ksc.w};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float ks = byte_scale(kw[t], i & 3);
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < 4; ++t) {
+          ks[t] = byte_scale(kw[t], i & 3);
+          sc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      }
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-          const bf16x8 k0 = decode8(kq[t][j].x, kq[t][j].y, ks), k1 = decode8(kq[t][j].z, kq[t][j].w, ks);
+      for (int j = 0; j < KJ; ++j)
 #pragma unroll
-          for (int e = T - 1; e >= 0; --e) {
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[e][2 * j], acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[e][2 * j + 1], acc, 0, 0, 0);
+        for (int e = T - 1; e >= 0; --e) {
+          const bf16x8 q0 = __builtin_bit_cast(bf16x8, lds.q[(e * 2 * KJ + 2 * j) * 64 + lane]);
+          const bf16x8 q1 = __builtin_bit_cast(bf16x8, lds.q[(e * 2 * KJ + 2 * j + 1) * 64 + lane]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(kq[t][j].x, kq[t][j].y, ks[t]), q0, sc[t], 0, 0, 0);
+            sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(kq[t][j].z, kq[t][j].w, ks[t]), q1, sc[t], 0, 0, 0);
           }
         }
-        sc[t] = acc;
+      if constexpr (kLate) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = kFirst; d < DT16; ++d) vq[d] = *reinterpret_cast<const uint4*>(vsrc + d * 256);
+      } else if (sn >= 0) {
+        load_keys(sn, pkn);
       }
-      if (sn >= 0) load_keys(sn, pkn);
-
-      const uint32_t vw[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
-      float vs[4][4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) vs[t][r] = byte_scale(vw[t], r);
 
       // Tokens that this row does not see, and bytes of the cache that hold
-      // no token that any row sees (they may be NaN codes: 0 * NaN).
-      const bool masked = prefix ? base + kStep > n : base + kStep > limit_first;
+      // no token that any row sees (they may be NaN codes and infinite
+      // scales: 0 * NaN).
+      const bool masked = prefix ? w.base + kStep > w.n : w.base + kStep > limit_first;
       if (masked || __any(bad)) {
-        const int first = base + 16 * g;
-        const int sees = bad ? 0 : (prefix ? n : limit) - first;  // of this row in block g
-        const int holds = bad ? 0 : n - first;                   // of any row
+        const int first = w.base + 16 * g;
+        const int sees = bad ? 0 : (prefix ? w.n : limit) - first;  // of this row in block g
+        const int holds = bad ? 0 : w.n - first;                    // of any row
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sc[t][r] = 4 * t + r < sees ? sc[t][r] : -__builtin_inff();
-            vs[t][r] = 4 * t + r < sees ? vs[t][r] : 0.0f;
-          }
+          for (int r = 0; r < 4; ++r) sc[t][r] = 4 * t + r < sees ? sc[t][r] : -__builtin_inff();
         uint32_t keep[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int c = min(max(holds - 4 * t, 0), 4);
-          keep[t] = c == 4 ? 0xFFFFFFFFu : (1u << (8 * c)) - 1u;
-        }
+        for (int t = 0; t < 4; ++t) keep[t] = keep_bytes(holds - 4 * t);
+        vsc.x &= keep[0];
+        vsc.y &= keep[1];
+        vsc.z &= keep[2];
+        vsc.w &= keep[3];
 #pragma unroll
         for (int d = 0; d < DT16; ++d) {
           vq[d].x &= keep[0];
@@ -394,23 +418,28 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
         for (int d = 0; d < DT16; ++d) o[d] *= f;
         m = mn;
       }
-      float w[16];
+      float wt[16];
+      const uint32_t vw[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][r], a.scale_log2, -m));
           l += e;
-          w[4 * t + r] = e * vs[t][r];
+          wt[4 * t + r] = e * byte_scale(vw[t], r);
         }
       bf16x8 pf[T][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int t = 0; t < T; ++t) pf[t][h] = take_term(w + 8 * h);
+        for (int t = 0; t < T; ++t) pf[t][h] = take_term(wt + 8 * h);
 
 #pragma unroll
       for (int d = 0; d < DT16; ++d) {
+        if (kLate && d == kFirst) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (sn >= 0) load_keys(sn, pkn);
+        }
         const bf16x8 v0 = decode8(vq[d].x, vq[d].y, 1.0f), v1 = decode8(vq[d].z, vq[d].w, 1.0f);
 #pragma unroll
         for (int e = T - 1; e >= 0; --e) {
@@ -422,45 +451,455 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
       pv = pvn;
     }
 
-    // Join the four waves.
+    // Join the four waves, register by register: 2 and 3 hand theirs to 0 and
+    // 1, then 1 to 0.
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    if (g == 0) {
-      lds_ml[wave][i][0] = m;
-      lds_ml[wave][i][1] = l;
-    }
-#pragma unroll
-    for (int d = 0; d < DT16; ++d) *reinterpret_cast<f32x4*>(&lds_o[wave][i][16 * d + 4 * g]) = o[d];
-    __syncthreads();
-    const bool whole = p.direct && u0 == 0 && u1 == units;
-    const int64_t slot = (int64_t)tile + blockIdx.x;
-    for (int e = threadIdx.x; e < kTileRows * (D / 4); e += kThreads) {
-      const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-      if (row0 + r >= p.rows) break;
-      float top = lds_ml[0][r][0];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds_ml[w][r][0]);
-      float sum = 0.0f;
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(lds_ml[w][r][0] - top);
-        sum += lds_ml[w][r][1] * f;
-        acc += *reinterpret_cast<const f32x4*>(&lds_o[w][r][d]) * f;
+    auto give = [&](float* to) __attribute__((always_inline)) {
+      if (g == 0) {
+        lds.ml[wave][i][0] = m;
+        lds.ml[wave][i][1] = l;
       }
-      if (whole) {
-        if (len >= 0) {
-          const float inv = inverse_sum(sum);
-          const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
-          const int rt = (row0 + r) / p.group;
-          store_out4<DT>(a, seq * p.q_len + rt, kvh * p.group + row0 + r - rt * p.group, d, v);
+#pragma unroll
+      for (int d = 0; d < DT16; ++d) *reinterpret_cast<f32x4*>(to + (d * 64 + lane) * 4) = o[d];
+    };
+    auto take = [&](const float* from, int other) __attribute__((always_inline)) {
+      const float mo = lds.ml[other][i][0], mn = fmaxf(m, mo);
+      const float f = __builtin_amdgcn_exp2f(m - mn), fo = __builtin_amdgcn_exp2f(mo - mn);
+      l = l * f + lds.ml[other][i][1] * fo;
+#pragma unroll
+      for (int d = 0; d < DT16; ++d) o[d] = o[d] * f + *reinterpret_cast<const f32x4*>(from + (d * 64 + lane) * 4) * fo;
+      m = mn;
+    };
+    if (wave >= 2) give(wave == 2 ? lds.part_a : lds.part_b);
+    __syncthreads();
+    if (wave < 2) take(wave == 0 ? lds.part_a : lds.part_b, wave + 2);
+    if (wave == 1) give(lds.part_b);
+    __syncthreads();
+    if (wave == 0) {
+      take(lds.part_b, 1);
+      if (row0 + i < p.rows) {
+        if (!(p.direct && u0 == 0 && u1 == units)) {
+          const int64_t at = ((int64_t)tile + wg) * kTileRows + i;
+          if (g == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
+#pragma unroll
+          for (int d = 0; d < DT16; ++d) *reinterpret_cast<f32x4*>(p.o + at * D + 16 * d + 4 * g) = o[d];
+        } else if (len >= 0) {
+          const float inv = inverse_sum(l);
+#pragma unroll
+          for (int d = 0; d < DT16; ++d) {
+            const float v[4] = {o[d][0] * inv, o[d][1] * inv, o[d][2] * inv, o[d][3] * inv};
+            store_out4<DT>(a, (int)token, head, 16 * d + 4 * g, v);
+          }
         }
-      } else {
-        *reinterpret_cast<f32x4*>(p.o + (slot * kTileRows + r) * D + d) = acc;
-        if (d == 0) *reinterpret_cast<float2*>(p.ml + (slot * kTileRows + r) * 2) = make_float2(top, sum);
       }
     }
-    __syncthreads();
+
+    unit += u1 - u0;
+    if (unit >= last_unit) break;
+    __syncthreads();  // the queries and the hand-over are read
+    u0 = 0;
+    if (++x == tiles_per_seq) {
+      x = 0;
+      ++seq;
+      len = own_len(p, seq);
+      units = tile_units(p, len);
+    }
+  }
+}
+
+// Two workgroups of a pass on a CU, except where one keeps more bytes in
+// flight than two would.
+template <int DT, int D>
+constexpr bool kPaired = DT == NVFP4_DTYPE_BF16 && D < 256;
+
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, (kPaired<DT, D>) ? 2 : 1) void kv_attention_kernel(KvAttnArgs a, Pass p) {
+  __shared__ __attribute__((aligned(16))) float part_a[16 * D], part_b[16 * D];
+  __shared__ uint4 q[kTerms<DT> * (D / 32) * 64];
+  __shared__ float ml[kWaves][32][2];
+  __shared__ int64_t line[kWaves + 2];
+  stream_body<DT, D, kPaired<DT, D>>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line});
+}
+
+// The same for many rows (bf16): tiles of 32 * WM rows on 32 x 32 x 16 MFMA.
+// A wave owns 32 rows; WM waves work on the same tokens (a region of the
+// step's LDS stage), 4 / WM regions hold different tokens.  Reading the bytes
+// of 64 tokens (D = 128) from L2 for each wave on its own would ask for the
+// whole 64 bytes a cycle of a CU's path to L2, so they come once per region
+// by LDS DMA, two stages deep, laid out as the lanes read them: piece
+// (tile of 32 tokens, 32 dimensions) is 1 KB, lane l's 16 bytes at 16 l.
+//   key piece: row i = l % 32 is token 16 h + 4 (i / 8) + i % 4 with
+//   h = i / 4 % 2, dimensions 16 (2 j + l / 32) ..; so register r of the
+//   scores is token r of block l / 32, again the second product's B operand.
+//   value piece: dimension l % 32, the 16 tokens of block l / 32.
+template <int D, int WM>
+struct RowsShape {
+  static constexpr int kWM = WM, kWT = kWaves / WM;
+  static constexpr int kStepTokens = D == 256 ? 32 : 64;
+  static constexpr int kTT = kStepTokens / 32;                 // 32-token tiles of a step
+  static constexpr int kD32 = D / 32;
+  static constexpr int kHalf = kStepTokens * D;                // key (or value) bytes of a region
+  static constexpr int kPieces = kHalf / 1024 / WM;            // key (or value) pieces that a wave copies,
+  static constexpr int kTiles = kPieces > kD32 ? kPieces / kD32 : 1;  // ... of so many 32-token tiles
+  static constexpr int kStageBytes = kWT * 2 * kHalf;
+  static constexpr int kRows = 32 * WM;
+  // Query fragments that a wave keeps in LDS and not in registers (D = 256:
+  // accumulators 128 and queries 64 of 256 leave too few).
+  static constexpr int kQueriesLds = D == 256 ? (WM == 4 ? 6 : WM == 2 ? 2 : 0) : 0;
+};
+
+typedef const __attribute__((address_space(1))) uint32_t* global_u32_ptr;
+
+__device__ __attribute__((always_inline)) inline void copy_to_lds16(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((global_u32_ptr)from, (lds_u32_ptr)to, 16, 0, 0);
+}
+
+// Two stage arrays and not one of two stages: the compiler then knows that
+// reading one does not wait for copies into the other.
+struct RowsLds {
+  uint8_t *stage_a, *stage_b;
+  float (*scales)[2][kStep];  // of a wave's tokens: keys', values'
+  float (*ml)[32][2];
+  int64_t* line;
+  uint4* q;  // [kWaves][kQueriesLds][64]
+};
+
+template <int D, int WM>
+__device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs& a, const Pass& p, const int wg, const RowsLds& lds) {
+  typedef RowsShape<D, WM> C;
+  constexpr int TT = C::kTT, D32 = C::kD32, PW = C::kPieces, NT = C::kTiles;
+  uint8_t* const stage_a = lds.stage_a;
+  uint8_t* const stage_b = lds.stage_b;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wt = wave / WM;
+  const int i = lane & 31, h = lane >> 5;
+  const int tiles_per_seq = a.c.heads * p.row_tiles;
+  const int prefix_steps = ceil_div(p.prefix_len, C::kStepTokens);
+  const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
+
+  // What this lane copies of a key piece, a value piece and the scales.
+  const int kh = (lane >> 2) & 1;
+  const int key_src = ((lane & 31) >> 3) * (4 * D) + h * 64 + (lane & 3) * 16;
+  const int value_src = i * 16;
+  const int scale_token = lane & (C::kStepTokens - 1);
+  const int key_token = 16 * kh + 4 * (i >> 3) + (i & 3);
+
+  Line line(p, tiles_per_seq, lds.line);
+  int64_t unit = (int64_t)wg * line.share;
+  const int64_t last_unit = min(unit + line.share, line.total * tiles_per_seq);
+  if (unit >= last_unit) return;
+  int seq;
+  int64_t seq_before;
+  line.find(p, unit / tiles_per_seq, &seq, &seq_before);
+
+  int len = own_len(p, seq), units = tile_units(p, len);
+  int x = (int)((unit - seq_before * tiles_per_seq) / units);
+  int u0 = (int)(unit - seq_before * tiles_per_seq - (int64_t)x * units);
+
+  while (true) {
+    const int u1 = (int)min((int64_t)units, u0 + (last_unit - unit));
+    const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * C::kRows;
+    const int tile = seq * tiles_per_seq + x;
+    if (u0 == 0) put_head(p, tile, wg, (int)((unit + units - 1) / line.share - wg) + 1);
+    const int row = min(row0 + 32 * wm + i, p.rows - 1);
+    const int row_token = row / p.group;
+    const int64_t token = (int64_t)seq * p.q_len + row_token;
+    const int limit = len - p.q_len + 1 + row_token;  // first own token that this row does not see
+    const int limit_first = len - p.q_len + 1 + min(row0 + 32 * wm, p.rows - 1) / p.group;
+    const int limit_last = len - p.q_len + 1 + (min(row0 + C::kRows, p.rows) - 1) / p.group;
+    const int steps = prefix_steps + ceil_div(max(limit_last, 0), C::kStepTokens);  // with a visible token
+    const int u_end = min(u1, ceil_div(steps, C::kWT));
+
+    constexpr int QL = C::kQueriesLds, QR = 2 * D32 - QL;
+    uint4* const queries = lds.q + wave * QL * 64 + lane;
+    bf16x8 qf[QR];
+    {
+      const int64_t at = token * a.ld_q + (int64_t)(kvh * p.group + row - row_token * p.group) * D + h * 16;
+#pragma unroll
+      for (int j = 0; j < 2 * D32; ++j) {
+        const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)a.q + at + (j >> 1) * 32 + 8 * (j & 1));
+        if (j < QR) qf[j] = __builtin_bit_cast(bf16x8, q);
+        else queries[(j - QR) * 64] = q;
+      }
+    }
+    auto query = [&](int j) __attribute__((always_inline)) {
+      return j < QR ? qf[j < QR ? j : 0] : __builtin_bit_cast(bf16x8, queries[(j < QR ? 0 : j - QR) * 64]);
+    };
+
+    float m = kLowest, l = 0.0f;
+    floatx16 o[D32];
+#pragma unroll
+    for (int d = 0; d < D32; ++d) o[d] = floatx16{};
+
+    struct Where {
+      const int* list;
+      int base, n;
+    };
+    auto where = [&](int s) __attribute__((always_inline)) {
+      if (s < prefix_steps) return Where{a.prefix_pages, s * C::kStepTokens, p.prefix_len};
+      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * C::kStepTokens, limit_last};
+    };
+    // Step of this region in unit u; past the last one, that one again (so
+    // every wave copies as much, and nothing reads it).
+    auto step_of = [&](int u) { return min(u * C::kWT + wt, steps - 1); };
+    // The blocks a lane copies from: of its key pieces, of its value pieces,
+    // and that of its token for the scales.
+    auto col_of_piece = [&](int k) { return NT == 1 ? wm * PW % D32 + k : k % D32; };
+    auto block_of = [&](const Where& w, int b) { return min((w.base >> 4) + b, (w.n - 1) >> 4); };
+    auto slot_of = [&](int blk) { return (kvh << a.c.page_shift) + (blk & page_blocks_mask) * 16; };
+    auto row_of = [&](int id, int64_t ld) {
+      return (uint64_t)((unsigned)id < (unsigned)a.c.n_pages ? (unsigned)id : 0u) * (uint64_t)(uint32_t)ld;
+    };
+    int pages[2 * NT + 1];
+    auto load_pages = [&](int u) __attribute__((always_inline)) {
+      const Where w = where(step_of(u));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int tile = NT == 1 ? wm * PW / D32 : t;
+        pages[t] = w.list[block_of(w, 2 * tile + kh) >> page_blocks_shift];
+        pages[NT + t] = w.list[block_of(w, 2 * tile + h) >> page_blocks_shift];
+      }
+      pages[2 * NT] = w.list[block_of(w, scale_token >> 4) >> page_blocks_shift];
+    };
+    // Starts the copy of unit u; its scales go through registers to the
+    // wave's own table (put_scales), as floats.
+    uint32_t key_scale = 0, value_scale = 0;
+    uint64_t bad = 0, bad_next = 0;  // bit 16 b for block b of the step if its page does not exist
+    auto copy = [&](int u, uint8_t* stage) __attribute__((always_inline)) {
+      const Where w = where(step_of(u));
+      uint8_t* const region = stage + wt * (2 * C::kHalf) + wm * PW * 1024;
+      const uint8_t *kp[NT], *vp[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int tile = NT == 1 ? wm * PW / D32 : t;
+        kp[t] = a.c.kc + row_of(pages[t], a.c.ld_codes) + (uint32_t)(slot_of(block_of(w, 2 * tile + kh)) * D + key_src);
+        vp[t] = a.c.vc + row_of(pages[NT + t], a.c.ld_codes) + (uint32_t)(slot_of(block_of(w, 2 * tile + h)) * D + value_src);
+      }
+#pragma unroll
+      for (int k = 0; k < PW; ++k)
+        copy_to_lds16(kp[NT == 1 ? 0 : k / D32] + col_of_piece(k) * 128, region + k * 1024);
+#pragma unroll
+      for (int k = 0; k < PW; ++k)
+        copy_to_lds16(vp[NT == 1 ? 0 : k / D32] + col_of_piece(k) * 512, region + C::kHalf + k * 1024);
+      const uint64_t at = row_of(pages[2 * NT], a.c.ld_scales) + (uint32_t)(slot_of(block_of(w, scale_token >> 4)) + (lane & 15));
+      key_scale = a.c.ks[at];
+      value_scale = a.c.vs[at];
+      bad_next = __ballot((unsigned)pages[2 * NT] >= (unsigned)a.c.n_pages) & (~0ull >> (64 - C::kStepTokens));
+    };
+    float* const key_scales = lds.scales[wave][0];
+    float* const value_scales = lds.scales[wave][1];
+    auto put_scales = [&]() __attribute__((always_inline)) {
+      key_scales[lane] = __uint_as_float(key_scale << 23);
+      value_scales[lane] = __uint_as_float(value_scale << 23);
+      bad = bad_next;
+    };
+
+    // One step. The fragments are read kAhead before their use and the order
+    // is pinned (sched_barrier): left alone, the compiler reads each
+    // right before its conversion and waits for it.
+    constexpr int kAhead = D == 256 ? 2 : 3, F = TT * D32;
+    auto step = [&](int u, uint8_t* stage) __attribute__((always_inline)) {
+      const int s = u * C::kWT + wt;
+      const Where w = where(min(s, steps - 1));
+      const int row_sees = s >= steps ? 0 : s < prefix_steps ? w.n : limit;  // tokens of the list before this row's first unseen one
+      const bool masked = bad != 0 || s >= steps || w.base + C::kStepTokens > (s < prefix_steps ? w.n : limit_first);
+      uint8_t* const keys = stage + wt * (2 * C::kHalf) + lane * 16;
+      uint8_t* const values = keys + C::kHalf;
+
+      if (masked) {
+        // Bytes that hold no token that any row sees may be NaN codes, and
+        // their scales infinite (0 * NaN): clear them.  The waves of a region
+        // write the same zeros, each before it reads.
+        asm volatile("");  // a real branch: the steps that take it are few
+        const int held = s >= steps ? 0 : w.n;
+        const bool there = w.base + scale_token < held && !(bad >> (scale_token & 48) & 1u);
+        if (!there) value_scales[lane] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int holds = (bad >> (16 * (2 * t + h)) & 1u) ? 0 : held - (w.base + 32 * t + 16 * h);
+          uint32_t keep[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) keep[e] = keep_bytes(holds - 4 * e);
+          for (int d = 0; d < D32; ++d) {
+            u32x4* const v = reinterpret_cast<u32x4*>(values + (t * D32 + d) * 1024);
+            *v = *v & u32x4{keep[0], keep[1], keep[2], keep[3]};
+          }
+        }
+      }
+
+      floatx16 sc[TT];
+      float ks[TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        ks[t] = key_scales[32 * t + key_token];
+        sc[t] = floatx16{};
+      }
+      uint4 fr[kAhead];
+#pragma unroll
+      for (int f = 0; f < kAhead; ++f) fr[f] = *reinterpret_cast<const uint4*>(keys + ((f % TT) * D32 + f / TT) * 1024);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {  // tile f % TT, dimensions 32 (f / TT) ..
+        const int t = f % TT, j = f / TT;
+        const uint4 q = fr[f % kAhead];
+        const bf16x8 k0 = decode8(q.x, q.y, ks[t]), k1 = decode8(q.z, q.w, ks[t]);
+        if (f + kAhead < F)
+          fr[f % kAhead] = *reinterpret_cast<const uint4*>(keys + (((f + kAhead) % TT) * D32 + (f + kAhead) / TT) * 1024);
+        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, query(2 * j), sc[t], 0, 0, 0);
+        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, query(2 * j + 1), sc[t], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int f = 0; f < kAhead; ++f) fr[f] = *reinterpret_cast<const uint4*>(values + ((f % TT) * D32 + f / TT) * 1024);
+
+      if (masked) {
+        asm volatile("");
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int sees = (bad >> (16 * (2 * t + h)) & 1u) ? 0 : row_sees - (w.base + 32 * t + 16 * h);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sc[t][r] = r < sees ? sc[t][r] : -__builtin_inff();
+        }
+      }
+
+      float top = kLowest;
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[t][r]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float mn = fmaxf(m, top * a.scale_log2);
+      if (__any(mn > m)) {
+        const float f = __builtin_amdgcn_exp2f(m - mn);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < D32; ++d) o[d] *= f;
+        m = mn;
+      }
+      bf16x8 pf[TT][2];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        float e[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          e[r] = __builtin_amdgcn_exp2f(fmaf(sc[t][r], a.scale_log2, -m));
+          l += e[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const f32x4 vs = *reinterpret_cast<const f32x4*>(value_scales + 32 * t + 16 * h + r);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) e[r + b] *= vs[b];
+        }
+        pf[t][0] = take_term(e);
+        pf[t][1] = take_term(e + 8);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int t = f % TT, d = f / TT;
+        const uint4 v = fr[f % kAhead];
+        const bf16x8 v0 = decode8(v.x, v.y, 1.0f), v1 = decode8(v.z, v.w, 1.0f);
+        if (f + kAhead < F)
+          fr[f % kAhead] = *reinterpret_cast<const uint4*>(values + (((f + kAhead) % TT) * D32 + (f + kAhead) / TT) * 1024);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, pf[t][0], o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, pf[t][1], o[d], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
+    // Unit u is in one stage while u + 1 is copied into the other: a wave's
+    // own copies have landed (wait_vmem) and every wave is done reading the
+    // stage that is overwritten (the barrier).
+    if (u0 < u_end) {
+      load_pages(u0);
+      copy(u0, stage_a);
+      load_pages(u0 + 1);
+      for (int u = u0; u < u_end; u += 2) {
+        wait_vmem<0>();
+        put_scales();
+        barrier_lds();
+        copy(u + 1, stage_b);
+        load_pages(u + 2);
+        step(u, stage_a);
+        if (u + 1 >= u_end) break;
+        wait_vmem<0>();
+        put_scales();
+        barrier_lds();
+        copy(u + 2, stage_a);
+        load_pages(u + 3);
+        step(u + 1, stage_b);
+      }
+      wait_vmem<0>();  // copies past the last unit
+    }
+
+    // Join the regions: waves of wt > 0 hand theirs to the wave of wt = 0
+    // with the same rows (register by register; half in each stage array).
+    l += __shfl_xor(l, 32);
+    barrier_lds();
+    constexpr int kOut = D32 * 16;  // accumulator registers
+    if constexpr (C::kWT > 1) {
+      float* const half_a = reinterpret_cast<float*>(stage_a);
+      float* const half_b = reinterpret_cast<float*>(stage_b);
+      if (wt > 0) {
+        const int at = ((wt - 1) * WM + wm) * (kOut / 2) * 64 + lane;
+#pragma unroll
+        for (int r = 0; r < kOut / 2; ++r) {
+          half_a[at + r * 64] = o[r >> 4][r & 15];
+          half_b[at + r * 64] = o[(r + kOut / 2) >> 4][r & 15];
+        }
+        if (h == 0) {
+          lds.ml[wave][i][0] = m;
+          lds.ml[wave][i][1] = l;
+        }
+      }
+      barrier_lds();
+      if (wt == 0) {
+        float top = m;
+#pragma unroll
+        for (int w = 1; w < C::kWT; ++w) top = fmaxf(top, lds.ml[w * WM + wm][i][0]);
+        const float f0 = __builtin_amdgcn_exp2f(m - top);
+        l *= f0;
+#pragma unroll
+        for (int d = 0; d < D32; ++d) o[d] *= f0;
+#pragma unroll
+        for (int w = 1; w < C::kWT; ++w) {
+          const float f = __builtin_amdgcn_exp2f(lds.ml[w * WM + wm][i][0] - top);
+          l += lds.ml[w * WM + wm][i][1] * f;
+          const int at = ((w - 1) * WM + wm) * (kOut / 2) * 64 + lane;
+#pragma unroll
+          for (int r = 0; r < kOut / 2; ++r) {
+            o[r >> 4][r & 15] += half_a[at + r * 64] * f;
+            o[(r + kOut / 2) >> 4][r & 15] += half_b[at + r * 64] * f;
+          }
+        }
+        m = top;
+      }
+    }
+    const int r = 32 * wm + i;  // row of the tile
+    if (wt == 0 && row0 + r < p.rows) {
+      const bool whole = p.direct && u0 == 0 && u1 == units;
+      if (!whole) {
+        const int64_t at = ((int64_t)tile + wg) * C::kRows + r;
+        if (h == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
+#pragma unroll
+        for (int d = 0; d < D32; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<f32x4*>(p.o + at * D + 32 * d + 8 * e + 4 * h) =
+                f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+      } else if (len >= 0) {
+        const float inv = inverse_sum(l);
+#pragma unroll
+        for (int d = 0; d < D32; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v[4] = {o[d][4 * e] * inv, o[d][4 * e + 1] * inv, o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv};
+            store_out4<NVFP4_DTYPE_BF16>(a, (int)token, kvh * p.group + row - row_token * p.group, 32 * d + 8 * e + 4 * h, v);
+          }
+      }
+    }
+    barrier_lds();
 
     unit += u1 - u0;
     if (unit >= last_unit) break;
@@ -474,61 +913,165 @@ __global__ __launch_bounds__(kThreads) void kv_attention_kernel(KvAttnArgs a, Pa
   }
 }
 
+template <int D, int WM>
+__global__ __launch_bounds__(kThreads, WM == 1 ? 1 : 2) void kv_attention_rows_kernel(KvAttnArgs a, Pass p) {
+  typedef RowsShape<D, WM> C;
+  __shared__ __attribute__((aligned(16))) uint8_t stage_a[C::kStageBytes], stage_b[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) float scales[kWaves][2][kStep];
+  __shared__ float ml[kWaves][32][2];
+  __shared__ int64_t line[kWaves + 2];
+  __shared__ uint4 q[C::kQueriesLds * kWaves * 64 + 1];
+  rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stage_a, stage_b, scales, ml, line, q});
+}
+
+// The shared prefix and the sequences' own tokens in one launch: the first is
+// bound by the matrix and vector units, the second by memory, so that each
+// uses what the other leaves.  Where not all workgroups fit the chip at once,
+// the first kSlots of the grid are those of the prefix (few and long, one
+// round) with own ones spread among them, by eights since workgroups are
+// dealt to the 8 XCDs in turn; the rest of the own ones follow as places
+// become free.  WM = 0: 16-row tiles for the prefix as well.
+constexpr int kSlots = 512;  // two workgroups on each of 256 CUs
+
+template <int DT, int D, int WM>
+__global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_attention_both_kernel(KvAttnArgs a, Pass shared, Pass own) {
+  constexpr int kStage = WM == 0 ? 0 : RowsShape<D, WM == 0 ? 4 : WM>::kStageBytes;
+  constexpr int kPart = 16 * D * (int)sizeof(float);
+  constexpr int kBytes = kStage > kPart ? kStage : kPart;
+  __shared__ __attribute__((aligned(16))) uint8_t stage_a[kBytes], stage_b[kBytes];
+  __shared__ __attribute__((aligned(16))) float scales[kWaves][2][kStep];
+  constexpr int kStreamQ = kTerms<DT> * (D / 32) * 64, kRowsQ = WM == 0 ? 0 : RowsShape<D, WM == 0 ? 4 : WM>::kQueriesLds * kWaves * 64;
+  __shared__ uint4 q[kStreamQ > kRowsQ ? kStreamQ : kRowsQ];
+  __shared__ float ml[kWaves][32][2];
+  __shared__ int64_t line[kWaves + 2];
+  const int b = blockIdx.x, n = shared.workgroups;
+  bool first = b < n;
+  int wg = first ? b : b - n;
+  if (gridDim.x > kSlots && b < kSlots) {  // here n is a multiple of 8 and less than kSlots
+    const int e = b >> 3, k = e * (n >> 3) / (kSlots / 8);
+    first = (e + 1) * (n >> 3) / (kSlots / 8) > k;
+    wg = (first ? k : e - k) * 8 + (b & 7);
+  } else if (gridDim.x > kSlots) {
+    first = false;
+    wg = b - n;
+  }
+  const StreamLds<DT, D> stream{(float*)stage_a, (float*)stage_b, q, ml, line};
+  if (!first) {
+    stream_body<DT, D, DT == NVFP4_DTYPE_BF16>(a, own, wg, stream);
+  } else if constexpr (WM == 0) {
+    stream_body<DT, D, DT == NVFP4_DTYPE_BF16>(a, shared, wg, stream);
+  } else {
+    rows_body<D, WM>(a, shared, wg, RowsLds{stage_a, stage_b, scales, ml, line, q});
+  }
+}
+
 // Joins the pieces of the rows: of the sequence's own pass and, where the
-// prefix was computed for all rows together, of that pass.  A workgroup
-// takes one tile of the own pass, a wave one row at a time.
-template <int DT, int D>
+// prefix was computed for all rows together, of that pass.  D / 4 lanes take
+// a row.  S = 1: as many rows as that gives, for many rows of few pieces;
+// S = 4: the four waves share the pieces of a row, for few rows cut into many.
+// The lanes of a row first read (M, l) of a piece each and find the weights,
+// then the pieces' o, kBatch loads at a time.
+template <int DT, int D, int S>
 __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs a, Pass own, Pass shared) {
-  constexpr int V = D / 64;  // dimensions of a lane
-  __shared__ int64_t lds_line[kWaves + 2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tiles_per_seq = a.c.heads * own.row_tiles;
-  const int tile = blockIdx.x, seq = tile / tiles_per_seq, x = tile - seq * tiles_per_seq;
-  const int kvh = x / own.row_tiles, row0 = (x - kvh * own.row_tiles) * kTileRows;
-  const int len = own_len(own, seq);
-  Line line(own, tiles_per_seq, lds_line);
-  const int units = tile_units(own, len);
-  const int64_t first = line.before_seq(own, seq) * tiles_per_seq + (int64_t)x * units;
-  const int w0 = (int)(first / line.share), w1 = (int)((first + units - 1) / line.share);
-  if (len < 0) return;
-  if (own.direct && w0 == w1) return;
+  constexpr int LR = D / 4, RW = 64 / LR;  // lanes of a row, rows of a wave
+  constexpr int R = RW * kWaves / S;       // rows of a workgroup at a time
+  constexpr int kBatch = 4;
+  __shared__ float lds_ml[kWaves][RW][2];
+  __shared__ __attribute__((aligned(16))) float lds_o[kWaves][RW][D];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k = lane & (LR - 1), group = lane / LR, part = S == 1 ? 0 : wave;
+  const int seq = blockIdx.x / a.c.heads, kvh = blockIdx.x - seq * a.c.heads;
+  if (own_len(own, seq) < 0) return;
 
-  int64_t shared_share = 1;
-  const int shared_units = shared.batch ? tile_units(shared, 0) : 0;
-  if (shared.batch) shared_share = ((int64_t)shared_units * a.c.heads * shared.row_tiles + shared.workgroups - 1) / shared.workgroups;
-
-  for (int r = wave; r < kTileRows && row0 + r < own.rows; r += kWaves) {
-    const int row = row0 + r, row_token = row / own.group, h = row - row_token * own.group;
+  for (int row0 = blockIdx.y * R; row0 < own.rows; row0 += gridDim.y * R) {
+    const int row = row0 + (S == 1 ? wave * RW : 0) + group;
+    const int rc = min(row, own.rows - 1);
+    const int row_token = rc / own.group, hd = rc - row_token * own.group;
     const int token = seq * own.q_len + row_token;
-    float m = kLowest, l = 0.0f, acc[V] = {};
-    auto add = [&](const Pass& p, int64_t at) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.ml + at * 2);
-      if (ml.y == 0.0f) return;  // no token in this piece
-      const float mn = fmaxf(m, ml.x), f = __builtin_amdgcn_exp2f(m - mn), fp = __builtin_amdgcn_exp2f(ml.x - mn);
-      l = l * f + ml.y * fp;
-      const float* src = p.o + at * D + lane * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = acc[e] * f + src[e] * fp;
-      m = mn;
-    };
+    // the row's pieces: the row in the first one's slot, and their number
+    const int tx = rc / own.tile_rows, tile = (seq * a.c.heads + kvh) * own.row_tiles + tx;
+    const int2 head = own.head[tile];
+    const bool done = row >= own.rows || (own.direct && head.y == 1);  // nothing there, or written by its workgroup
+    const int n_own = done ? 0 : head.y;
+    const int64_t own_at = ((int64_t)tile + head.x) * own.tile_rows + (rc - tx * own.tile_rows);
+    int n_shared = 0;
+    int64_t shared_at = 0;
     if (shared.batch) {
-      const int64_t pr = (int64_t)token * shared.group + h;
-      const int t = kvh * shared.row_tiles + (int)(pr / kTileRows);
-      const int64_t u = (int64_t)t * shared_units;
-      for (int64_t w = u / shared_share; w <= (u + shared_units - 1) / shared_share; ++w)
-        add(shared, (t + w) * kTileRows + pr % kTileRows);
+      const int pr = token * shared.group + hd, pt = pr / shared.tile_rows, t = kvh * shared.row_tiles + pt;
+      const int2 sh = shared.head[t];
+      n_shared = done ? 0 : sh.y;
+      shared_at = ((int64_t)t + sh.x) * shared.tile_rows + (pr - pt * shared.tile_rows);
     }
-    for (int w = w0; w <= w1; ++w) add(own, ((int64_t)tile + w) * kTileRows + r);
-    const float inv = inverse_sum(l);
+    const int n = n_own + n_shared;
+    // row of piece j (of the first one where the row has none: any valid place)
+    auto place = [&](int j, bool& is_own) {
+      is_own = j >= n_shared;
+      return is_own ? own_at + (int64_t)max(min(j - n_shared, n_own - 1), 0) * own.tile_rows
+                    : shared_at + (int64_t)j * shared.tile_rows;
+    };
+    const int most = (int)wave_max((float)n);  // (exact: n is at most a few thousand)
+
+    float m = kLowest, l = 0.0f;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < most; c += LR * S) {
+      const int j = c + k * S + part;
+      float2 ml = make_float2(kLowest, 0.0f);
+      if (j < n) {
+        bool is_own;
+        const int64_t at = place(j, is_own);
+        ml = *reinterpret_cast<const float2*>((is_own ? own.ml : shared.ml) + at * 2);
+      }
+      float mn = fmaxf(m, ml.x);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] *= inv;
-    const int64_t at = token * a.ld_out + (int64_t)(kvh * own.group + h) * D + lane * V;
-    if constexpr (DT == NVFP4_DTYPE_F32) {
+      for (int off = LR / 2; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor(mn, off));
+      const float f = ml.y > 0.0f ? __builtin_amdgcn_exp2f(ml.x - mn) : 0.0f;  // a piece without tokens holds nothing
+      float sum = ml.y * f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) ((float*)a.out)[at + e] = acc[e];
-    } else {
+      for (int off = LR / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+      const float old = __builtin_amdgcn_exp2f(m - mn);
+      l = l * old + sum;
+      acc *= old;
+      m = mn;
+      const int count = min(LR, ceil_div(most - c, S));
+      for (int q0 = 0; q0 < count; q0 += kBatch) {
+        f32x4 v[kBatch];
+        float wq[kBatch];
 #pragma unroll
-      for (int e = 0; e < V; ++e) ((uint16_t*)a.out)[at + e] = (uint16_t)f32_to_bf16_bits(acc[e]);
+        for (int b = 0; b < kBatch; ++b) {
+          const int q = min(q0 + b, LR - 1);
+          const float wf = __shfl(f, group * LR + q);
+          wq[b] = q0 + b < LR ? wf : 0.0f;
+          bool is_own;
+          const int64_t at = place(min(c + q * S + part, max(n - 1, 0)), is_own);
+          v[b] = wq[b] != 0.0f ? *reinterpret_cast<const f32x4*>((is_own ? own.o : shared.o) + at * D + 4 * k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) acc += v[b] * wq[b];
+      }
+    }
+    if constexpr (S > 1) {
+      if (k == 0) {
+        lds_ml[wave][group][0] = m;
+        lds_ml[wave][group][1] = l;
+      }
+      *reinterpret_cast<f32x4*>(&lds_o[wave][group][4 * k]) = acc;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < S; ++w) m = fmaxf(m, lds_ml[w][group][0]);
+      l = 0.0f;
+      acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < S; ++w) {
+        const float f = __builtin_amdgcn_exp2f(lds_ml[w][group][0] - m);
+        l += lds_ml[w][group][1] * f;
+        acc += *reinterpret_cast<const f32x4*>(&lds_o[w][group][4 * k]) * f;
+      }
+      __syncthreads();
+    }
+    if (!done && part == 0) {
+      const float inv = inverse_sum(l);
+      const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+      store_out4<DT>(a, token, kvh * own.group + hd, 4 * k, v);
     }
   }
 }
@@ -538,8 +1081,37 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
 struct Plan {
   Pass own{}, shared{};  // shared.batch == 0: no such pass
   bool join;
+  int join_waves;  // waves of a row in the join
   size_t floats;
 };
+
+int64_t pass_tiles(const KvAttnArgs& a, const Pass& p) { return (int64_t)p.batch * a.c.heads * p.row_tiles; }
+// Floats of a pass's part of the workspace: partials, and the tiles' heads.
+size_t pass_floats(const KvAttnArgs& a, const Pass& p) {
+  return (size_t)(pass_tiles(a, p) + p.workgroups) * p.tile_rows * (2 + a.c.dim) + (2 * (size_t)pass_tiles(a, p) + 3) / 4 * 4;
+}
+
+// Tile shape and number of workgroups of a pass with its rows, prefix_len
+// and max_len set: 16-row tiles for up to stream_rows rows.
+void shape_pass(const KvAttnArgs& a, Pass& p, int stream_rows) {
+  int per_cu;
+  if (a.dtype == NVFP4_DTYPE_F32 || p.rows <= stream_rows) {
+    p.tile_rows = kTileRows;
+    p.step = kStep;
+    p.step_waves = kWaves;
+    per_cu = a.dtype == NVFP4_DTYPE_F32 || (a.c.dim == 256 && stream_rows == kTileRows) ? 1 : 2;
+  } else {
+    const int wm = p.rows <= 32 ? 1 : p.rows <= 64 ? 2 : 4;
+    p.tile_rows = 32 * wm;
+    p.step = a.c.dim == 256 ? 32 : 64;
+    p.step_waves = kWaves / wm;
+    per_cu = wm == 1 ? 1 : 2;
+  }
+  p.row_tiles = ceil_div(p.rows, p.tile_rows);
+  const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step);
+  const int64_t units = pass_tiles(a, p) * max(1, ceil_div(steps, p.step_waves));
+  p.workgroups = (int)min(units, (int64_t)(256 * per_cu));
+}
 
 Plan make_plan(const KvAttnArgs& a) {
   Plan pl{};
@@ -548,31 +1120,48 @@ Plan make_plan(const KvAttnArgs& a) {
   own.q_len = a.q_len;
   own.group = a.group;
   own.rows = a.q_len * a.group;
-  own.row_tiles = ceil_div(own.rows, kTileRows);
   own.lens = a.lens;
   own.max_len = a.max_len;
-  const bool share = a.batch > 1 && a.prefix_len >= 256;
+  const bool share = a.batch > 1 && a.prefix_len >= 256 && own.rows < 128;
   own.prefix_len = share ? 0 : a.prefix_len;
   own.direct = !share;
-  const int max_units = ceil_div(ceil_div(own.prefix_len, kStep) + ceil_div(own.max_len, kStep), kWaves);
-  const int64_t own_tiles = (int64_t)own.batch * a.c.heads * own.row_tiles;
-  own.workgroups = (int)min(own_tiles * max(max_units, 1), (int64_t)(a.c.dim == 256 ? 256 : 512));
-  pl.join = share || max_units > 1;
-  size_t slots = (size_t)own_tiles + own.workgroups;
-  size_t at = pl.join ? slots * kTileRows * (2 + a.c.dim) : 0;
+  shape_pass(a, own, kTileRows);
+  const int own_steps = ceil_div(own.prefix_len, own.step) + ceil_div(own.max_len, own.step);
+  pl.join = share || own_steps > own.step_waves;
+  pl.floats = pl.join ? pass_floats(a, own) : 0;
+  int64_t pieces = own.workgroups / pass_tiles(a, own);
   if (share) {
     Pass& sh = pl.shared;
     sh.batch = 1;
     sh.q_len = a.batch * a.q_len;
     sh.group = a.group;
     sh.rows = sh.q_len * a.group;
-    sh.row_tiles = ceil_div(sh.rows, kTileRows);
     sh.prefix_len = a.prefix_len;
-    const int64_t tiles = (int64_t)a.c.heads * sh.row_tiles;
-    sh.workgroups = (int)min(tiles * ceil_div(ceil_div(a.prefix_len, kStep), kWaves), (int64_t)(a.c.dim == 256 ? 256 : 512));
-    at += (size_t)(tiles + sh.workgroups) * kTileRows * (2 + a.c.dim);
+    // together with an own pass of 16-row tiles (launch_both), two such tiles
+    // rather than one of 32: that one's LDS would leave one workgroup to a CU
+    shape_pass(a, sh, own.tile_rows == kTileRows ? 2 * kTileRows : kTileRows);
   }
-  pl.floats = at;
+  if (share && own.tile_rows == kTileRows && pl.shared.workgroups + own.workgroups > kSlots) {
+    // launch_both: the prefix's workgroups get their part of the places by
+    // the time that both take.  Measured alone: a unit of a 64- or 128-row
+    // tile 3.0 us, one of a 16-row tile 7 us per 128 dimensions (two
+    // workgroups to a CU); the sequences are taken to be half of max_len.
+    Pass& sh = pl.shared;
+    auto units = [&](const Pass& p, int len) {
+      return (double)pass_tiles(a, p) * max(1, ceil_div(ceil_div(p.prefix_len, p.step) + ceil_div(len, p.step), p.step_waves));
+    };
+    const double narrow = 7.0 * a.c.dim / 128, ts = units(sh, 0) * (sh.tile_rows == kTileRows ? narrow : 3.0);
+    const double to = units(own, (own.max_len + 1) / 2) * narrow;
+    const int n = (int)(kSlots * ts / (ts + to)) & ~7;
+    sh.workgroups = min(max(n, 64), kSlots - 64);
+    const int64_t most = (int64_t)units(sh, 0);
+    if (sh.workgroups > most) sh.workgroups = (int)((most + 7) & ~7);
+  }
+  if (share) {
+    pl.floats += pass_floats(a, pl.shared);
+    pieces += pl.shared.workgroups / pass_tiles(a, pl.shared);
+  }
+  pl.join_waves = pieces > 16 ? kWaves : 1;
   return pl;
 }
 
@@ -587,6 +1176,38 @@ void for_types(int dtype, int dim, F f) {
   else with(std::integral_constant<int, NVFP4_DTYPE_F32>());
 }
 
+template <int DT, int D>
+hipError_t launch_pass(const KvAttnArgs& a, const Pass& p, hipStream_t s) {
+  if (p.tile_rows == kTileRows) {
+    kv_attention_kernel<DT, D><<<p.workgroups, kThreads, 0, s>>>(a, p);
+  } else if constexpr (DT == NVFP4_DTYPE_BF16) {
+    if (p.tile_rows == 32) kv_attention_rows_kernel<D, 1><<<p.workgroups, kThreads, 0, s>>>(a, p);
+    else if (p.tile_rows == 64) kv_attention_rows_kernel<D, 2><<<p.workgroups, kThreads, 0, s>>>(a, p);
+    else kv_attention_rows_kernel<D, 4><<<p.workgroups, kThreads, 0, s>>>(a, p);
+  }
+  return hipGetLastError();
+}
+
+// The prefix of all and the sequences' own tokens.
+template <int DT, int D>
+hipError_t launch_both(const KvAttnArgs& a, const Pass& shared, const Pass& own, hipStream_t s) {
+  const int grid = shared.workgroups + own.workgroups;
+  if (shared.tile_rows == kTileRows) {
+    kv_attention_both_kernel<DT, D, 0><<<grid, kThreads, 0, s>>>(a, shared, own);
+  } else if constexpr (DT == NVFP4_DTYPE_BF16) {
+    if (shared.tile_rows == 64) kv_attention_both_kernel<DT, D, 2><<<grid, kThreads, 0, s>>>(a, shared, own);
+    else kv_attention_both_kernel<DT, D, 4><<<grid, kThreads, 0, s>>>(a, shared, own);
+  }
+  return hipGetLastError();
+}
+
+template <int DT, int D, int S>
+hipError_t launch_join(const KvAttnArgs& a, const Plan& pl, hipStream_t s) {
+  const dim3 grid(a.batch * a.c.heads, min(ceil_div(pl.own.rows, 256 / D * kWaves / S), 65535));
+  kv_attention_join_kernel<DT, D, S><<<grid, kThreads, 0, s>>>(a, pl.own, pl.shared);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t kv_attention_workspace(const KvAttnArgs& a) {
@@ -595,26 +1216,25 @@ size_t kv_attention_workspace(const KvAttnArgs& a) {
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, void* ws, hipStream_t s) {
   Plan pl = make_plan(a);
-  const int64_t own_tiles = (int64_t)pl.own.batch * a.c.heads * pl.own.row_tiles;
   float* at = (float*)ws;
-  auto place = [&](Pass& p, int64_t tiles) {
-    const int64_t slots = tiles + p.workgroups;
+  auto place = [&](Pass& p) {
+    const int64_t rows = (pass_tiles(a, p) + p.workgroups) * p.tile_rows;
     p.o = at;
-    p.ml = at + slots * kTileRows * a.c.dim;
-    at = p.ml + slots * kTileRows * 2;
+    p.ml = at + rows * a.c.dim;
+    p.head = (int2*)(p.ml + rows * 2);
+    at += pass_floats(a, p);
   };
-  place(pl.own, own_tiles);
-  if (pl.shared.batch) place(pl.shared, (int64_t)a.c.heads * pl.shared.row_tiles);
+  if (pl.join) place(pl.own);
+  if (pl.shared.batch) place(pl.shared);
   hipError_t err = hipSuccess;
   for_types(a.dtype, a.c.dim, [&](auto dt, auto d) {
-    if (pl.shared.batch) {
-      kv_attention_kernel<dt(), d()><<<pl.shared.workgroups, kThreads, 0, s>>>(a, pl.shared);
-      if ((err = hipGetLastError()) != hipSuccess) return;
+    if (pl.shared.batch && pl.own.tile_rows == kTileRows) {
+      if ((err = launch_both<dt(), d()>(a, pl.shared, pl.own, s)) != hipSuccess) return;
+    } else {
+      if (pl.shared.batch && (err = launch_pass<dt(), d()>(a, pl.shared, s)) != hipSuccess) return;
+      if ((err = launch_pass<dt(), d()>(a, pl.own, s)) != hipSuccess || !pl.join) return;
     }
-    kv_attention_kernel<dt(), d()><<<pl.own.workgroups, kThreads, 0, s>>>(a, pl.own);
-    if ((err = hipGetLastError()) != hipSuccess || !pl.join) return;
-    kv_attention_join_kernel<dt(), d()><<<(int)own_tiles, kThreads, 0, s>>>(a, pl.own, pl.shared);
-    err = hipGetLastError();
+    err = pl.join_waves == 1 ? launch_join<dt(), d(), 1>(a, pl, s) : launch_join<dt(), d(), kWaves>(a, pl, s);
   });
   return err;
 }

@@ -41,6 +41,7 @@ int check_pages(const nvfp4_kv_pages* c, KvPages& out) {
   const int64_t per = (int64_t)c->kv_heads * c->page_size;
   if (c->ld_codes < per * c->head_dim || c->ld_codes % 16 != 0) return NVFP4_ERR_STRIDE;
   if (c->ld_scales < per || c->ld_scales % 16 != 0) return NVFP4_ERR_STRIDE;
+  if (c->ld_codes >= kIndexLimit || c->ld_scales >= kIndexLimit) return NVFP4_ERR_RANGE;
   if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16))
     return NVFP4_ERR_ALIGN;
   out.kc = c->k_codes;
@@ -67,8 +68,8 @@ int check_batch(const nvfp4_kv_batch* b, int page_size, int q_heads, int dtype, 
   if (b->batch >= kIndexLimit || b->q_len >= kIndexLimit || b->max_len >= kIndexLimit || b->prefix_len >= kIndexLimit)
     return NVFP4_ERR_RANGE;
   if (b->batch * b->q_len >= kIndexLimit / q_heads) return NVFP4_ERR_RANGE;
-  // one workgroup of 256 threads for each 16 rows of a sequence and kv head, in a grid of less than 2^32
-  if (b->batch * a.c.heads * ((b->q_len * (q_heads / a.c.heads) + 15) / 16) >= (int64_t)1 << 24) return NVFP4_ERR_RANGE;
+  // a column of workgroups of 256 threads for each sequence and kv head, in a grid of less than 2^32
+  if (b->batch * a.c.heads >= (int64_t)1 << 24) return NVFP4_ERR_RANGE;
   a.dtype = dtype;
   a.q_heads = q_heads;
   a.group = q_heads / a.c.heads;

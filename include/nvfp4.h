@@ -445,8 +445,8 @@ int nvfp4_gdn_recurrence(const nvfp4_gdn_inputs* in, int in_dtype, int64_t token
  *   head_dim 64, 128 or 256; page_size a power of two, 16 <= page_size <=
  *   4096; 1 <= kv_heads <= 4096; n_pages * page_size < 2^31.
  *   ld_codes >= kv_heads * page_size * head_dim, ld_scales >= kv_heads *
- *   page_size (bytes between pages), both multiples of 16; all four pointers
- *   16-byte aligned.
+ *   page_size (bytes between pages), both multiples of 16 and below 2^31; all
+ *   four pointers 16-byte aligned.
  */
 typedef struct {
   uint8_t* k_codes;
@@ -535,8 +535,7 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
  * bf16, with NVFP4_DTYPE_F32 queries and weights enter as three bf16 terms
  * (24 bits).  The result does not depend on timing: the same call on the same
  * data gives the same bits.  1 <= q_len, batch * q_len < 2^31 / q_heads,
- * batch * kv_heads * ceil(q_len * q_heads / kv_heads / 16) < 2^24; q_heads a
- * multiple of kv_heads.  At most three launches.  batch = 0 is a
+ * batch * kv_heads < 2^24; q_heads a multiple of kv_heads.  At most three launches.  batch = 0 is a
  * valid call that does nothing.
  */
 int nvfp4_kv_pages_attention(const nvfp4_kv_pages* cache, const nvfp4_kv_batch* batch, const void* q,
