@@ -144,6 +144,62 @@ struct Line {
   }
 };
 
+// A workgroup's walk over its share: tile by tile, the units [u0, u1) of each.
+struct Walk {
+  int wg;  // the share's number
+  int64_t unit, last;
+  int tiles_per_seq;
+  int seq, len, units, x, tile;  // sequence, its own length and units; tile of the sequence, of the pass
+  int u0, u1;
+  bool any;
+  // Workgroups are dealt to the 8 XCDs in turn; each XCD gets neighbouring
+  // shares, which read the same pages (row tiles of a head, parts of one
+  // sequence) and find them in its L2.
+  __device__ Walk(const KvAttnArgs& a, const Pass& p, int dealt, int64_t* scratch) {
+    const int q = p.workgroups / 8, r = p.workgroups % 8, xcd = dealt % 8;
+    wg = xcd * q + min(xcd, r) + dealt / 8;
+    tiles_per_seq = a.c.heads * p.row_tiles;
+    Line line(p, tiles_per_seq, scratch);
+    unit = (int64_t)wg * line.share;
+    last = min(unit + line.share, line.total * tiles_per_seq);
+    any = unit < last;
+    if (!any) return;
+    int64_t before;
+    line.find(p, unit / tiles_per_seq, &seq, &before);
+    len = own_len(p, seq);
+    units = tile_units(p, len);
+    x = (int)((unit - before * tiles_per_seq) / units);
+    u0 = (int)(unit - before * tiles_per_seq - (int64_t)x * units);
+    share = line.share;
+    place(p);
+  }
+  __device__ bool next(const Pass& p) {
+    unit += u1 - u0;
+    if (unit >= last) return false;
+    u0 = 0;
+    if (++x == tiles_per_seq) {
+      x = 0;
+      ++seq;
+      len = own_len(p, seq);
+      units = tile_units(p, len);
+    }
+    place(p);
+    return true;
+  }
+  // every unit of the tile is this workgroup's
+  __device__ bool whole() const { return u0 == 0 && u1 == units; }
+
+ private:
+  int64_t share;
+  __device__ void place(const Pass& p) {
+    u1 = (int)min((int64_t)units, u0 + (last - unit));
+    tile = seq * tiles_per_seq + x;
+    // the join wants to know: the workgroup of unit 0 and the number of pieces
+    if (p.head != nullptr && u0 == 0 && threadIdx.x == 0)
+      p.head[tile] = make_int2(wg, (int)((unit + units - 1) / share - wg) + 1);
+  }
+};
+
 // 8 E4M3 bytes -> 8 bf16 values times the power of two `s` (exact).
 __device__ inline bf16x8 decode8(uint32_t a, uint32_t b, float s) {
   const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, s, false);
@@ -176,10 +232,6 @@ __device__ inline bf16x8 take_term(float f[8]) {
 __device__ inline uint32_t keep_bytes(int n) {
   const int c = min(max(n, 0), 4);
   return c == 4 ? 0xFFFFFFFFu : (1u << (8 * c)) - 1u;
-}
-
-__device__ inline void put_head(const Pass& p, int tile, int wg, int pieces) {
-  if (p.head != nullptr && threadIdx.x == 0) p.head[tile] = make_int2(wg, pieces);
 }
 
 // 1 / l, 0 for a row without tokens.
@@ -223,28 +275,15 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int tiles_per_seq = a.c.heads * p.row_tiles;
   const int prefix_steps = ceil_div(p.prefix_len, kStep);
   const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
 
-  Line line(p, tiles_per_seq, lds.line);
-  int64_t unit = (int64_t)wg * line.share;
-  const int64_t last_unit = min(unit + line.share, line.total * tiles_per_seq);
-  if (unit >= last_unit) return;
-  int seq;
-  int64_t seq_before;
-  line.find(p, unit / tiles_per_seq, &seq, &seq_before);
-
-  int len = own_len(p, seq), units = tile_units(p, len);
-  int x = (int)((unit - seq_before * tiles_per_seq) / units);  // tile of the sequence
-  int u0 = (int)(unit - seq_before * tiles_per_seq - (int64_t)x * units);
-
-  while (true) {
-    const int u1 = (int)min((int64_t)units, u0 + (last_unit - unit));
+  Walk t(a, p, wg, lds.line);
+  if (!t.any) return;
+  do {
+    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
     const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * kTileRows;
     const int steps = prefix_steps + ceil_div(max(len, 0), kStep);
-    const int tile = seq * tiles_per_seq + x;
-    if (u0 == 0) put_head(p, tile, wg, (int)((unit + units - 1) / line.share - wg) + 1);
 
     // This lane's query row and the first own token that it does not see.
     const int row = min(row0 + i, p.rows - 1);
@@ -479,8 +518,8 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
     if (wave == 0) {
       take(lds.part_b, 1);
       if (row0 + i < p.rows) {
-        if (!(p.direct && u0 == 0 && u1 == units)) {
-          const int64_t at = ((int64_t)tile + wg) * kTileRows + i;
+        if (!(p.direct && t.whole())) {
+          const int64_t at = ((int64_t)tile + t.wg) * kTileRows + i;
           if (g == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
 #pragma unroll
           for (int d = 0; d < DT16; ++d) *reinterpret_cast<f32x4*>(p.o + at * D + 16 * d + 4 * g) = o[d];
@@ -494,18 +533,8 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
         }
       }
     }
-
-    unit += u1 - u0;
-    if (unit >= last_unit) break;
     __syncthreads();  // the queries and the hand-over are read
-    u0 = 0;
-    if (++x == tiles_per_seq) {
-      x = 0;
-      ++seq;
-      len = own_len(p, seq);
-      units = tile_units(p, len);
-    }
-  }
+  } while (t.next(p));
 }
 
 // Two workgroups of a pass on a CU, except where one keeps more bytes in
@@ -522,8 +551,8 @@ __global__ __launch_bounds__(kThreads, (kPaired<DT, D>) ? 2 : 1) void kv_attenti
   stream_body<DT, D, kPaired<DT, D>>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line});
 }
 
-// The same for many rows (bf16): tiles of 32 * WM rows on 32 x 32 x 16 MFMA.
-// A wave owns 32 rows; WM waves work on the same tokens (a region of the
+// The same for more rows (bf16): tiles of 32 * WM rows (WM = 1, 2; with D =
+// 256 also 4) on 32 x 32 x 16 MFMA.  A wave owns 32 rows; WM waves work on the same tokens (a region of the
 // step's LDS stage), 4 / WM regions hold different tokens.  Reading the bytes
 // of 64 tokens (D = 128) from L2 for each wave on its own would ask for the
 // whole 64 bytes a cycle of a CU's path to L2, so they come once per region
@@ -536,8 +565,8 @@ __global__ __launch_bounds__(kThreads, (kPaired<DT, D>) ? 2 : 1) void kv_attenti
 template <int D, int WM>
 struct RowsShape {
   static constexpr int kWM = WM, kWT = kWaves / WM;
-  static constexpr int kStepTokens = D == 256 ? 32 : 64;
-  static constexpr int kTT = kStepTokens / 32;                 // 32-token tiles of a step
+  static constexpr int kTT = D == 256 ? 1 : 2;                 // 32-token tiles of a step
+  static constexpr int kStepTokens = 32 * kTT;
   static constexpr int kD32 = D / 32;
   static constexpr int kHalf = kStepTokens * D;                // key (or value) bytes of a region
   static constexpr int kPieces = kHalf / 1024 / WM;            // key (or value) pieces that a wave copies,
@@ -549,16 +578,18 @@ struct RowsShape {
   static constexpr int kQueriesLds = D == 256 ? (WM == 4 ? 6 : WM == 2 ? 2 : 0) : 0;
 };
 
-typedef const __attribute__((address_space(1))) uint32_t* global_u32_ptr;
-
-__device__ __attribute__((always_inline)) inline void copy_to_lds16(const uint8_t* from, uint8_t* to) {
-  __builtin_amdgcn_global_load_lds((global_u32_ptr)from, (lds_u32_ptr)to, 16, 0, 0);
+// LDS DMA of 16 bytes a lane: lane l's go to `to` + 16 l (`to` uniform).  As
+// the builtin, it would make every LDS read of the compiler's wait for every
+// copy in flight; written out, the kernel's own wait_vmem and barrier order
+// it (and no other instruction here uses m0).
+__device__ __attribute__((always_inline)) inline void copy_to_lds16(const uint8_t* from, const uint8_t* to) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(from) : "memory");
 }
 
-// Two stage arrays and not one of two stages: the compiler then knows that
-// reading one does not wait for copies into the other.
 struct RowsLds {
-  uint8_t *stage_a, *stage_b;
+  uint8_t* stages;  // 2 * kStageBytes
   float (*scales)[2][kStep];  // of a wave's tokens: keys', values'
   float (*ml)[32][2];
   int64_t* line;
@@ -569,12 +600,10 @@ template <int D, int WM>
 __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs& a, const Pass& p, const int wg, const RowsLds& lds) {
   typedef RowsShape<D, WM> C;
   constexpr int TT = C::kTT, D32 = C::kD32, PW = C::kPieces, NT = C::kTiles;
-  uint8_t* const stage_a = lds.stage_a;
-  uint8_t* const stage_b = lds.stage_b;
+  uint8_t* const stages = lds.stages;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wt = wave / WM;
   const int i = lane & 31, h = lane >> 5;
-  const int tiles_per_seq = a.c.heads * p.row_tiles;
   const int prefix_steps = ceil_div(p.prefix_len, C::kStepTokens);
   const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
 
@@ -585,23 +614,11 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
   const int scale_token = lane & (C::kStepTokens - 1);
   const int key_token = 16 * kh + 4 * (i >> 3) + (i & 3);
 
-  Line line(p, tiles_per_seq, lds.line);
-  int64_t unit = (int64_t)wg * line.share;
-  const int64_t last_unit = min(unit + line.share, line.total * tiles_per_seq);
-  if (unit >= last_unit) return;
-  int seq;
-  int64_t seq_before;
-  line.find(p, unit / tiles_per_seq, &seq, &seq_before);
-
-  int len = own_len(p, seq), units = tile_units(p, len);
-  int x = (int)((unit - seq_before * tiles_per_seq) / units);
-  int u0 = (int)(unit - seq_before * tiles_per_seq - (int64_t)x * units);
-
-  while (true) {
-    const int u1 = (int)min((int64_t)units, u0 + (last_unit - unit));
+  Walk t(a, p, wg, lds.line);
+  if (!t.any) return;
+  do {
+    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
     const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * C::kRows;
-    const int tile = seq * tiles_per_seq + x;
-    if (u0 == 0) put_head(p, tile, wg, (int)((unit + units - 1) / line.share - wg) + 1);
     const int row = min(row0 + 32 * wm + i, p.rows - 1);
     const int row_token = row / p.group;
     const int64_t token = (int64_t)seq * p.q_len + row_token;
@@ -665,7 +682,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
     // Starts the copy of unit u; its scales go through registers to the
     // wave's own table (put_scales), as floats.
     uint32_t key_scale = 0, value_scale = 0;
-    uint64_t bad = 0, bad_next = 0;  // bit 16 b for block b of the step if its page does not exist
+    uint64_t bad = 0, bad_next = 0;  // bit t for token t of the stage if its page does not exist
     auto copy = [&](int u, uint8_t* stage) __attribute__((always_inline)) {
       const Where w = where(step_of(u));
       uint8_t* const region = stage + wt * (2 * C::kHalf) + wm * PW * 1024;
@@ -685,7 +702,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       const uint64_t at = row_of(pages[2 * NT], a.c.ld_scales) + (uint32_t)(slot_of(block_of(w, scale_token >> 4)) + (lane & 15));
       key_scale = a.c.ks[at];
       value_scale = a.c.vs[at];
-      bad_next = __ballot((unsigned)pages[2 * NT] >= (unsigned)a.c.n_pages) & (~0ull >> (64 - C::kStepTokens));
+      bad_next = __ballot((unsigned)pages[2 * NT] >= (unsigned)a.c.n_pages);
     };
     float* const key_scales = lds.scales[wave][0];
     float* const value_scales = lds.scales[wave][1];
@@ -695,15 +712,20 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       bad = bad_next;
     };
 
-    // One step. The fragments are read kAhead before their use and the order
-    // is pinned (sched_barrier): left alone, the compiler reads each
-    // right before its conversion and waits for it.
+    // One step.  The fragments (keys, then values) are read kAhead before
+    // their use and converted one ahead, and the order is pinned
+    // (sched_barrier): left alone, the compiler reads each right before its
+    // conversion and converts it right before its product, and the wave waits
+    // for both.
     constexpr int kAhead = D == 256 ? 2 : 3, F = TT * D32;
     auto step = [&](int u, uint8_t* stage) __attribute__((always_inline)) {
       const int s = u * C::kWT + wt;
       const Where w = where(min(s, steps - 1));
-      const int row_sees = s >= steps ? 0 : s < prefix_steps ? w.n : limit;  // tokens of the list before this row's first unseen one
-      const bool masked = bad != 0 || s >= steps || w.base + C::kStepTokens > (s < prefix_steps ? w.n : limit_first);
+      const int held = s >= steps ? 0 : w.n;  // tokens of the list that any row sees
+      const int row_sees = s >= steps ? 0 : s < prefix_steps ? w.n : limit;
+      const int all_see = s >= steps ? 0 : s < prefix_steps ? w.n : limit_first;
+      const int base = w.base;
+      const bool masked = bad != 0 || base + C::kStepTokens > all_see;
       uint8_t* const keys = stage + wt * (2 * C::kHalf) + lane * 16;
       uint8_t* const values = keys + C::kHalf;
 
@@ -712,12 +734,10 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
         // their scales infinite (0 * NaN): clear them.  The waves of a region
         // write the same zeros, each before it reads.
         asm volatile("");  // a real branch: the steps that take it are few
-        const int held = s >= steps ? 0 : w.n;
-        const bool there = w.base + scale_token < held && !(bad >> (scale_token & 48) & 1u);
-        if (!there) value_scales[lane] = 0.0f;
+        if (lane < 32 * TT && (base + lane >= held || (bad >> lane & 1u))) value_scales[lane] = 0.0f;
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const int holds = (bad >> (16 * (2 * t + h)) & 1u) ? 0 : held - (w.base + 32 * t + 16 * h);
+          const int holds = (bad >> (32 * t + 16 * h) & 1u) ? 0 : held - (base + 32 * t + 16 * h);
           uint32_t keep[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) keep[e] = keep_bytes(holds - 4 * e);
@@ -735,28 +755,40 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
         ks[t] = key_scales[32 * t + key_token];
         sc[t] = floatx16{};
       }
+      // The conversions of fragment f + 1 go between the two products of f.
+      auto key_at = [&](int f) { return *reinterpret_cast<const uint4*>(keys + ((f % TT) * D32 + f / TT) * 1024); };
+      auto value_at = [&](int f) { return *reinterpret_cast<const uint4*>(values + ((f % TT) * D32 + f / TT) * 1024); };
       uint4 fr[kAhead];
 #pragma unroll
-      for (int f = 0; f < kAhead; ++f) fr[f] = *reinterpret_cast<const uint4*>(keys + ((f % TT) * D32 + f / TT) * 1024);
+      for (int f = 0; f < kAhead; ++f) fr[f] = key_at(f);
+      bf16x8 c0 = decode8(fr[0].x, fr[0].y, ks[0]), c1 = decode8(fr[0].z, fr[0].w, ks[0]);
 #pragma unroll
       for (int f = 0; f < F; ++f) {  // tile f % TT, dimensions 32 (f / TT) ..
         const int t = f % TT, j = f / TT;
-        const uint4 q = fr[f % kAhead];
-        const bf16x8 k0 = decode8(q.x, q.y, ks[t]), k1 = decode8(q.z, q.w, ks[t]);
-        if (f + kAhead < F)
-          fr[f % kAhead] = *reinterpret_cast<const uint4*>(keys + (((f + kAhead) % TT) * D32 + (f + kAhead) / TT) * 1024);
-        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, query(2 * j), sc[t], 0, 0, 0);
-        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, query(2 * j + 1), sc[t], 0, 0, 0);
+        fr[f % kAhead] = f + kAhead < F ? key_at(f + kAhead) : value_at(f + kAhead - F);
+        const uint4 q = fr[(f + 1) % kAhead];
+        const float kn = f + 1 < F ? ks[(f + 1) % TT] : 1.0f;
+        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, query(2 * j), sc[t], 0, 0, 0);
+        const bf16x8 n0 = decode8(q.x, q.y, kn);
         __builtin_amdgcn_sched_barrier(0);
+        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, query(2 * j + 1), sc[t], 0, 0, 0);
+        const bf16x8 n1 = decode8(q.z, q.w, kn);
+        __builtin_amdgcn_sched_barrier(0);
+        c0 = n0;
+        c1 = n1;
       }
+      f32x4 vs[TT][4];
 #pragma unroll
-      for (int f = 0; f < kAhead; ++f) fr[f] = *reinterpret_cast<const uint4*>(values + ((f % TT) * D32 + f / TT) * 1024);
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vs[t][r] = *reinterpret_cast<const f32x4*>(value_scales + 32 * t + 16 * h + 4 * r);
+      __builtin_amdgcn_sched_barrier(0);
 
       if (masked) {
         asm volatile("");
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const int sees = (bad >> (16 * (2 * t + h)) & 1u) ? 0 : row_sees - (w.base + 32 * t + 16 * h);
+          const int sees = (bad >> (32 * t + 16 * h) & 1u) ? 0 : row_sees - (base + 32 * t + 16 * h);
 #pragma unroll
           for (int r = 0; r < 16; ++r) sc[t][r] = r < sees ? sc[t][r] : -__builtin_inff();
         }
@@ -786,11 +818,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
           l += e[r];
         }
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const f32x4 vs = *reinterpret_cast<const f32x4*>(value_scales + 32 * t + 16 * h + r);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) e[r + b] *= vs[b];
-        }
+        for (int r = 0; r < 16; ++r) e[r] *= vs[t][r >> 2][r & 3];
         pf[t][0] = take_term(e);
         pf[t][1] = take_term(e + 8);
       }
@@ -798,13 +826,16 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int t = f % TT, d = f / TT;
-        const uint4 v = fr[f % kAhead];
-        const bf16x8 v0 = decode8(v.x, v.y, 1.0f), v1 = decode8(v.z, v.w, 1.0f);
-        if (f + kAhead < F)
-          fr[f % kAhead] = *reinterpret_cast<const uint4*>(values + (((f + kAhead) % TT) * D32 + (f + kAhead) / TT) * 1024);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, pf[t][0], o[d], 0, 0, 0);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, pf[t][1], o[d], 0, 0, 0);
+        if (f + kAhead < F) fr[(f + F) % kAhead] = value_at(f + kAhead);
+        const uint4 v = fr[(f + 1 + F) % kAhead];
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, pf[t][0], o[d], 0, 0, 0);
+        const bf16x8 n0 = f + 1 < F ? decode8(v.x, v.y, 1.0f) : c0;
         __builtin_amdgcn_sched_barrier(0);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, pf[t][1], o[d], 0, 0, 0);
+        const bf16x8 n1 = f + 1 < F ? decode8(v.z, v.w, 1.0f) : c1;
+        __builtin_amdgcn_sched_barrier(0);
+        c0 = n0;
+        c1 = n1;
       }
     };
 
@@ -813,41 +844,30 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
     // stage that is overwritten (the barrier).
     if (u0 < u_end) {
       load_pages(u0);
-      copy(u0, stage_a);
+      copy(u0, stages + (u0 & 1) * C::kStageBytes);
       load_pages(u0 + 1);
-      for (int u = u0; u < u_end; u += 2) {
+      for (int u = u0; u < u_end; ++u) {
         wait_vmem<0>();
         put_scales();
         barrier_lds();
-        copy(u + 1, stage_b);
+        copy(u + 1, stages + (~u & 1) * C::kStageBytes);
         load_pages(u + 2);
-        step(u, stage_a);
-        if (u + 1 >= u_end) break;
-        wait_vmem<0>();
-        put_scales();
-        barrier_lds();
-        copy(u + 2, stage_a);
-        load_pages(u + 3);
-        step(u + 1, stage_b);
+        step(u, stages + (u & 1) * C::kStageBytes);
       }
       wait_vmem<0>();  // copies past the last unit
     }
 
     // Join the regions: waves of wt > 0 hand theirs to the wave of wt = 0
-    // with the same rows (register by register; half in each stage array).
+    // with the same rows (register by register).
     l += __shfl_xor(l, 32);
     barrier_lds();
     constexpr int kOut = D32 * 16;  // accumulator registers
     if constexpr (C::kWT > 1) {
-      float* const half_a = reinterpret_cast<float*>(stage_a);
-      float* const half_b = reinterpret_cast<float*>(stage_b);
+      float* const given = reinterpret_cast<float*>(stages);
       if (wt > 0) {
-        const int at = ((wt - 1) * WM + wm) * (kOut / 2) * 64 + lane;
+        const int at = ((wt - 1) * WM + wm) * kOut * 64 + lane;
 #pragma unroll
-        for (int r = 0; r < kOut / 2; ++r) {
-          half_a[at + r * 64] = o[r >> 4][r & 15];
-          half_b[at + r * 64] = o[(r + kOut / 2) >> 4][r & 15];
-        }
+        for (int r = 0; r < kOut; ++r) given[at + r * 64] = o[r >> 4][r & 15];
         if (h == 0) {
           lds.ml[wave][i][0] = m;
           lds.ml[wave][i][1] = l;
@@ -866,21 +886,18 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
         for (int w = 1; w < C::kWT; ++w) {
           const float f = __builtin_amdgcn_exp2f(lds.ml[w * WM + wm][i][0] - top);
           l += lds.ml[w * WM + wm][i][1] * f;
-          const int at = ((w - 1) * WM + wm) * (kOut / 2) * 64 + lane;
+          const int at = ((w - 1) * WM + wm) * kOut * 64 + lane;
 #pragma unroll
-          for (int r = 0; r < kOut / 2; ++r) {
-            o[r >> 4][r & 15] += half_a[at + r * 64] * f;
-            o[(r + kOut / 2) >> 4][r & 15] += half_b[at + r * 64] * f;
-          }
+          for (int r = 0; r < kOut; ++r) o[r >> 4][r & 15] += given[at + r * 64] * f;
         }
         m = top;
       }
     }
     const int r = 32 * wm + i;  // row of the tile
     if (wt == 0 && row0 + r < p.rows) {
-      const bool whole = p.direct && u0 == 0 && u1 == units;
+      const bool whole = p.direct && t.whole();
       if (!whole) {
-        const int64_t at = ((int64_t)tile + wg) * C::kRows + r;
+        const int64_t at = ((int64_t)tile + t.wg) * C::kRows + r;
         if (h == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
 #pragma unroll
         for (int d = 0; d < D32; ++d)
@@ -900,28 +917,353 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       }
     }
     barrier_lds();
-
-    unit += u1 - u0;
-    if (unit >= last_unit) break;
-    u0 = 0;
-    if (++x == tiles_per_seq) {
-      x = 0;
-      ++seq;
-      len = own_len(p, seq);
-      units = tile_units(p, len);
-    }
-  }
+  } while (t.next(p));
 }
 
 template <int D, int WM>
 __global__ __launch_bounds__(kThreads, WM == 1 ? 1 : 2) void kv_attention_rows_kernel(KvAttnArgs a, Pass p) {
   typedef RowsShape<D, WM> C;
-  __shared__ __attribute__((aligned(16))) uint8_t stage_a[C::kStageBytes], stage_b[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t stages[2 * C::kStageBytes];
   __shared__ __attribute__((aligned(16))) float scales[kWaves][2][kStep];
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[kWaves + 2];
   __shared__ uint4 q[C::kQueriesLds * kWaves * 64 + 1];
-  rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stage_a, stage_b, scales, ml, line, q});
+  rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stages, scales, ml, line, q});
+}
+
+// Tiles of 128 rows, D <= 128: the four waves own 32 each and all work on the same
+// tokens.  Here the conversion to bf16 would be made four times over, and the
+// instructions a wave issues are what bounds it, so each wave converts a
+// quarter of the step and the stage holds bf16: fragment (tile of 32 tokens,
+// 16 dimensions) of the keys, or (tile, 32 dimensions, half of a block's
+// tokens) of the values, 1 KB each, lane l's 8 values at 16 l.  The bytes go
+// through registers: asked for a step ahead, converted after the step's
+// products, one barrier a step.  (With D = 256 the accumulators and queries
+// take 192 of 256 registers and this form spills; it stays with rows_body.)
+template <int D>
+struct WideShape {
+  static constexpr int kTT = 2;                           // 32-token tiles of a step
+  static constexpr int kStepTokens = 32 * kTT;
+  static constexpr int kD32 = D / 32;
+  static constexpr int kPieces = kTT * kD32 / 4;          // raw KB of keys, and of values, of a wave
+  static constexpr int kHalf = kStepTokens * D * 2;       // bytes of a stage's keys, or values
+  static constexpr int kStageBytes = 2 * kHalf;
+  static constexpr int kRows = 128;
+  };
+
+struct WideLds {
+  uint8_t* stages;          // 2 * kStageBytes
+  float (*scales)[kStep];   // values' scales of each stage
+  uint64_t* bad;            // of each stage: bit t for token t if its page does not exist
+  int64_t* line;
+};
+
+template <int D>
+__device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs& a, const Pass& p, const int wg, const WideLds& lds) {
+  typedef WideShape<D> C;
+  static_assert(D <= 128, "no registers for wider heads");
+  constexpr int TT = C::kTT, D32 = C::kD32, PW = C::kPieces, ST = C::kStepTokens;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 31, h = lane >> 5;
+  const int prefix_steps = ceil_div(p.prefix_len, ST);
+  const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
+
+  // What this lane converts (see rows_body): PW pieces of one 32-token tile.
+  const int my_tile = wave * PW / D32, my_col = wave * PW % D32;
+  const int kh = (lane >> 2) & 1, key_row = 4 * (i >> 3) + (i & 3);  // block of the tile, token of the block
+  const int key_src = (i >> 3) * (4 * D) + h * 64 + (lane & 3) * 16 + my_col * 128;
+  const int value_src = i * 16 + my_col * 512;
+  const int scale_token = lane & (ST - 1);
+
+  Walk t(a, p, wg, lds.line);
+  if (!t.any) return;
+  do {
+    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
+    const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * C::kRows;
+    const int row = min(row0 + 32 * wave + i, p.rows - 1);
+    const int row_token = row / p.group;
+    const int64_t token = (int64_t)seq * p.q_len + row_token;
+    const int limit = len - p.q_len + 1 + row_token;  // first own token that this row does not see
+    const int limit_first = len - p.q_len + 1 + min(row0 + 32 * wave, p.rows - 1) / p.group;
+    const int limit_last = len - p.q_len + 1 + (min(row0 + C::kRows, p.rows) - 1) / p.group;
+    const int steps = prefix_steps + ceil_div(max(limit_last, 0), ST);  // with a visible token
+    const int u_end = min(u1, steps);
+
+    bf16x8 qf[2 * D32];
+    {
+      const int64_t at = token * a.ld_q + (int64_t)(kvh * p.group + row - row_token * p.group) * D + h * 16;
+#pragma unroll
+      for (int j = 0; j < 2 * D32; ++j)
+        qf[j] = *reinterpret_cast<const bf16x8*>((const uint16_t*)a.q + at + (j >> 1) * 32 + 8 * (j & 1));
+    }
+
+    float m = kLowest, l = 0.0f;
+    floatx16 o[D32];
+#pragma unroll
+    for (int d = 0; d < D32; ++d) o[d] = floatx16{};
+
+    struct Where {
+      const int* list;
+      int base, n;
+    };
+    auto where = [&](int u) __attribute__((always_inline)) {
+      const int s = min(u, steps - 1);
+      if (s < prefix_steps) return Where{a.prefix_pages, s * ST, p.prefix_len};
+      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * ST, limit_last};
+    };
+    auto block_of = [&](const Where& w, int b) { return min((w.base >> 4) + b, (w.n - 1) >> 4); };
+    auto slot_of = [&](int blk) { return (kvh << a.c.page_shift) + (blk & page_blocks_mask) * 16; };
+    auto row_of = [&](int id, int64_t ld) {
+      return (uint64_t)((unsigned)id < (unsigned)a.c.n_pages ? (unsigned)id : 0u) * (uint64_t)(uint32_t)ld;
+    };
+
+    int key_page = 0, value_page = 0;
+    auto load_pages = [&](const Where& w) __attribute__((always_inline)) {
+      key_page = w.list[block_of(w, 2 * my_tile + kh) >> page_blocks_shift];
+      value_page = w.list[block_of(w, 2 * my_tile + h) >> page_blocks_shift];
+    };
+    uint4 kraw[PW], vraw[PW];
+    uint32_t kscale = 0;
+    bool value_gone = false;
+    // A step's loads in four parts (see step()).
+    constexpr int kLoadParts = 4;
+    const uint8_t* src = nullptr;
+    auto load_part = [&](const Where& w, int part) __attribute__((always_inline)) {
+      const int kat = slot_of(block_of(w, 2 * my_tile + kh));
+      if (part == 0) {
+        src = a.c.kc + row_of(key_page, a.c.ld_codes) + (uint32_t)(kat * D + key_src);
+#pragma unroll
+        for (int k = 0; k < PW; ++k) kraw[k] = *reinterpret_cast<const uint4*>(src + k * 128);
+      } else if (part == 1) {
+        src = a.c.vc + row_of(value_page, a.c.ld_codes) + (uint32_t)(slot_of(block_of(w, 2 * my_tile + h)) * D + value_src);
+#pragma unroll
+        for (int k = 0; k < PW; ++k) vraw[k] = *reinterpret_cast<const uint4*>(src + k * 512);
+      } else if (part == 2) {
+        kscale = a.c.ks[row_of(key_page, a.c.ld_scales) + (uint32_t)(kat + key_row)];
+      } else {
+        value_gone = (unsigned)value_page >= (unsigned)a.c.n_pages;
+      }
+    };
+    auto load = [&](const Where& w) __attribute__((always_inline)) {
+#pragma unroll
+      for (int part = 0; part < kLoadParts; ++part) load_part(w, part);
+    };
+    const int to_frag = (my_tile * D32 + my_col) * 2048 + lane * 16;
+    constexpr int kPutParts = 4 * PW;
+    auto put_part = [&](int stage, int part) __attribute__((always_inline)) {
+      uint8_t* const to = lds.stages + stage * C::kStageBytes + to_frag + part / 2 % PW * 2048 + (part & 1) * 1024;
+      const uint4 q = part < 2 * PW ? kraw[part / 2 % PW] : vraw[part / 2 % PW];
+      const uint32_t lo = part & 1 ? q.z : q.x, hi = part & 1 ? q.w : q.y;
+      if (part < 2 * PW) *reinterpret_cast<bf16x8*>(to) = decode8(lo, hi, __uint_as_float(kscale << 23));
+      else *reinterpret_cast<bf16x8*>(to + C::kHalf) = decode8(lo, hi, 1.0f);
+    };
+    auto put = [&](int stage) __attribute__((always_inline)) {
+#pragma unroll
+      for (int part = 0; part < kPutParts; ++part) put_part(stage, part);
+    };
+    // Bytes that hold no token that any row sees may be NaN codes, and their
+    // scales infinite (0 * NaN): zeros instead.
+    auto clear = [&](const Where& w, int stage) __attribute__((always_inline)) {
+      if (w.base + ST > w.n || __any(value_gone)) {
+        uint8_t* const to = lds.stages + stage * C::kStageBytes + C::kHalf + to_frag;
+        const int holds = value_gone ? 0 : w.n - (w.base + 32 * my_tile + 16 * h);
+#pragma unroll
+        for (int k = 0; k < PW; ++k) {
+          const uint4 v = make_uint4(vraw[k].x & keep_bytes(holds), vraw[k].y & keep_bytes(holds - 4),
+                                     vraw[k].z & keep_bytes(holds - 8), vraw[k].w & keep_bytes(holds - 12));
+          *reinterpret_cast<bf16x8*>(to + k * 2048) = decode8(v.x, v.y, 1.0f);
+          *reinterpret_cast<bf16x8*>(to + k * 2048 + 1024) = decode8(v.z, v.w, 1.0f);
+        }
+      }
+    };
+    // The values' scales, by wave 0, another step ahead: lane t's token t.
+    int scale_page = 0;
+    uint32_t vscale = 0;
+    uint64_t gone = 0;
+    auto load_scale_page = [&](const Where& w) __attribute__((always_inline)) {
+      scale_page = w.list[block_of(w, scale_token >> 4) >> page_blocks_shift];
+    };
+    auto load_scales = [&](const Where& w) __attribute__((always_inline)) {
+      vscale = a.c.vs[row_of(scale_page, a.c.ld_scales) + (uint32_t)(slot_of(block_of(w, scale_token >> 4)) + (lane & 15))];
+      gone = __ballot((unsigned)scale_page >= (unsigned)a.c.n_pages);
+    };
+    auto put_scales = [&](const Where& w, int stage) __attribute__((always_inline)) {
+      const bool none = w.base + scale_token >= w.n || (gone >> scale_token & 1u);
+      lds.scales[stage][lane] = none ? 0.0f : __uint_as_float(vscale << 23);
+      if (lane == 0) lds.bad[stage] = gone;
+    };
+
+    // One step, with the next one's bytes asked for and converted inside.  A
+    // wave issues one instruction in about 5 cycles and a product occupies
+    // the matrix unit for 32, so after each product come a few other
+    // instructions: the next step's addresses and loads in the first half,
+    // the softmax of the second tile and the conversions in the second.
+    // sched_barrier pins that order (and the fragments' reads, kAhead
+    // before their product); the compiler's own bunches products and reads.
+    // The parts with products run at raised priority: without it the older of
+    // two waves on a SIMD always wins, finishes its share early and leaves the
+    // other alone (at equal shares of 75 units 155 and 205 us, now 160 and
+    // 184).
+    constexpr int kAhead = 4, F = 2 * TT * D32, FT = 2 * D32;
+    auto step = [&](const Where& w, bool prefix, int stage, const Where& next, const Where& after) __attribute__((always_inline)) {
+      const uint8_t* const keys = lds.stages + stage * C::kStageBytes + lane * 16;
+      const uint8_t* const values = keys + C::kHalf;
+      const float* const scales = lds.scales[stage];
+      // key product f: tile f / 2 % TT, 16 dimensions; value product f: tile
+      // f / FT, 32 dimensions and half the tokens
+      auto key_at = [&](int f) {
+        return *reinterpret_cast<const bf16x8*>(keys + ((f / 2 % TT) * D32 + f / (2 * TT)) * 2048 + (f & 1) * 1024);
+      };
+      auto value_at = [&](int f) { return *reinterpret_cast<const bf16x8*>(values + f * 1024); };
+      floatx16 sc[TT];
+#pragma unroll
+      for (int k = 0; k < TT; ++k) sc[k] = floatx16{};
+      bf16x8 fr[kAhead];
+#pragma unroll
+      for (int f = 0; f < kAhead; ++f) fr[f] = key_at(f);
+      const uint64_t bad64 = lds.bad[stage];
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const bf16x8 k = fr[f % kAhead];
+        sc[f / 2 % TT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[2 * (f / (2 * TT)) + (f & 1)], sc[f / 2 % TT], 0, 0, 0);
+        fr[f % kAhead] = f + kAhead < F ? key_at(f + kAhead) : value_at(f + kAhead - F);
+        if (f < kLoadParts) load_part(next, f);
+        if (f == kLoadParts) load_pages(after);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      f32x4 vs[TT][4];
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vs[k][r] = *reinterpret_cast<const f32x4*>(scales + 32 * k + 16 * h + 4 * r);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(0);
+
+      const uint32_t bad_lo = __builtin_amdgcn_readfirstlane((uint32_t)bad64), bad_hi = __builtin_amdgcn_readfirstlane((uint32_t)(bad64 >> 32));
+      if ((bad_lo | bad_hi) != 0 || w.base + ST > (prefix ? w.n : limit_first)) {
+        asm volatile("");
+#pragma unroll
+        for (int k = 0; k < TT; ++k) {
+          const int sees = ((k ? bad_hi : bad_lo) >> (16 * h) & 1u) ? 0 : (prefix ? w.n : limit) - (w.base + 32 * k + 16 * h);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sc[k][r] = r < sees ? sc[k][r] : -__builtin_inff();
+        }
+      }
+
+      float top = kLowest;
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float mn = fmaxf(m, top * a.scale_log2);
+      if (__any(mn > m)) {
+        const float f = __builtin_amdgcn_exp2f(m - mn);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < D32; ++d) o[d] *= f;
+        m = mn;
+      }
+      uint32_t pf[TT][8];  // pairs of weights as bf16
+      auto weight_pair = [&](int k, int r) __attribute__((always_inline)) {
+        const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[k][r], a.scale_log2, -m));
+        const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[k][r + 1], a.scale_log2, -m));
+        l += e0;
+        l += e1;
+        pf[k][r >> 1] = pack_bf16x2(e0 * vs[k][r >> 2][r & 3], e1 * vs[k][r >> 2][(r & 3) + 1]);
+      };
+      auto weights = [&](int k, int half) __attribute__((always_inline)) {
+        return __builtin_bit_cast(bf16x8, u32x4{pf[k][4 * half], pf[k][4 * half + 1], pf[k][4 * half + 2], pf[k][4 * half + 3]});
+      };
+      auto product = [&](int f) __attribute__((always_inline)) {
+        const bf16x8 v = fr[(f + F) % kAhead];
+        o[f % FT / 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, weights(f / FT, f & 1), o[f % FT / 2], 0, 0, 0);
+        if (f + kAhead < F) fr[(f + F) % kAhead] = value_at(f + kAhead);
+      };
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) weight_pair(0, r);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int f = 0; f < FT; ++f) {
+        product(f);
+#pragma unroll
+        for (int r = 0; r < 16 / FT; r += 2) weight_pair(1, f * (16 / FT) + r);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int f = 0; f < FT; ++f) {
+        product((TT - 1) * FT + f);
+        if (f >= FT - kPutParts) put_part(stage ^ 1, f - (FT - kPutParts));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      clear(next, stage ^ 1);
+      if (wave == 0) put_scales(next, stage ^ 1);
+    };
+
+    if (u0 < u_end) {
+      Where w = where(u0), next = where(u0 + 1);
+      load_pages(w);
+      load(w);
+      load_pages(next);
+      if (wave == 0) {
+        load_scale_page(w);
+        load_scales(w);
+        put_scales(w, u0 & 1);
+        load_scale_page(next);
+        load_scales(next);
+        load_scale_page(where(u0 + 2));
+      }
+      put(u0 & 1);
+      clear(w, u0 & 1);
+      barrier_lds();
+      for (int u = u0; u < u_end; ++u) {
+        const Where after = where(u + 2);
+        step(w, u < prefix_steps, u & 1, next, after);
+        if (wave == 0) {
+          load_scales(after);
+          load_scale_page(where(u + 3));
+        }
+        w = next;
+        next = after;
+        barrier_lds();  // the other stage is full, and no wave reads this one any more
+      }
+    }
+
+    l += __shfl_xor(l, 32);
+    const int r = 32 * wave + i;  // row of the tile
+    if (row0 + r < p.rows) {
+      if (!(p.direct && t.whole())) {
+        const int64_t at = ((int64_t)tile + t.wg) * C::kRows + r;
+        if (h == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
+#pragma unroll
+        for (int d = 0; d < D32; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<f32x4*>(p.o + at * D + 32 * d + 8 * e + 4 * h) =
+                f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+      } else if (len >= 0) {
+        const float inv = inverse_sum(l);
+#pragma unroll
+        for (int d = 0; d < D32; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v[4] = {o[d][4 * e] * inv, o[d][4 * e + 1] * inv, o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv};
+            store_out4<NVFP4_DTYPE_BF16>(a, (int)token, kvh * p.group + row - row_token * p.group, 32 * d + 8 * e + 4 * h, v);
+          }
+      }
+    }
+  } while (t.next(p));
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnArgs a, Pass p) {
+  typedef WideShape<D> C;
+  __shared__ __attribute__((aligned(16))) uint8_t stages[2 * C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) float scales[2][kStep];
+  __shared__ uint64_t bad[2];
+  __shared__ int64_t line[kWaves + 2];
+  wide_body<D>(a, p, blockIdx.x, WideLds{stages, scales, bad, line});
 }
 
 // The shared prefix and the sequences' own tokens in one launch: the first is
@@ -935,12 +1277,13 @@ constexpr int kSlots = 512;  // two workgroups on each of 256 CUs
 
 template <int DT, int D, int WM>
 __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_attention_both_kernel(KvAttnArgs a, Pass shared, Pass own) {
-  constexpr int kStage = WM == 0 ? 0 : RowsShape<D, WM == 0 ? 4 : WM>::kStageBytes;
+  constexpr bool kWide = WM == 4 && D <= 128;
+  constexpr int kStage = WM == 0 ? 0 : kWide ? WideShape<D>::kStageBytes : RowsShape<D, WM == 0 ? 2 : WM>::kStageBytes;
   constexpr int kPart = 16 * D * (int)sizeof(float);
-  constexpr int kBytes = kStage > kPart ? kStage : kPart;
-  __shared__ __attribute__((aligned(16))) uint8_t stage_a[kBytes], stage_b[kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t stages[2 * (kStage > kPart ? kStage : kPart)];
   __shared__ __attribute__((aligned(16))) float scales[kWaves][2][kStep];
-  constexpr int kStreamQ = kTerms<DT> * (D / 32) * 64, kRowsQ = WM == 0 ? 0 : RowsShape<D, WM == 0 ? 4 : WM>::kQueriesLds * kWaves * 64;
+  __shared__ uint64_t bad[2];
+  constexpr int kStreamQ = kTerms<DT> * (D / 32) * 64, kRowsQ = WM == 0 || kWide ? 0 : RowsShape<D, WM == 0 ? 2 : WM>::kQueriesLds * kWaves * 64;
   __shared__ uint4 q[kStreamQ > kRowsQ ? kStreamQ : kRowsQ];
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[kWaves + 2];
@@ -955,13 +1298,15 @@ __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_a
     first = false;
     wg = b - n;
   }
-  const StreamLds<DT, D> stream{(float*)stage_a, (float*)stage_b, q, ml, line};
+  const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), q, ml, line};
   if (!first) {
     stream_body<DT, D, DT == NVFP4_DTYPE_BF16>(a, own, wg, stream);
   } else if constexpr (WM == 0) {
     stream_body<DT, D, DT == NVFP4_DTYPE_BF16>(a, shared, wg, stream);
+  } else if constexpr (kWide) {
+    wide_body<D>(a, shared, wg, WideLds{stages, scales[0], bad, line});
   } else {
-    rows_body<D, WM>(a, shared, wg, RowsLds{stage_a, stage_b, scales, ml, line, q});
+    rows_body<D, WM>(a, shared, wg, RowsLds{stages, scales, ml, line, q});
   }
 }
 
@@ -1183,6 +1528,7 @@ hipError_t launch_pass(const KvAttnArgs& a, const Pass& p, hipStream_t s) {
   } else if constexpr (DT == NVFP4_DTYPE_BF16) {
     if (p.tile_rows == 32) kv_attention_rows_kernel<D, 1><<<p.workgroups, kThreads, 0, s>>>(a, p);
     else if (p.tile_rows == 64) kv_attention_rows_kernel<D, 2><<<p.workgroups, kThreads, 0, s>>>(a, p);
+    else if constexpr (D <= 128) kv_attention_wide_kernel<D><<<p.workgroups, kThreads, 0, s>>>(a, p);
     else kv_attention_rows_kernel<D, 4><<<p.workgroups, kThreads, 0, s>>>(a, p);
   }
   return hipGetLastError();
