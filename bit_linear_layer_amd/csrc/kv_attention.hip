@@ -65,6 +65,7 @@ struct Pass {
   const int* lens;  // null: no tokens of the sequences' own
   int max_len;
   int workgroups;
+  int solo;       // a share is a wave's, not a workgroup's (16-row tiles, step_waves 1)
   int direct;     // every tile is whole in one workgroup and nothing joins it: write the output
   float* ml;      // partials: [slot][tile_rows][2] and [slot][tile_rows][D]
   float* o;
@@ -76,6 +77,7 @@ __device__ __host__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; 
 __device__ inline int own_len(const Pass& p, int b) {
   return p.lens == nullptr ? 0 : max(min(p.lens[b], p.max_len), -1);
 }
+__device__ __host__ inline int pass_shares(const Pass& p) { return p.solo ? p.workgroups * kWaves : p.workgroups; }
 __device__ inline int tile_units(const Pass& p, int len) {
   const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(max(len, 0), p.step);
   return max(1, ceil_div(steps, p.step_waves));  // a tile without tokens is one empty unit
@@ -86,7 +88,7 @@ __device__ inline int tile_units(const Pass& p, int len) {
 struct Line {
   int64_t total;       // units of all sequences, one tile each
   int64_t share;       // units of a workgroup, all tiles counted
-  int64_t* scratch;    // LDS, kWaves + 2
+  int64_t* scratch;    // LDS, 2 * kWaves
   int per;
   int64_t before;      // units before this thread's sequences
   __device__ Line(const Pass& p, int tiles_per_seq, int64_t* scratch_) : scratch(scratch_) {
@@ -110,41 +112,40 @@ struct Line {
       total += scratch[w];
     }
     const int64_t all = total * tiles_per_seq;
-    share = (all + p.workgroups - 1) / p.workgroups;
+    const int n = pass_shares(p);
+    share = (all + n - 1) / n;
   }
-  // The sequence that holds position v of the line, and the units before it.
+  // The sequence that holds position v of the line, and the units before it;
+  // in a solo pass each wave asks for its own v.
   __device__ void find(const Pass& p, int64_t v, int* seq, int64_t* seq_before) {
+    const int b0 = threadIdx.x * per, wave = threadIdx.x >> 6, n = p.solo ? kWaves : 1;
+    __syncthreads();  // the scan's sums are read
+    if ((threadIdx.x & 63) == 0 && wave < n) scratch[wave] = v;
+    __syncthreads();
+    int64_t want[kWaves];
+    for (int w = 0; w < kWaves; ++w) want[w] = scratch[min(w, n - 1)];
+    __syncthreads();
     int64_t at = before;
-    const int b0 = threadIdx.x * per;
     for (int b = b0; b < min(b0 + per, p.batch); ++b) {
       const int u = tile_units(p, own_len(p, b));
-      if (v >= at && v < at + u) {
-        scratch[kWaves] = b;
-        scratch[kWaves + 1] = at;
-      }
+      for (int w = 0; w < n; ++w)
+        if (want[w] >= at && want[w] < at + u) {
+          scratch[2 * w] = b;
+          scratch[2 * w + 1] = at;
+        }
       at += u;
     }
     __syncthreads();
-    *seq = (int)scratch[kWaves];
-    *seq_before = scratch[kWaves + 1];
+    const int mine = min(wave, n - 1);
+    *seq = (int)scratch[2 * mine];
+    *seq_before = scratch[2 * mine + 1];
     __syncthreads();
-  }
-  // The units before sequence b.
-  __device__ int64_t before_seq(const Pass& p, int b) {
-    const int b0 = threadIdx.x * per;
-    if (b >= b0 && b < b0 + per) {
-      int64_t at = before;
-      for (int i = b0; i < b; ++i) at += tile_units(p, own_len(p, i));
-      scratch[kWaves] = at;
-    }
-    __syncthreads();
-    const int64_t at = scratch[kWaves];
-    __syncthreads();
-    return at;
   }
 };
 
 // A workgroup's walk over its share: tile by tile, the units [u0, u1) of each.
+// SOLO: each wave walks a share of its own.
+template <bool SOLO>
 struct Walk {
   int wg;  // the share's number
   int64_t unit, last;
@@ -158,19 +159,23 @@ struct Walk {
   __device__ Walk(const KvAttnArgs& a, const Pass& p, int dealt, int64_t* scratch) {
     const int q = p.workgroups / 8, r = p.workgroups % 8, xcd = dealt % 8;
     wg = xcd * q + min(xcd, r) + dealt / 8;
+    if constexpr (SOLO) wg = wg * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     tiles_per_seq = a.c.heads * p.row_tiles;
     Line line(p, tiles_per_seq, scratch);
-    unit = (int64_t)wg * line.share;
-    last = min(unit + line.share, line.total * tiles_per_seq);
+    share = uniform(line.share);
+    unit = wg * share;
+    last = uniform(min(unit + share, line.total * tiles_per_seq));
     any = unit < last;
-    if (!any) return;
+    if (!SOLO && !any) return;
     int64_t before;
-    line.find(p, unit / tiles_per_seq, &seq, &before);
-    len = own_len(p, seq);
+    line.find(p, unit / tiles_per_seq, &seq, &before);  // (past the end nothing is found)
+    if (!any) return;
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    before = uniform(before);
+    len = __builtin_amdgcn_readfirstlane(own_len(p, seq));
     units = tile_units(p, len);
     x = (int)((unit - before * tiles_per_seq) / units);
     u0 = (int)(unit - before * tiles_per_seq - (int64_t)x * units);
-    share = line.share;
     place(p);
   }
   __device__ bool next(const Pass& p) {
@@ -180,7 +185,7 @@ struct Walk {
     if (++x == tiles_per_seq) {
       x = 0;
       ++seq;
-      len = own_len(p, seq);
+      len = __builtin_amdgcn_readfirstlane(own_len(p, seq));
       units = tile_units(p, len);
     }
     place(p);
@@ -191,11 +196,15 @@ struct Walk {
 
  private:
   int64_t share;
+  // A value that all lanes hold, in scalar registers.
+  static __device__ int64_t uniform(int64_t v) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) | (int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
+  }
   __device__ void place(const Pass& p) {
     u1 = (int)min((int64_t)units, u0 + (last - unit));
     tile = seq * tiles_per_seq + x;
     // the join wants to know: the workgroup of unit 0 and the number of pieces
-    if (p.head != nullptr && u0 == 0 && threadIdx.x == 0)
+    if (p.head != nullptr && u0 == 0 && (threadIdx.x & (SOLO ? 63 : kThreads - 1)) == 0)
       p.head[tile] = make_int2(wg, (int)((unit + units - 1) / share - wg) + 1);
   }
 };
@@ -260,16 +269,20 @@ constexpr int kTerms = DT == NVFP4_DTYPE_BF16 ? 1 : 3;
 template <int DT, int D>
 struct StreamLds {
   float *part_a, *part_b;  // a wave's accumulators each: 16 * D
-  uint4* q;                // [kTerms][D / 32][64]
+  uint4* q;                // [kTerms][D / 32][64], SOLO: for each wave
   float (*ml)[32][2];
   int64_t* line;
 };
 
 // PAIR: two workgroups share a CU, i.e. 256 registers a wave.
-template <int DT, int D, bool PAIR>
+// SOLO: each wave has tiles of its own, from its queries to its result: for
+// many short tiles, where four waves to a tile would mostly wait for each
+// other and for the hand-over of their sums.
+template <int DT, int D, bool PAIR, bool SOLO>
 __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnArgs& a, const Pass& p, const int wg,
                                                                   const StreamLds<DT, D>& lds) {
   constexpr int T = kTerms<DT>;
+  constexpr int SW = SOLO ? 1 : kWaves;  // waves that share a tile
   constexpr int KJ = D / 64;   // 16-byte pieces of a token that a lane holds
   constexpr int DT16 = D / 16; // output tiles of 16 dimensions
 
@@ -278,7 +291,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
   const int prefix_steps = ceil_div(p.prefix_len, kStep);
   const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
 
-  Walk t(a, p, wg, lds.line);
+  Walk<SOLO> t(a, p, wg, lds.line);
   if (!t.any) return;
   do {
     const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
@@ -294,16 +307,17 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
     const int limit_first = len - p.q_len + 1 + row0 / p.group, limit_last = len - p.q_len + 1 + tile_last / p.group;
 
     const int head = kvh * p.group + row - row_token * p.group;
-    for (int j = wave; j < 2 * KJ; j += kWaves) {
+    uint4* const queries = SOLO ? lds.q + wave * (T * 2 * KJ * 64) : lds.q;
+    for (int j = SOLO ? 0 : wave; j < 2 * KJ; j += SOLO ? 1 : kWaves) {
       const int64_t at = token * a.ld_q + (int64_t)head * D + (4 * (j >> 1) + g) * 16 + 8 * (j & 1);
       if constexpr (T == 1) {
-        lds.q[j * 64 + lane] = *reinterpret_cast<const uint4*>((const uint16_t*)a.q + at);
+        queries[j * 64 + lane] = *reinterpret_cast<const uint4*>((const uint16_t*)a.q + at);
       } else {
         const float* s = (const float*)a.q + at;
         const float4 lo = *reinterpret_cast<const float4*>(s), hi = *reinterpret_cast<const float4*>(s + 4);
         float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int t = 0; t < T; ++t) lds.q[(t * 2 * KJ + j) * 64 + lane] = __builtin_bit_cast(uint4, take_term(f));
+        for (int t = 0; t < T; ++t) queries[(t * 2 * KJ + j) * 64 + lane] = __builtin_bit_cast(uint4, take_term(f));
       }
     }
 
@@ -324,7 +338,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
     };
     // A wave's next step from s on that holds a visible token, or -1.
     auto next_step = [&](int s) {
-      const int end = min(u1 * kWaves, steps);
+      const int end = min(u1 * SW, steps);
       if (s >= end) return -1;
       if (s >= prefix_steps && (s - prefix_steps) * kStep >= limit_last) return -1;  // later ones neither
       return s;
@@ -359,18 +373,18 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       ksc = *reinterpret_cast<const uint4*>(a.c.ks + row_of(pk, a.c.ld_scales) + (uint32_t)at);
     };
 
-    int s = next_step(u0 * kWaves + wave);
+    int s = next_step(SOLO ? u0 : u0 * SW + wave);
     int pk = 0, pv = 0;
     if (s >= 0) {
       page_ids(s, pk, pv);
       load_keys(s, pk);
     }
-    __syncthreads();  // the queries are in LDS
+    if constexpr (!SOLO) __syncthreads();  // the queries are in LDS
     while (s >= 0) {
       const Where w = where(s);
       const bool prefix = s < prefix_steps;
       const bool bad = (unsigned)pv >= (unsigned)a.c.n_pages;
-      const int sn = next_step(s + kWaves);
+      const int sn = next_step(s + SW);
       int pkn = 0, pvn = 0;
       if (sn >= 0) page_ids(sn, pkn, pvn);
 
@@ -400,8 +414,8 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       for (int j = 0; j < KJ; ++j)
 #pragma unroll
         for (int e = T - 1; e >= 0; --e) {
-          const bf16x8 q0 = __builtin_bit_cast(bf16x8, lds.q[(e * 2 * KJ + 2 * j) * 64 + lane]);
-          const bf16x8 q1 = __builtin_bit_cast(bf16x8, lds.q[(e * 2 * KJ + 2 * j + 1) * 64 + lane]);
+          const bf16x8 q0 = __builtin_bit_cast(bf16x8, queries[(e * 2 * KJ + 2 * j) * 64 + lane]);
+          const bf16x8 q1 = __builtin_bit_cast(bf16x8, queries[(e * 2 * KJ + 2 * j + 1) * 64 + lane]);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(kq[t][j].x, kq[t][j].y, ks[t]), q0, sc[t], 0, 0, 0);
@@ -510,13 +524,15 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       for (int d = 0; d < DT16; ++d) o[d] = o[d] * f + *reinterpret_cast<const f32x4*>(from + (d * 64 + lane) * 4) * fo;
       m = mn;
     };
-    if (wave >= 2) give(wave == 2 ? lds.part_a : lds.part_b);
-    __syncthreads();
-    if (wave < 2) take(wave == 0 ? lds.part_a : lds.part_b, wave + 2);
-    if (wave == 1) give(lds.part_b);
-    __syncthreads();
-    if (wave == 0) {
-      take(lds.part_b, 1);
+    if constexpr (!SOLO) {
+      if (wave >= 2) give(wave == 2 ? lds.part_a : lds.part_b);
+      __syncthreads();
+      if (wave < 2) take(wave == 0 ? lds.part_a : lds.part_b, wave + 2);
+      if (wave == 1) give(lds.part_b);
+      __syncthreads();
+      if (wave == 0) take(lds.part_b, 1);
+    }
+    if (SOLO || wave == 0) {
       if (row0 + i < p.rows) {
         if (!(p.direct && t.whole())) {
           const int64_t at = ((int64_t)tile + t.wg) * kTileRows + i;
@@ -533,7 +549,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
         }
       }
     }
-    __syncthreads();  // the queries and the hand-over are read
+    if constexpr (!SOLO) __syncthreads();  // the queries and the hand-over are read
   } while (t.next(p));
 }
 
@@ -542,13 +558,13 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
 template <int DT, int D>
 constexpr bool kPaired = DT == NVFP4_DTYPE_BF16 && D < 256;
 
-template <int DT, int D>
+template <int DT, int D, bool SOLO>
 __global__ __launch_bounds__(kThreads, (kPaired<DT, D>) ? 2 : 1) void kv_attention_kernel(KvAttnArgs a, Pass p) {
   __shared__ __attribute__((aligned(16))) float part_a[16 * D], part_b[16 * D];
-  __shared__ uint4 q[kTerms<DT> * (D / 32) * 64];
+  __shared__ uint4 q[kTerms<DT> * (D / 32) * 64 * (SOLO ? kWaves : 1)];
   __shared__ float ml[kWaves][32][2];
-  __shared__ int64_t line[kWaves + 2];
-  stream_body<DT, D, kPaired<DT, D>>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line});
+  __shared__ int64_t line[2 * kWaves];
+  stream_body<DT, D, kPaired<DT, D>, SOLO>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line});
 }
 
 // The same for more rows (bf16): tiles of 32 * WM rows (WM = 1, 2; with D =
@@ -614,7 +630,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
   const int scale_token = lane & (C::kStepTokens - 1);
   const int key_token = 16 * kh + 4 * (i >> 3) + (i & 3);
 
-  Walk t(a, p, wg, lds.line);
+  Walk<false> t(a, p, wg, lds.line);
   if (!t.any) return;
   do {
     const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
@@ -926,7 +942,7 @@ __global__ __launch_bounds__(kThreads, WM == 1 ? 1 : 2) void kv_attention_rows_k
   __shared__ __attribute__((aligned(16))) uint8_t stages[2 * C::kStageBytes];
   __shared__ __attribute__((aligned(16))) float scales[kWaves][2][kStep];
   __shared__ float ml[kWaves][32][2];
-  __shared__ int64_t line[kWaves + 2];
+  __shared__ int64_t line[2 * kWaves];
   __shared__ uint4 q[C::kQueriesLds * kWaves * 64 + 1];
   rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stages, scales, ml, line, q});
 }
@@ -975,7 +991,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
   const int value_src = i * 16 + my_col * 512;
   const int scale_token = lane & (ST - 1);
 
-  Walk t(a, p, wg, lds.line);
+  Walk<false> t(a, p, wg, lds.line);
   if (!t.any) return;
   do {
     const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
@@ -1262,7 +1278,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
   __shared__ __attribute__((aligned(16))) uint8_t stages[2 * C::kStageBytes];
   __shared__ __attribute__((aligned(16))) float scales[2][kStep];
   __shared__ uint64_t bad[2];
-  __shared__ int64_t line[kWaves + 2];
+  __shared__ int64_t line[2 * kWaves];
   wide_body<D>(a, p, blockIdx.x, WideLds{stages, scales, bad, line});
 }
 
@@ -1275,18 +1291,19 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
 // become free.  WM = 0: 16-row tiles for the prefix as well.
 constexpr int kSlots = 512;  // two workgroups on each of 256 CUs
 
-template <int DT, int D, int WM>
+template <int DT, int D, int WM, bool SOLO>
 __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_attention_both_kernel(KvAttnArgs a, Pass shared, Pass own) {
   constexpr bool kWide = WM == 4 && D <= 128;
   constexpr int kStage = WM == 0 ? 0 : kWide ? WideShape<D>::kStageBytes : RowsShape<D, WM == 0 ? 2 : WM>::kStageBytes;
-  constexpr int kPart = 16 * D * (int)sizeof(float);
-  __shared__ __attribute__((aligned(16))) uint8_t stages[2 * (kStage > kPart ? kStage : kPart)];
+  constexpr int kPart = SOLO && WM != 0 ? 0 : 16 * D * (int)sizeof(float);  // a solo wave hands nothing over
+  constexpr int kStreamBytes = 2 * kPart + kTerms<DT> * (D / 32) * 1024 * (SOLO ? kWaves : 1);
+  constexpr int kRowsQ = WM == 0 || kWide ? 0 : RowsShape<D, WM == 0 ? 2 : WM>::kQueriesLds * kWaves * 64;
+  __shared__ __attribute__((aligned(16))) uint8_t stages[2 * kStage > kStreamBytes ? 2 * kStage : kStreamBytes];
   __shared__ __attribute__((aligned(16))) float scales[kWaves][2][kStep];
   __shared__ uint64_t bad[2];
-  constexpr int kStreamQ = kTerms<DT> * (D / 32) * 64, kRowsQ = WM == 0 || kWide ? 0 : RowsShape<D, WM == 0 ? 2 : WM>::kQueriesLds * kWaves * 64;
-  __shared__ uint4 q[kStreamQ > kRowsQ ? kStreamQ : kRowsQ];
+  __shared__ uint4 q[kRowsQ + 1];
   __shared__ float ml[kWaves][32][2];
-  __shared__ int64_t line[kWaves + 2];
+  __shared__ int64_t line[2 * kWaves];
   const int b = blockIdx.x, n = shared.workgroups;
   bool first = b < n;
   int wg = first ? b : b - n;
@@ -1298,11 +1315,11 @@ __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_a
     first = false;
     wg = b - n;
   }
-  const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), q, ml, line};
+  const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), (uint4*)(stages + 2 * kPart), ml, line};
   if (!first) {
-    stream_body<DT, D, DT == NVFP4_DTYPE_BF16>(a, own, wg, stream);
+    stream_body<DT, D, DT == NVFP4_DTYPE_BF16, SOLO>(a, own, wg, stream);
   } else if constexpr (WM == 0) {
-    stream_body<DT, D, DT == NVFP4_DTYPE_BF16>(a, shared, wg, stream);
+    stream_body<DT, D, DT == NVFP4_DTYPE_BF16, false>(a, shared, wg, stream);
   } else if constexpr (kWide) {
     wide_body<D>(a, shared, wg, WideLds{stages, scales[0], bad, line});
   } else {
@@ -1433,8 +1450,16 @@ struct Plan {
 int64_t pass_tiles(const KvAttnArgs& a, const Pass& p) { return (int64_t)p.batch * a.c.heads * p.row_tiles; }
 // Floats of a pass's part of the workspace: partials, and the tiles' heads.
 size_t pass_floats(const KvAttnArgs& a, const Pass& p) {
-  return (size_t)(pass_tiles(a, p) + p.workgroups) * p.tile_rows * (2 + a.c.dim) + (2 * (size_t)pass_tiles(a, p) + 3) / 4 * 4;
+  return (size_t)(pass_tiles(a, p) + pass_shares(p)) * p.tile_rows * (2 + a.c.dim) + (2 * (size_t)pass_tiles(a, p) + 3) / 4 * 4;
 }
+
+// Tiles from which on each is one wave's: half of the waves that the chip holds
+// (2 workgroups of 4 on 256 CUs).  Measured, a workgroup to a tile -> a wave,
+// 4 query rows, 128 dimensions: 1024 tiles of 1 to 512 tokens 24.1 -> 25.4 us,
+// after a prefix of 512 and of up to 1024 tokens 46.7 -> 43.8; 2048 tiles 38.9 -> 37.7, of 64 tokens
+// after a prefix of 256 41.5 -> 27.2; 1024 tiles of 64 dimensions and up to 300
+// tokens 18.5 -> 14.9; 2048 in float32 62 -> 46.
+constexpr int64_t kSoloTiles = 1024;
 
 // Tile shape and number of workgroups of a pass with its rows, prefix_len
 // and max_len set: 16-row tiles for up to stream_rows rows.
@@ -1453,9 +1478,13 @@ void shape_pass(const KvAttnArgs& a, Pass& p, int stream_rows) {
     per_cu = wm == 1 ? 1 : 2;
   }
   p.row_tiles = ceil_div(p.rows, p.tile_rows);
+  if (p.tile_rows == kTileRows && pass_tiles(a, p) >= kSoloTiles && p.batch > 1) {
+    p.solo = 1;
+    p.step_waves = 1;
+  }
   const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step);
   const int64_t units = pass_tiles(a, p) * max(1, ceil_div(steps, p.step_waves));
-  p.workgroups = (int)min(units, (int64_t)(256 * per_cu));
+  p.workgroups = (int)min((units + (p.solo ? kWaves - 1 : 0)) / (p.solo ? kWaves : 1), (int64_t)(256 * per_cu));
 }
 
 Plan make_plan(const KvAttnArgs& a) {
@@ -1489,13 +1518,13 @@ Plan make_plan(const KvAttnArgs& a) {
   if (share && own.tile_rows == kTileRows && pl.shared.workgroups + own.workgroups > kSlots) {
     // launch_both: the prefix's workgroups get their part of the places by
     // the time that both take.  Measured alone: a unit of a 64- or 128-row
-    // tile 3.0 us, one of a 16-row tile 7 us per 128 dimensions (two
-    // workgroups to a CU); the sequences are taken to be half of max_len.
+    // tile 2.6 us, one of a 16-row tile 7 us per 128 dimensions (two
+    // workgroups to a CU; 256 tokens, in a solo pass 64); the sequences are taken to be half of max_len.
     Pass& sh = pl.shared;
     auto units = [&](const Pass& p, int len) {
       return (double)pass_tiles(a, p) * max(1, ceil_div(ceil_div(p.prefix_len, p.step) + ceil_div(len, p.step), p.step_waves));
     };
-    const double narrow = 7.0 * a.c.dim / 128, ts = units(sh, 0) * (sh.tile_rows == kTileRows ? narrow : 3.0);
+    const double narrow = 7.0 * a.c.dim / 128 * (own.solo ? 0.25 : 1.0), ts = units(sh, 0) * (sh.tile_rows == kTileRows ? 7.0 * a.c.dim / 128 : 2.6);
     const double to = units(own, (own.max_len + 1) / 2) * narrow;
     const int n = (int)(kSlots * ts / (ts + to)) & ~7;
     sh.workgroups = min(max(n, 64), kSlots - 64);
@@ -1523,8 +1552,10 @@ void for_types(int dtype, int dim, F f) {
 
 template <int DT, int D>
 hipError_t launch_pass(const KvAttnArgs& a, const Pass& p, hipStream_t s) {
-  if (p.tile_rows == kTileRows) {
-    kv_attention_kernel<DT, D><<<p.workgroups, kThreads, 0, s>>>(a, p);
+  if (p.solo) {
+    kv_attention_kernel<DT, D, true><<<p.workgroups, kThreads, 0, s>>>(a, p);
+  } else if (p.tile_rows == kTileRows) {
+    kv_attention_kernel<DT, D, false><<<p.workgroups, kThreads, 0, s>>>(a, p);
   } else if constexpr (DT == NVFP4_DTYPE_BF16) {
     if (p.tile_rows == 32) kv_attention_rows_kernel<D, 1><<<p.workgroups, kThreads, 0, s>>>(a, p);
     else if (p.tile_rows == 64) kv_attention_rows_kernel<D, 2><<<p.workgroups, kThreads, 0, s>>>(a, p);
@@ -1535,14 +1566,14 @@ hipError_t launch_pass(const KvAttnArgs& a, const Pass& p, hipStream_t s) {
 }
 
 // The prefix of all and the sequences' own tokens.
-template <int DT, int D>
+template <int DT, int D, bool SOLO>
 hipError_t launch_both(const KvAttnArgs& a, const Pass& shared, const Pass& own, hipStream_t s) {
   const int grid = shared.workgroups + own.workgroups;
   if (shared.tile_rows == kTileRows) {
-    kv_attention_both_kernel<DT, D, 0><<<grid, kThreads, 0, s>>>(a, shared, own);
+    kv_attention_both_kernel<DT, D, 0, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own);
   } else if constexpr (DT == NVFP4_DTYPE_BF16) {
-    if (shared.tile_rows == 64) kv_attention_both_kernel<DT, D, 2><<<grid, kThreads, 0, s>>>(a, shared, own);
-    else kv_attention_both_kernel<DT, D, 4><<<grid, kThreads, 0, s>>>(a, shared, own);
+    if (shared.tile_rows == 64) kv_attention_both_kernel<DT, D, 2, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own);
+    else kv_attention_both_kernel<DT, D, 4, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own);
   }
   return hipGetLastError();
 }
@@ -1564,7 +1595,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& a, void* ws, hipStream_t s) {
   Plan pl = make_plan(a);
   float* at = (float*)ws;
   auto place = [&](Pass& p) {
-    const int64_t rows = (pass_tiles(a, p) + p.workgroups) * p.tile_rows;
+    const int64_t rows = (pass_tiles(a, p) + pass_shares(p)) * p.tile_rows;
     p.o = at;
     p.ml = at + rows * a.c.dim;
     p.head = (int2*)(p.ml + rows * 2);
@@ -1575,7 +1606,8 @@ hipError_t launch_kv_attention(const KvAttnArgs& a, void* ws, hipStream_t s) {
   hipError_t err = hipSuccess;
   for_types(a.dtype, a.c.dim, [&](auto dt, auto d) {
     if (pl.shared.batch && pl.own.tile_rows == kTileRows) {
-      if ((err = launch_both<dt(), d()>(a, pl.shared, pl.own, s)) != hipSuccess) return;
+      err = pl.own.solo ? launch_both<dt(), d(), true>(a, pl.shared, pl.own, s) : launch_both<dt(), d(), false>(a, pl.shared, pl.own, s);
+      if (err != hipSuccess) return;
     } else {
       if (pl.shared.batch && (err = launch_pass<dt(), d()>(a, pl.shared, s)) != hipSuccess) return;
       if ((err = launch_pass<dt(), d()>(a, pl.own, s)) != hipSuccess || !pl.join) return;

@@ -58,17 +58,16 @@ class Pages:
     def write(self, k, v, slots):
         """k, v [rows, heads * dim]; rows outside the cache are dropped."""
         d = np.arange(self.dim)
+        kc, ks = quantize_rows(np.reshape(k, (len(slots), self.heads, self.dim)))
+        vc, vs = quantize_rows(np.reshape(v, (len(slots), self.heads, self.dim)))
         for r, slot in enumerate(slots):
             if not 0 <= slot < self.n_pages * self.page:
                 continue
             for h in range(self.heads):
                 page, block, o, s = self._at(slot, h)
-                cols = slice(h * self.dim, (h + 1) * self.dim)
-                kc, ks = quantize_rows(k[r, cols])
-                vc, vs = quantize_rows(v[r, cols])
-                self.k_codes[page, block + key_index(o, d, self.dim)] = kc
-                self.v_codes[page, block + value_index(o, d)] = vc
-                self.k_scales[page, s], self.v_scales[page, s] = ks, vs
+                self.k_codes[page, block + key_index(o, d, self.dim)] = kc[r, h]
+                self.v_codes[page, block + value_index(o, d)] = vc[r, h]
+                self.k_scales[page, s], self.v_scales[page, s] = ks[r, h], vs[r, h]
 
     def read(self, slots):
         """Keys and values [rows, heads, dim] float64 of slots inside the cache."""
