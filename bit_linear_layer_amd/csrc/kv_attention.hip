@@ -1284,15 +1284,36 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
 
 // The shared prefix and the sequences' own tokens in one launch: the first is
 // bound by the matrix and vector units, the second by memory, so that each
-// uses what the other leaves.  Where not all workgroups fit the chip at once,
-// the first kSlots of the grid are those of the prefix (few and long, one
-// round) with own ones spread among them, by eights since workgroups are
-// dealt to the 8 XCDs in turn; the rest of the own ones follow as places
-// become free.  WM = 0: 16-row tiles for the prefix as well.
-constexpr int kSlots = 512;  // two workgroups on each of 256 CUs
+// uses what the other leaves.  Where there is more work than places on the
+// chip (`slots`), the grid fills those once and is divided by the time that
+// both passes take, which depends on the lengths: so the workgroups divide it
+// themselves, each finding the same number.  The two kinds are spread among
+// each other by eights, since workgroups are dealt to the 8 XCDs in turn.
+// (64 sequences of 64 to 1024 tokens after 16384, 256 dimensions: 70 us + join;
+// divided on the host for half of the longest length, with further own
+// workgroups that follow as places become free: 82.)
+// WM = 0: 16-row tiles for the prefix as well.
+struct Split {
+  int slots;           // 0: every unit has a workgroup, shared.workgroups of them for the prefix
+  float shared_time;   // of one workgroup for the whole prefix pass, us
+  float own_unit_time; // ... for a unit of an own tile
+};
+
+// Fewer workgroups make a long tail of the prefix where the sequences have most
+// of the work: 256 of up to 512 tokens after 256 took 57 us with 24 of them,
+// 40 with 64.
+constexpr int kSharedLeast = 64;
+
+__device__ inline int shared_slots(const KvAttnArgs& a, const Split& split, const Pass& shared, const Pass& own, int64_t* scratch) {
+  const int tiles = a.c.heads * own.row_tiles;
+  const float own_time = (float)(Line(own, tiles, scratch).total * tiles) * split.own_unit_time;
+  __syncthreads();  // the scratch is free again
+  const int n = (int)((float)split.slots * split.shared_time / (split.shared_time + own_time)) & ~7;
+  return __builtin_amdgcn_readfirstlane(max(min(n, shared.workgroups), min(kSharedLeast, shared.workgroups)));
+}
 
 template <int DT, int D, int WM, bool SOLO>
-__global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_attention_both_kernel(KvAttnArgs a, Pass shared, Pass own) {
+__global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_attention_both_kernel(KvAttnArgs a, Pass shared, Pass own, Split split) {
   constexpr bool kWide = WM == 4 && D <= 128;
   constexpr int kStage = WM == 0 ? 0 : kWide ? WideShape<D>::kStageBytes : RowsShape<D, WM == 0 ? 2 : WM>::kStageBytes;
   constexpr int kPart = SOLO && WM != 0 ? 0 : 16 * D * (int)sizeof(float);  // a solo wave hands nothing over
@@ -1304,16 +1325,16 @@ __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_a
   __shared__ uint4 q[kRowsQ + 1];
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[2 * kWaves];
-  const int b = blockIdx.x, n = shared.workgroups;
-  bool first = b < n;
-  int wg = first ? b : b - n;
-  if (gridDim.x > kSlots && b < kSlots) {  // here n is a multiple of 8 and less than kSlots
-    const int e = b >> 3, k = e * (n >> 3) / (kSlots / 8);
-    first = (e + 1) * (n >> 3) / (kSlots / 8) > k;
+  const int b = blockIdx.x;
+  bool first = b < shared.workgroups;
+  int wg = first ? b : b - shared.workgroups;
+  if (split.slots) {
+    const int n = shared_slots(a, split, shared, own, line), eights = split.slots / 8;
+    const int e = b >> 3, k = e * (n >> 3) / eights;
+    first = (e + 1) * (n >> 3) / eights > k;
     wg = (first ? k : e - k) * 8 + (b & 7);
-  } else if (gridDim.x > kSlots) {
-    first = false;
-    wg = b - n;
+    shared.workgroups = n;
+    own.workgroups = split.slots - n;
   }
   const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), (uint4*)(stages + 2 * kPart), ml, line};
   if (!first) {
@@ -1444,6 +1465,7 @@ struct Plan {
   Pass own{}, shared{};  // shared.batch == 0: no such pass
   bool join;
   int join_waves;  // waves of a row in the join
+  Split split;     // of launch_both
   size_t floats;
 };
 
@@ -1502,8 +1524,6 @@ Plan make_plan(const KvAttnArgs& a) {
   shape_pass(a, own, kTileRows);
   const int own_steps = ceil_div(own.prefix_len, own.step) + ceil_div(own.max_len, own.step);
   pl.join = share || own_steps > own.step_waves;
-  pl.floats = pl.join ? pass_floats(a, own) : 0;
-  int64_t pieces = own.workgroups / pass_tiles(a, own);
   if (share) {
     Pass& sh = pl.shared;
     sh.batch = 1;
@@ -1515,22 +1535,22 @@ Plan make_plan(const KvAttnArgs& a) {
     // rather than one of 32: that one's LDS would leave one workgroup to a CU
     shape_pass(a, sh, own.tile_rows == kTileRows ? 2 * kTileRows : kTileRows);
   }
-  if (share && own.tile_rows == kTileRows && pl.shared.workgroups + own.workgroups > kSlots) {
-    // launch_both: the prefix's workgroups get their part of the places by
-    // the time that both take.  Measured alone: a unit of a 64- or 128-row
-    // tile 2.6 us, one of a 16-row tile 7 us per 128 dimensions (two
-    // workgroups to a CU; 256 tokens, in a solo pass 64); the sequences are taken to be half of max_len.
+  if (share) {
+    // The units' times with both kinds on the chip, for a workgroup: 2.6 us for
+    // one of 64 or 128 rows (3.4 with 256 dimensions), 5 per 128 dimensions for
+    // 256 tokens of 16 rows.  float32 gains nothing: its tiles are all alike.
     Pass& sh = pl.shared;
-    auto units = [&](const Pass& p, int len) {
-      return (double)pass_tiles(a, p) * max(1, ceil_div(ceil_div(p.prefix_len, p.step) + ceil_div(len, p.step), p.step_waves));
-    };
-    const double narrow = 7.0 * a.c.dim / 128 * (own.solo ? 0.25 : 1.0), ts = units(sh, 0) * (sh.tile_rows == kTileRows ? 7.0 * a.c.dim / 128 : 2.6);
-    const double to = units(own, (own.max_len + 1) / 2) * narrow;
-    const int n = (int)(kSlots * ts / (ts + to)) & ~7;
-    sh.workgroups = min(max(n, 64), kSlots - 64);
-    const int64_t most = (int64_t)units(sh, 0);
-    if (sh.workgroups > most) sh.workgroups = (int)((most + 7) & ~7);
+    const int slots = 512;
+    const float narrow = 5.0f * a.c.dim / 128;
+    auto units = [&](const Pass& p) { return pass_tiles(a, p) * max(1, ceil_div(ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step), p.step_waves)); };
+    if (a.dtype == NVFP4_DTYPE_BF16 && own.tile_rows == kTileRows && units(sh) + (own.solo ? (units(own) + kWaves - 1) / kWaves : units(own)) > slots) {
+      sh.workgroups = (int)min((units(sh) + 7) / 8 * 8, (int64_t)slots - 16);
+      own.workgroups = slots - min(kSharedLeast, sh.workgroups);
+      pl.split = {slots, (float)units(sh) * (sh.tile_rows == kTileRows ? narrow : a.c.dim == 256 ? 3.4f : 2.6f), own.solo ? narrow / 4 : narrow};
+    }
   }
+  pl.floats = pl.join ? pass_floats(a, own) : 0;
+  int64_t pieces = own.workgroups / pass_tiles(a, own);
   if (share) {
     pl.floats += pass_floats(a, pl.shared);
     pieces += pl.shared.workgroups / pass_tiles(a, pl.shared);
@@ -1567,13 +1587,14 @@ hipError_t launch_pass(const KvAttnArgs& a, const Pass& p, hipStream_t s) {
 
 // The prefix of all and the sequences' own tokens.
 template <int DT, int D, bool SOLO>
-hipError_t launch_both(const KvAttnArgs& a, const Pass& shared, const Pass& own, hipStream_t s) {
-  const int grid = shared.workgroups + own.workgroups;
+hipError_t launch_both(const KvAttnArgs& a, const Plan& pl, hipStream_t s) {
+  const Pass &shared = pl.shared, &own = pl.own;
+  const int grid = pl.split.slots ? pl.split.slots : shared.workgroups + own.workgroups;
   if (shared.tile_rows == kTileRows) {
-    kv_attention_both_kernel<DT, D, 0, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own);
+    kv_attention_both_kernel<DT, D, 0, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own, pl.split);
   } else if constexpr (DT == NVFP4_DTYPE_BF16) {
-    if (shared.tile_rows == 64) kv_attention_both_kernel<DT, D, 2, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own);
-    else kv_attention_both_kernel<DT, D, 4, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own);
+    if (shared.tile_rows == 64) kv_attention_both_kernel<DT, D, 2, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own, pl.split);
+    else kv_attention_both_kernel<DT, D, 4, SOLO><<<grid, kThreads, 0, s>>>(a, shared, own, pl.split);
   }
   return hipGetLastError();
 }
@@ -1606,7 +1627,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& a, void* ws, hipStream_t s) {
   hipError_t err = hipSuccess;
   for_types(a.dtype, a.c.dim, [&](auto dt, auto d) {
     if (pl.shared.batch && pl.own.tile_rows == kTileRows) {
-      err = pl.own.solo ? launch_both<dt(), d(), true>(a, pl.shared, pl.own, s) : launch_both<dt(), d(), false>(a, pl.shared, pl.own, s);
+      err = pl.own.solo ? launch_both<dt(), d(), true>(a, pl, s) : launch_both<dt(), d(), false>(a, pl, s);
       if (err != hipSuccess) return;
     } else {
       if (pl.shared.batch && (err = launch_pass<dt(), d()>(a, pl.shared, s)) != hipSuccess) return;
