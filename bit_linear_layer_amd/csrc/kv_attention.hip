@@ -65,6 +65,7 @@ struct Pass {
   const int* lens;  // null: no tokens of the sequences' own
   int max_len;
   int workgroups;
+  int start;      // what a tile's beginning and end take, in units
   int solo;       // a share is a wave's, not a workgroup's (16-row tiles, step_waves 1)
   int direct;     // every tile is whole in one workgroup and nothing joins it: write the output
   float* ml;      // partials: [slot][tile_rows][2] and [slot][tile_rows][D]
@@ -78,24 +79,30 @@ __device__ inline int own_len(const Pass& p, int b) {
   return p.lens == nullptr ? 0 : max(min(p.lens[b], p.max_len), -1);
 }
 __device__ __host__ inline int pass_shares(const Pass& p) { return p.solo ? p.workgroups * kWaves : p.workgroups; }
-__device__ inline int tile_units(const Pass& p, int len) {
-  const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(max(len, 0), p.step);
-  return max(1, ceil_div(steps, p.step_waves));  // a tile without tokens is one empty unit
+__device__ inline int ceil_pow2(int a, int b) { return (a + b - 1) >> __builtin_ctz(b); }
+// Units of row tile `rt` of a sequence with `len` own tokens: those that its
+// last row sees.  A tile without tokens is one empty unit.
+__device__ inline int tile_units(const Pass& p, int len, int rt) {
+  if (len < 0) return 1;  // no sequence, no result
+  const int last = min((rt + 1) * p.tile_rows, p.rows) - 1;
+  const int seen = max(len - p.q_len + 1 + (p.q_len == 1 ? 0 : last / p.group), 0);
+  return max(1, ceil_pow2(ceil_pow2(p.prefix_len, p.step) + ceil_pow2(seen, p.step), p.step_waves));
 }
 
-// Units of the sequences before `b` (sum over one tile each), and where a
-// position on that line lies.  All threads call it; the answer is uniform.
+// The tiles lie on a line of units: sequence by sequence, row tile by row
+// tile, and of each the kv heads, which all have the same units.  All threads
+// call this; the answers are uniform.
 struct Line {
-  int64_t total;       // units of all sequences, one tile each
-  int64_t share;       // units of a workgroup, all tiles counted
+  int64_t units;       // of all row tiles, one head each
+  int start;           // what counts as units before each tile's own
+  int64_t share, all;  // of a share and in total, starts included, all heads counted
   int64_t* scratch;    // LDS, 2 * kWaves
   int per;
-  int64_t before;      // units before this thread's sequences
-  __device__ Line(const Pass& p, int tiles_per_seq, int64_t* scratch_) : scratch(scratch_) {
-    per = ceil_div(p.batch, kThreads);
-    const int b0 = threadIdx.x * per;
+  int64_t before;      // units before this thread's row tiles, starts included
+  __device__ Line(const Pass& p, int heads, int64_t* scratch_) : scratch(scratch_) {
+    per = ceil_div(p.batch * p.row_tiles, kThreads);
     int64_t sum = 0;
-    for (int b = b0; b < min(b0 + per, p.batch); ++b) sum += tile_units(p, own_len(p, b));
+    each(p, [&](int, int, int units) { sum += units; });
     int64_t incl = sum;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -106,19 +113,22 @@ struct Line {
     if (lane == 63) scratch[wave] = incl;
     __syncthreads();
     before = incl - sum;
-    total = 0;
+    units = 0;
     for (int w = 0; w < kWaves; ++w) {
       if (w < wave) before += scratch[w];
-      total += scratch[w];
+      units += scratch[w];
     }
-    const int64_t all = total * tiles_per_seq;
-    const int n = pass_shares(p);
+    // where shares are a few units, they would only become more uneven
+    const int n = pass_shares(p), tiles = p.batch * p.row_tiles;
+    start = units * heads >= 4 * (int64_t)n ? p.start : 0;
+    before += (int64_t)start * min((int64_t)threadIdx.x * per, (int64_t)tiles);
+    all = (units + (int64_t)start * tiles) * heads;
     share = (all + n - 1) / n;
   }
-  // The sequence that holds position v of the line, and the units before it;
-  // in a solo pass each wave asks for its own v.
-  __device__ void find(const Pass& p, int64_t v, int* seq, int64_t* seq_before) {
-    const int b0 = threadIdx.x * per, wave = threadIdx.x >> 6, n = p.solo ? kWaves : 1;
+  // The row tile that holds position v of the line (one head each), and the
+  // units before it; in a solo pass each wave asks for its own v.
+  __device__ void find(const Pass& p, int64_t v, int* seq, int* rt, int64_t* units_before) {
+    const int wave = threadIdx.x >> 6, n = p.solo ? kWaves : 1;
     __syncthreads();  // the scan's sums are read
     if ((threadIdx.x & 63) == 0 && wave < n) scratch[wave] = v;
     __syncthreads();
@@ -126,31 +136,48 @@ struct Line {
     for (int w = 0; w < kWaves; ++w) want[w] = scratch[min(w, n - 1)];
     __syncthreads();
     int64_t at = before;
-    for (int b = b0; b < min(b0 + per, p.batch); ++b) {
-      const int u = tile_units(p, own_len(p, b));
+    each(p, [&](int b, int r, int units) {
+      units += start;
       for (int w = 0; w < n; ++w)
-        if (want[w] >= at && want[w] < at + u) {
-          scratch[2 * w] = b;
+        if (want[w] >= at && want[w] < at + units) {
+          scratch[2 * w] = (int64_t)b << 32 | r;
           scratch[2 * w + 1] = at;
         }
-      at += u;
-    }
+      at += units;
+    });
     __syncthreads();
     const int mine = min(wave, n - 1);
-    *seq = (int)scratch[2 * mine];
-    *seq_before = scratch[2 * mine + 1];
+    *seq = (int)(scratch[2 * mine] >> 32);
+    *rt = (int)scratch[2 * mine];
+    *units_before = scratch[2 * mine + 1];
     __syncthreads();
+  }
+
+ private:
+  template <class F>
+  __device__ void each(const Pass& p, F f) const {  // this thread's row tiles
+    const int e0 = threadIdx.x * per, n = min(per, p.batch * p.row_tiles - e0);
+    if (n <= 0) return;
+    int b = p.row_tiles == 1 ? e0 : e0 / p.row_tiles, r = e0 - b * p.row_tiles, len = own_len(p, b);
+    for (int k = 0; k < n; ++k) {
+      f(b, r, tile_units(p, len, r));
+      if (++r == p.row_tiles) {
+        r = 0;
+        len = own_len(p, min(++b, p.batch - 1));
+      }
+    }
   }
 };
 
-// A workgroup's walk over its share: tile by tile, the units [u0, u1) of each.
+// A walk over a share, tile by tile, and of each the units [u0, u1).
 // SOLO: each wave walks a share of its own.
 template <bool SOLO>
 struct Walk {
   int wg;  // the share's number
-  int64_t unit, last;
-  int tiles_per_seq;
-  int seq, len, units, x, tile;  // sequence, its own length and units; tile of the sequence, of the pass
+  int64_t at, end, last;  // on the line: this piece, the share's end
+  int heads;
+  int seq, rt, kvh, tile;  // sequence, its row tile and kv head; the tile's place on the line
+  int len, units;          // of the sequence, of the tile
   int u0, u1;
   bool any;
   // Workgroups are dealt to the 8 XCDs in turn; each XCD gets neighbouring
@@ -160,35 +187,41 @@ struct Walk {
     const int q = p.workgroups / 8, r = p.workgroups % 8, xcd = dealt % 8;
     wg = xcd * q + min(xcd, r) + dealt / 8;
     if constexpr (SOLO) wg = wg * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    tiles_per_seq = a.c.heads * p.row_tiles;
-    Line line(p, tiles_per_seq, scratch);
+    heads = a.c.heads;
+    Line line(p, heads, scratch);
     share = uniform(line.share);
-    unit = wg * share;
-    last = uniform(min(unit + share, line.total * tiles_per_seq));
-    any = unit < last;
+    start = __builtin_amdgcn_readfirstlane(line.start);
+    at = wg * share;
+    last = uniform(min(at + share, line.all));
+    any = at < last;
     if (!SOLO && !any) return;
     int64_t before;
-    line.find(p, unit / tiles_per_seq, &seq, &before);  // (past the end nothing is found)
+    line.find(p, at / heads, &seq, &rt, &before);  // (past the end nothing is found)
     if (!any) return;
     seq = __builtin_amdgcn_readfirstlane(seq);
-    before = uniform(before);
+    rt = __builtin_amdgcn_readfirstlane(rt);
+    before = uniform(before) * heads;
     len = __builtin_amdgcn_readfirstlane(own_len(p, seq));
-    units = tile_units(p, len);
-    x = (int)((unit - before * tiles_per_seq) / units);
-    u0 = (int)(unit - before * tiles_per_seq - (int64_t)x * units);
-    place(p);
+    units = __builtin_amdgcn_readfirstlane(tile_units(p, len, rt));
+    kvh = __builtin_amdgcn_readfirstlane((int)((at - before) / (start + units)));
+    place(p, __builtin_amdgcn_readfirstlane((int)(at - before - (int64_t)kvh * (start + units))));
+    if (u0 == u1) any = next(p);
   }
   __device__ bool next(const Pass& p) {
-    unit += u1 - u0;
-    if (unit >= last) return false;
-    u0 = 0;
-    if (++x == tiles_per_seq) {
-      x = 0;
-      ++seq;
-      len = __builtin_amdgcn_readfirstlane(own_len(p, seq));
-      units = tile_units(p, len);
-    }
-    place(p);
+    do {
+      at = end;
+      if (at >= last) return false;
+      if (++kvh == heads) {
+        kvh = 0;
+        if (++rt == p.row_tiles) {
+          rt = 0;
+          ++seq;
+          len = __builtin_amdgcn_readfirstlane(own_len(p, seq));
+        }
+        units = __builtin_amdgcn_readfirstlane(tile_units(p, len, rt));
+      }
+      place(p, 0);
+    } while (u0 == u1);  // a start only
     return true;
   }
   // every unit of the tile is this workgroup's
@@ -196,16 +229,21 @@ struct Walk {
 
  private:
   int64_t share;
+  int start;
   // A value that all lanes hold, in scalar registers.
   static __device__ int64_t uniform(int64_t v) {
     return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) | (int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
   }
-  __device__ void place(const Pass& p) {
-    u1 = (int)min((int64_t)units, u0 + (last - unit));
-    tile = seq * tiles_per_seq + x;
-    // the join wants to know: the workgroup of unit 0 and the number of pieces
-    if (p.head != nullptr && u0 == 0 && (threadIdx.x & (SOLO ? 63 : kThreads - 1)) == 0)
-      p.head[tile] = make_int2(wg, (int)((unit + units - 1) / share - wg) + 1);
+  // The share's part of the tile, `from` units (starts included) after its first.
+  __device__ void place(const Pass& p, int from) {
+    const int64_t tile_end = at - from + start + units;
+    end = min(tile_end, last);
+    u0 = max(from - start, 0);
+    u1 = max(from - start + (int)(end - at), 0);
+    tile = (seq * p.row_tiles + rt) * heads + kvh;
+    // the join wants to know: the share of unit 0 and the number of pieces
+    if (p.head != nullptr && u0 == 0 && u1 > 0 && (threadIdx.x & (SOLO ? 63 : kThreads - 1)) == 0)
+      p.head[tile] = make_int2(wg, (int)((tile_end - 1) / share - wg) + 1);
   }
 };
 
@@ -294,9 +332,8 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
   Walk<SOLO> t(a, p, wg, lds.line);
   if (!t.any) return;
   do {
-    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
-    const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * kTileRows;
-    const int steps = prefix_steps + ceil_div(max(len, 0), kStep);
+    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, tile = t.tile;
+    const int kvh = t.kvh, row0 = t.rt * kTileRows;
 
     // This lane's query row and the first own token that it does not see.
     const int row = min(row0 + i, p.rows - 1);
@@ -305,6 +342,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
     const int limit = len - p.q_len + 1 + row_token;
     const int tile_last = min(row0 + kTileRows, p.rows) - 1;
     const int limit_first = len - p.q_len + 1 + row0 / p.group, limit_last = len - p.q_len + 1 + tile_last / p.group;
+    const int steps = prefix_steps + ceil_div(max(limit_last, 0), kStep);  // with a visible token
 
     const int head = kvh * p.group + row - row_token * p.group;
     uint4* const queries = SOLO ? lds.q + wave * (T * 2 * KJ * 64) : lds.q;
@@ -338,10 +376,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
     };
     // A wave's next step from s on that holds a visible token, or -1.
     auto next_step = [&](int s) {
-      const int end = min(u1 * SW, steps);
-      if (s >= end) return -1;
-      if (s >= prefix_steps && (s - prefix_steps) * kStep >= limit_last) return -1;  // later ones neither
-      return s;
+      return s < min(u1 * SW, steps) ? s : -1;
     };
     // Blocks past the last token take the last one's page and are masked below.
     auto block_of = [&](const Where& w, int b) { return min((w.base >> 4) + b, (w.n - 1) >> 4); };
@@ -633,8 +668,8 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
   Walk<false> t(a, p, wg, lds.line);
   if (!t.any) return;
   do {
-    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
-    const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * C::kRows;
+    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, tile = t.tile;
+    const int kvh = t.kvh, row0 = t.rt * C::kRows;
     const int row = min(row0 + 32 * wm + i, p.rows - 1);
     const int row_token = row / p.group;
     const int64_t token = (int64_t)seq * p.q_len + row_token;
@@ -994,8 +1029,8 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
   Walk<false> t(a, p, wg, lds.line);
   if (!t.any) return;
   do {
-    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, x = t.x, tile = t.tile;
-    const int kvh = x / p.row_tiles, row0 = (x - kvh * p.row_tiles) * C::kRows;
+    const int u0 = t.u0, u1 = t.u1, seq = t.seq, len = t.len, tile = t.tile;
+    const int kvh = t.kvh, row0 = t.rt * C::kRows;
     const int row = min(row0 + 32 * wave + i, p.rows - 1);
     const int row_token = row / p.group;
     const int64_t token = (int64_t)seq * p.q_len + row_token;
@@ -1305,8 +1340,7 @@ struct Split {
 constexpr int kSharedLeast = 64;
 
 __device__ inline int shared_slots(const KvAttnArgs& a, const Split& split, const Pass& shared, const Pass& own, int64_t* scratch) {
-  const int tiles = a.c.heads * own.row_tiles;
-  const float own_time = (float)(Line(own, tiles, scratch).total * tiles) * split.own_unit_time;
+  const float own_time = (float)(Line(own, a.c.heads, scratch).units * a.c.heads) * split.own_unit_time;
   __syncthreads();  // the scratch is free again
   const int n = (int)((float)split.slots * split.shared_time / (split.shared_time + own_time)) & ~7;
   return __builtin_amdgcn_readfirstlane(max(min(n, shared.workgroups), min(kSharedLeast, shared.workgroups)));
@@ -1372,7 +1406,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
     const int row_token = rc / own.group, hd = rc - row_token * own.group;
     const int token = seq * own.q_len + row_token;
     // the row's pieces: the row in the first one's slot, and their number
-    const int tx = rc / own.tile_rows, tile = (seq * a.c.heads + kvh) * own.row_tiles + tx;
+    const int tx = rc / own.tile_rows, tile = (seq * own.row_tiles + tx) * a.c.heads + kvh;
     const int2 head = own.head[tile];
     const bool done = row >= own.rows || (own.direct && head.y == 1);  // nothing there, or written by its workgroup
     const int n_own = done ? 0 : head.y;
@@ -1380,7 +1414,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
     int n_shared = 0;
     int64_t shared_at = 0;
     if (shared.batch) {
-      const int pr = token * shared.group + hd, pt = pr / shared.tile_rows, t = kvh * shared.row_tiles + pt;
+      const int pr = token * shared.group + hd, pt = pr / shared.tile_rows, t = pt * a.c.heads + kvh;
       const int2 sh = shared.head[t];
       n_shared = done ? 0 : sh.y;
       shared_at = ((int64_t)t + sh.x) * shared.tile_rows + (pr - pt * shared.tile_rows);
@@ -1504,6 +1538,12 @@ void shape_pass(const KvAttnArgs& a, Pass& p, int stream_rows) {
     p.solo = 1;
     p.step_waves = 1;
   }
+  // Queries, page ids and first bytes come one after another before a tile's
+  // first product, and its result leaves after the last.  Counted as 1, 2, 3
+  // units: 256 sequences of 1 to 512 tokens 35.5, 35.9, 35.6 us (0: 37.9), in
+  // float32 36.7, 38.2, 40.1 (46.9); a whole prompt of 4096, whose first tiles
+  // see few tokens, 234, 207, 195 (317), with 4 and 6 196 and 198.
+  p.start = p.tile_rows == kTileRows ? 1 : 3;
   const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step);
   const int64_t units = pass_tiles(a, p) * max(1, ceil_div(steps, p.step_waves));
   p.workgroups = (int)min((units + (p.solo ? kWaves - 1 : 0)) / (p.solo ? kWaves : 1), (int64_t)(256 * per_cu));

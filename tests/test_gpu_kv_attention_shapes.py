@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.gpu_util import say
+import bit_linear_layer_amd as nv
+from tests.gpu_util import DEV, say
 from tests.test_gpu_kv_pages import BF16, F32, Setup
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,77 @@ def test_many_rows(case, bad):
     dim, heads, group, page, lens, q_len, prefix = case
     say(f"kv attention rows {case} {bad}")
     run(33, dim, heads, group, page, lens, q_len, prefix, BF16, bad)
+
+
+def test_a_whole_prompt():
+    """Row tiles whose first sees 16 tokens and whose last sees 1000."""
+    say("kv attention whole prompt")
+    run(34, 64, 5, 8, 32, [1000], 1000, 0, BF16, False)
+
+
+def dense(s_q, dev, slots, q_len, heads, group, dim):
+    """Attention of q_len queries in 64 bits over the tokens read back, the
+    scale of its rounding errors, and F of the top of test_gpu_kv_pages.py."""
+    k, v = nv.kv_pages_read(dev, slots, F32)
+    k, v = (t.view(-1, heads, dim).transpose(0, 1).double().contiguous() for t in (k, v))
+    q = s_q.view(q_len, heads, group, dim).permute(1, 0, 2, 3).reshape(heads, q_len * group, dim).double().contiguous()
+    x = torch.matmul(q, k.transpose(1, 2).contiguous()) * dim ** -0.5
+    n = k.shape[1]
+    sees = n - q_len + torch.arange(q_len, device=DEV).repeat_interleave(group)
+    x = x.masked_fill(torch.arange(n, device=DEV)[None, :] > sees[:, None], float("-inf"))
+    p = torch.softmax(x, -1)
+    size = dim ** -0.5 * float(q.norm(dim=-1).max() * k.norm(dim=-1).max())
+    f = 2.0 ** -24 * (4 * (dim + 16) * size + 2 * (n + 64) + 16)
+    back = lambda t: t.view(heads, q_len, group, dim).permute(1, 0, 2, 3).reshape(q_len, -1)
+    return back(torch.matmul(p, v)), back(torch.matmul(p, v.abs())), f
+
+
+LARGE = [
+    # dim, kv heads, group, page, batch, longest, prefix, dtype
+    (128, 8, 4, 64, 512, 300, 0, BF16),    # a wave to a tile, several tiles to a wave
+    (64, 8, 2, 16, 512, 300, 0, F32),
+    (128, 8, 4, 64, 96, 4096, 0, BF16),    # a workgroup to a tile, several units
+    (256, 4, 6, 64, 96, 4096, 0, BF16),
+    (64, 8, 1, 128, 96, 4096, 0, F32),
+    (128, 8, 4, 64, 300, 300, 2100, BF16), # with a prefix: the launch divides itself
+    (256, 4, 6, 64, 64, 1000, 3000, BF16),
+    (64, 8, 4, 64, 64, 3000, 700, BF16),
+    (128, 8, 1, 64, 24, 5000, 3000, BF16),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=[str(c[:7]).replace(" ", "") + str(c[7])[6:] for c in LARGE])
+def test_large_batches(case):
+    """More units than the chip holds, against 64-bit attention over the
+    tokens read back."""
+    dim, heads, group, page, batch, longest, prefix, dtype = case
+    say(f"kv attention large {case}")
+    g = torch.Generator(device=DEV).manual_seed(5)
+    cols, shared = -(-longest // page), -(-prefix // page)
+    n_pages = batch * cols + shared
+    dev = nv.empty_kv_pages(n_pages, heads, dim, page)
+    for i in range(0, n_pages * page, 1 << 15):
+        n = min(1 << 15, n_pages * page - i)
+        k, v = (torch.randn((n, heads * dim), generator=g, device=DEV).to(BF16) for _ in range(2))
+        nv.kv_pages_write(dev, k, v, torch.arange(i, i + n, device=DEV))
+    ids = torch.randperm(n_pages, generator=g, device=DEV).int()
+    table, prefix_pages = ids[: batch * cols].view(batch, cols).contiguous(), ids[batch * cols:].contiguous()
+    lens = torch.randint(0, longest + 1, (batch,), generator=g, device=DEV).int()
+    lens[:3] = torch.tensor([longest, -1, 0], dtype=torch.int32)
+    q = torch.randn((batch, heads * group * dim), generator=g, device=DEV).to(dtype)
+    out = nv.kv_pages_attention(q, dev, table, lens, prefix_pages=prefix_pages, prefix_len=prefix)
+    at = torch.arange(prefix, device=DEV)
+    before = prefix_pages.long()[at // page] * page + at % page
+    half, last = (2.0 ** -8, 2.0 ** -8) if dtype == BF16 else (0.0, 2.0 ** -24)
+    for b, n in enumerate(lens.tolist()):
+        if n < 0:
+            continue
+        at = torch.arange(n, device=DEV)
+        slots = torch.cat([before, table.long()[b, at // page] * page + at % page])
+        if slots.numel() == 0:
+            assert torch.all(out[b] == 0)
+            continue
+        want, scale, f = dense(q[b], dev, slots, 1, heads, group, dim)
+        err = (out[b].double() - want[0]).abs()
+        tol = (half + f) * scale[0] * (1 + last) + last * want[0].abs()
+        assert torch.all(err <= tol), (b, n, float((err - tol).max()))
