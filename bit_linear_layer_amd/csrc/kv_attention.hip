@@ -100,57 +100,61 @@ struct Line {
   int per;
   int64_t before;      // units before this thread's row tiles, starts included
   __device__ Line(const Pass& p, int heads, int64_t* scratch_) : scratch(scratch_) {
-    per = ceil_div(p.batch * p.row_tiles, kThreads);
-    int64_t sum = 0;
-    each(p, [&](int, int, int units) { sum += units; });
-    int64_t incl = sum;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = pass_shares(p), tiles = p.batch * p.row_tiles;
+    per = ceil_div(tiles, kThreads);
+    if (tiles == 1) {  // no scan (one sequence's first tokens: 8.6 -> 7.4 us)
+      units = tile_units(p, own_len(p, 0), 0);
+      before = 0;
+    } else {
+      int64_t sum = 0;
+      each(p, [&](int, int, int u) { sum += u; });
+      int64_t incl = sum;
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int64_t up = __shfl_up(incl, off);
-      if (lane >= off) incl += up;
-    }
-    if (lane == 63) scratch[wave] = incl;
-    __syncthreads();
-    before = incl - sum;
-    units = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) before += scratch[w];
-      units += scratch[w];
+      for (int off = 1; off < 64; off <<= 1) {
+        const int64_t up = __shfl_up(incl, off);
+        if (lane >= off) incl += up;
+      }
+      if (lane == 63) scratch[wave] = incl;
+      __syncthreads();
+      before = incl - sum;
+      units = 0;
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) before += scratch[w];
+        units += scratch[w];
+      }
     }
     // where shares are a few units, they would only become more uneven
-    const int n = pass_shares(p), tiles = p.batch * p.row_tiles;
     start = units * heads >= 4 * (int64_t)n ? p.start : 0;
     before += (int64_t)start * min((int64_t)threadIdx.x * per, (int64_t)tiles);
     all = (units + (int64_t)start * tiles) * heads;
     share = (all + n - 1) / n;
   }
-  // The row tile that holds position v of the line (one head each), and the
-  // units before it; in a solo pass each wave asks for its own v.
-  __device__ void find(const Pass& p, int64_t v, int* seq, int* rt, int64_t* units_before) {
-    const int wave = threadIdx.x >> 6, n = p.solo ? kWaves : 1;
-    __syncthreads();  // the scan's sums are read
-    if ((threadIdx.x & 63) == 0 && wave < n) scratch[wave] = v;
-    __syncthreads();
+  // The row tile in which share `wg` begins, and what lies before it on the
+  // line (one head each); in a solo pass wave w asks for share wg + w.
+  __device__ void find(const Pass& p, int heads, int wg, int* seq, int* rt, int64_t* units_before) {
+    *seq = *rt = 0;
+    *units_before = 0;
+    if (p.batch * p.row_tiles == 1) return;
+    const int n = p.solo ? kWaves : 1;
     int64_t want[kWaves];
-    for (int w = 0; w < kWaves; ++w) want[w] = scratch[min(w, n - 1)];
-    __syncthreads();
-    int64_t at = before;
-    each(p, [&](int b, int r, int units) {
-      units += start;
+    for (int w = 0; w < n; ++w) want[w] = (wg + w) * share / heads;
+    __syncthreads();  // the scan's sums are read
+    int64_t pos = before;
+    each(p, [&](int b, int r, int u) {
+      u += start;
       for (int w = 0; w < n; ++w)
-        if (want[w] >= at && want[w] < at + units) {
+        if (want[w] >= pos && want[w] < pos + u) {
           scratch[2 * w] = (int64_t)b << 32 | r;
-          scratch[2 * w + 1] = at;
+          scratch[2 * w + 1] = pos;
         }
-      at += units;
+      pos += u;
     });
     __syncthreads();
-    const int mine = min(wave, n - 1);
+    const int mine = p.solo ? threadIdx.x >> 6 : 0;
     *seq = (int)(scratch[2 * mine] >> 32);
     *rt = (int)scratch[2 * mine];
     *units_before = scratch[2 * mine + 1];
-    __syncthreads();
   }
 
  private:
@@ -186,7 +190,8 @@ struct Walk {
   __device__ Walk(const KvAttnArgs& a, const Pass& p, int dealt, int64_t* scratch) {
     const int q = p.workgroups / 8, r = p.workgroups % 8, xcd = dealt % 8;
     wg = xcd * q + min(xcd, r) + dealt / 8;
-    if constexpr (SOLO) wg = wg * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int first = SOLO ? wg * kWaves : wg;  // share of the workgroup's first wave
+    wg = SOLO ? first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : first;
     heads = a.c.heads;
     Line line(p, heads, scratch);
     share = uniform(line.share);
@@ -196,7 +201,7 @@ struct Walk {
     any = at < last;
     if (!SOLO && !any) return;
     int64_t before;
-    line.find(p, at / heads, &seq, &rt, &before);  // (past the end nothing is found)
+    line.find(p, heads, first, &seq, &rt, &before);  // (past the end nothing is found)
     if (!any) return;
     seq = __builtin_amdgcn_readfirstlane(seq);
     rt = __builtin_amdgcn_readfirstlane(rt);
@@ -1324,9 +1329,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
 // both passes take, which depends on the lengths: so the workgroups divide it
 // themselves, each finding the same number.  The two kinds are spread among
 // each other by eights, since workgroups are dealt to the 8 XCDs in turn.
-// (64 sequences of 64 to 1024 tokens after 16384, 256 dimensions: 70 us + join;
+// (64 sequences of 64 to 1024 tokens after 16384, 256 dimensions: 69 us and join;
 // divided on the host for half of the longest length, with further own
-// workgroups that follow as places become free: 82.)
+// workgroups that follow as places became free, 71 to 84 from run to run.)
 // WM = 0: 16-row tiles for the prefix as well.
 struct Split {
   int slots;           // 0: every unit has a workgroup, shared.workgroups of them for the prefix
