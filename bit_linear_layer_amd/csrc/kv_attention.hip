@@ -25,11 +25,12 @@
 // scale included; the value's scale multiplies the softmax weight, exactly.
 //
 // Work is divided evenly whatever the lengths: the tiles' token ranges, in
-// units of 256 tokens (one step for each of the workgroup's 4 waves), form one
-// line that is cut into equal shares, one per workgroup.  A tile that a cut
-// divides leaves partial (M, l, o) in the workspace, in slot tile + workgroup
-// (distinct for every piece, since one of the two grows from piece to piece),
-// and a second kernel joins them.
+// units of one step for each wave that takes other tokens (256 tokens here),
+// form one line that is cut into equal shares, one per workgroup or, for many
+// short tiles, per wave.  A tile that a cut divides leaves partial (M, l, o)
+// in the workspace, in slot tile + share (distinct for every piece, since one
+// of the two grows from piece to piece), and a second kernel joins them.
+// Larger tiles, for more rows, are described at rows_body and wide_body.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1446,7 +1447,7 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
       float mn = fmaxf(m, ml.x);
 #pragma unroll
       for (int off = LR / 2; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor(mn, off));
-      const float f = ml.y > 0.0f ? __builtin_amdgcn_exp2f(ml.x - mn) : 0.0f;  // a piece without tokens holds nothing
+      const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - mn);  // a piece without tokens holds nothing
       float sum = ml.y * f;
 #pragma unroll
       for (int off = LR / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
@@ -1509,6 +1510,11 @@ struct Plan {
 };
 
 int64_t pass_tiles(const KvAttnArgs& a, const Pass& p) { return (int64_t)p.batch * a.c.heads * p.row_tiles; }
+// Units if every sequence has max_len tokens.
+int64_t pass_units(const KvAttnArgs& a, const Pass& p) {
+  const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step);
+  return pass_tiles(a, p) * max(1, ceil_div(steps, p.step_waves));
+}
 // Floats of a pass's part of the workspace: partials, and the tiles' heads.
 size_t pass_floats(const KvAttnArgs& a, const Pass& p) {
   return (size_t)(pass_tiles(a, p) + pass_shares(p)) * p.tile_rows * (2 + a.c.dim) + (2 * (size_t)pass_tiles(a, p) + 3) / 4 * 4;
@@ -1517,9 +1523,9 @@ size_t pass_floats(const KvAttnArgs& a, const Pass& p) {
 // Tiles from which on each is one wave's: half of the waves that the chip holds
 // (2 workgroups of 4 on 256 CUs).  Measured, a workgroup to a tile -> a wave,
 // 4 query rows, 128 dimensions: 1024 tiles of 1 to 512 tokens 24.1 -> 25.4 us,
-// after a prefix of 512 and of up to 1024 tokens 46.7 -> 43.8; 2048 tiles 38.9 -> 37.7, of 64 tokens
-// after a prefix of 256 41.5 -> 27.2; 1024 tiles of 64 dimensions and up to 300
-// tokens 18.5 -> 14.9; 2048 in float32 62 -> 46.
+// of up to 1024 tokens after a prefix of 512 46.7 -> 43.8; 2048 tiles of 1 to
+// 512 tokens 38.9 -> 37.7, of 64 after a prefix of 256 41.5 -> 27.2; 1024 tiles
+// of 64 dimensions and up to 300 tokens 18.5 -> 14.9; 2048 in float32 62 -> 46.
 constexpr int64_t kSoloTiles = 1024;
 
 // Tile shape and number of workgroups of a pass with its rows, prefix_len
@@ -1549,9 +1555,8 @@ void shape_pass(const KvAttnArgs& a, Pass& p, int stream_rows) {
   // float32 36.7, 38.2, 40.1 (46.9); a whole prompt of 4096, whose first tiles
   // see few tokens, 234, 207, 195 (317), with 4 and 6 196 and 198.
   p.start = p.tile_rows == kTileRows ? 1 : 3;
-  const int steps = ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step);
-  const int64_t units = pass_tiles(a, p) * max(1, ceil_div(steps, p.step_waves));
-  p.workgroups = (int)min((units + (p.solo ? kWaves - 1 : 0)) / (p.solo ? kWaves : 1), (int64_t)(256 * per_cu));
+  const int64_t units = pass_units(a, p);
+  p.workgroups = (int)min(p.solo ? (units + kWaves - 1) / kWaves : units, (int64_t)(256 * per_cu));
 }
 
 Plan make_plan(const KvAttnArgs& a) {
@@ -1579,19 +1584,19 @@ Plan make_plan(const KvAttnArgs& a) {
     // together with an own pass of 16-row tiles (launch_both), two such tiles
     // rather than one of 32: that one's LDS would leave one workgroup to a CU
     shape_pass(a, sh, own.tile_rows == kTileRows ? 2 * kTileRows : kTileRows);
-  }
-  if (share) {
+
     // The units' times with both kinds on the chip, for a workgroup: 2.6 us for
     // one of 64 or 128 rows (3.4 with 256 dimensions), 5 per 128 dimensions for
     // 256 tokens of 16 rows.  float32 gains nothing: its tiles are all alike.
-    Pass& sh = pl.shared;
-    const int slots = 512;
-    const float narrow = 5.0f * a.c.dim / 128;
-    auto units = [&](const Pass& p) { return pass_tiles(a, p) * max(1, ceil_div(ceil_div(p.prefix_len, p.step) + ceil_div(p.max_len, p.step), p.step_waves)); };
-    if (a.dtype == NVFP4_DTYPE_BF16 && own.tile_rows == kTileRows && units(sh) + (own.solo ? (units(own) + kWaves - 1) / kWaves : units(own)) > slots) {
-      sh.workgroups = (int)min((units(sh) + 7) / 8 * 8, (int64_t)slots - 16);
+    constexpr int slots = 512;  // two workgroups on each of 256 CUs
+    const int64_t sh_units = pass_units(a, sh), own_units = pass_units(a, own);
+    if (a.dtype == NVFP4_DTYPE_BF16 && own.tile_rows == kTileRows &&
+        sh_units + (own.solo ? (own_units + kWaves - 1) / kWaves : own_units) > slots) {
+      const float narrow = 5.0f * a.c.dim / 128;
+      const float wide = sh.tile_rows == kTileRows ? narrow : a.c.dim == 256 ? 3.4f : 2.6f;
+      sh.workgroups = (int)min((sh_units + 7) / 8 * 8, (int64_t)slots - 16);
       own.workgroups = slots - min(kSharedLeast, sh.workgroups);
-      pl.split = {slots, (float)units(sh) * (sh.tile_rows == kTileRows ? narrow : a.c.dim == 256 ? 3.4f : 2.6f), own.solo ? narrow / 4 : narrow};
+      pl.split = {slots, (float)sh_units * wide, own.solo ? narrow / 4 : narrow};
     }
   }
   pl.floats = pl.join ? pass_floats(a, own) : 0;

@@ -23,7 +23,7 @@ struct KvAttnArgs {
   void* out; int64_t ld_out;
   int dtype;
   int q_heads, group;
-  int batch, q_len;  // batch * q_len * q_heads < 2^31
+  int batch, q_len;  // batch * q_len * q_heads < 2^30
   const int* lens;   // null: all zero
   int max_len;
   const int* table; int64_t ld_table;

@@ -13,6 +13,7 @@ using namespace nvfp4;
 namespace {
 
 constexpr int64_t kIndexLimit = (int64_t)1 << 31;
+constexpr int64_t kLengthLimit = (int64_t)1 << 30;  // tokens and rows round up to whole steps and tiles in 32 bits
 constexpr int64_t kRowLimit = (int64_t)1 << 28;  // 16 threads a row in a grid of less than 2^32
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -55,19 +56,19 @@ int check_pages(const nvfp4_kv_pages* c, KvPages& out) {
 
 // A dense operand whose rows hold `width` elements of `esz` bytes.
 int check_rows(const void* p, int64_t ld, int64_t width, int esz) {
-  if (ld < width || (ld * esz) % 16 != 0) return NVFP4_ERR_STRIDE;
+  if (ld < width || ld % (16 / esz) != 0) return NVFP4_ERR_STRIDE;
   return aligned(p, 16) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
 // The sizes of a batch over cache `c` (already in a.c), not its pointers.
-int check_batch(const nvfp4_kv_batch* b, int page_size, int q_heads, int dtype, KvAttnArgs& a) {
+int check_batch(const nvfp4_kv_batch* b, int q_heads, int dtype, KvAttnArgs& a) {
   if (b == nullptr) return NVFP4_ERR_NULL;
   if (elem_size(dtype) == 0) return NVFP4_ERR_DTYPE;
   if (q_heads < 1 || q_heads % a.c.heads != 0) return NVFP4_ERR_SHAPE;
   if (b->batch < 0 || b->q_len < 1 || b->max_len < 0 || b->prefix_len < 0) return NVFP4_ERR_SHAPE;
-  if (b->batch >= kIndexLimit || b->q_len >= kIndexLimit || b->max_len >= kIndexLimit || b->prefix_len >= kIndexLimit)
+  if (b->batch >= kIndexLimit || b->q_len >= kIndexLimit || b->max_len >= kLengthLimit || b->prefix_len >= kLengthLimit)
     return NVFP4_ERR_RANGE;
-  if (b->batch * b->q_len >= kIndexLimit / q_heads) return NVFP4_ERR_RANGE;
+  if (b->batch * b->q_len >= kLengthLimit / q_heads) return NVFP4_ERR_RANGE;
   // a column of workgroups of 256 threads for each sequence and kv head, in a grid of less than 2^32
   if (b->batch * a.c.heads >= (int64_t)1 << 24) return NVFP4_ERR_RANGE;
   a.dtype = dtype;
@@ -124,7 +125,7 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
                                                 int dtype) {
   KvAttnArgs a{};
   if (check_pages_shape(cache, a.c) != NVFP4_OK) return 0;
-  if (check_batch(batch, cache->page_size, q_heads, dtype, a) != NVFP4_OK) return 0;
+  if (check_batch(batch, q_heads, dtype, a) != NVFP4_OK) return 0;
   return kv_attention_workspace(a);
 }
 
@@ -134,7 +135,7 @@ int nvfp4_kv_pages_attention(const nvfp4_kv_pages* cache, const nvfp4_kv_batch* 
   KvAttnArgs a{};
   int st = check_pages(cache, a.c);
   if (st != NVFP4_OK) return st;
-  if ((st = check_batch(batch, cache->page_size, q_heads, dtype, a)) != NVFP4_OK) return st;
+  if ((st = check_batch(batch, q_heads, dtype, a)) != NVFP4_OK) return st;
   a.scale_log2 = scale * 1.44269504088896341f;
   if (!(scale > 0.0f) || !isfinite(a.scale_log2)) return NVFP4_ERR_VALUE;
   if (a.batch == 0) return NVFP4_OK;

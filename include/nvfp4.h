@@ -429,6 +429,8 @@ int nvfp4_gdn_recurrence(const nvfp4_gdn_inputs* in, int in_dtype, int64_t token
  *   codes       the E4M3 byte nearest to the exact x / 2^e, ties to the even
  *               code, sign = IEEE sign bit (nothing saturates);
  *   value read  code * 2^e.
+ * An element that is not finite becomes the NaN code; a NaN does not count in
+ * the maximum.
  * A power of two keeps E4M3's relative precision and makes the decoded value
  * exact in bf16 (for e >= -117, below which the smallest codes are bf16
  * subnormals).
@@ -529,14 +531,16 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
  *   workspace  DEVICE, >= nvfp4_kv_pages_attention_workspace_bytes bytes,
  *              16-byte aligned, contents arbitrary; calls that may overlap in
  *              time need one each.
- * The prefix is read once for all sequences, not once for each.  Products of
- * bf16 queries are exact, sums and the softmax are float32; with NVFP4_DTYPE_
+ * A prefix of 256 tokens or more is computed once for all sequences where
+ * each has fewer than 128 query rows a kv head (q_len * q_heads / kv_heads).
+ * Products of bf16 queries are exact, sums and the softmax are float32; with NVFP4_DTYPE_
  * BF16 each softmax weight enters its product with the values rounded to
  * bf16, with NVFP4_DTYPE_F32 queries and weights enter as three bf16 terms
  * (24 bits).  The result does not depend on timing: the same call on the same
- * data gives the same bits.  1 <= q_len, batch * q_len < 2^31 / q_heads,
- * batch * kv_heads < 2^24; q_heads a multiple of kv_heads.  At most three launches.  batch = 0 is a
- * valid call that does nothing.
+ * data gives the same bits.  1 <= q_len, batch * q_len < 2^30 / q_heads,
+ * max_len and prefix_len < 2^30, batch * kv_heads < 2^24; q_heads a multiple
+ * of kv_heads.  At most three launches.  batch = 0 is a valid call that does
+ * nothing.
  */
 int nvfp4_kv_pages_attention(const nvfp4_kv_pages* cache, const nvfp4_kv_batch* batch, const void* q,
                              int64_t ld_q, int dtype, int q_heads, float scale, void* out, int64_t ld_out,

@@ -164,3 +164,18 @@ def test_large_batches(case):
         err = (out[b].double() - want[0]).abs()
         tol = (half + f) * scale[0] * (1 + last) + last * want[0].abs()
         assert torch.all(err <= tol), (b, n, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("q_len,prefix,dtype", [(1, 0, BF16), (1, 300, BF16), (40, 300, BF16), (80, 0, BF16), (1, 300, F32)])
+def test_a_query_that_is_not_a_number(q_len, prefix, dtype):
+    """NaN in one query row and head: NaN there, also where pieces are joined,
+    and every other row as without it."""
+    say(f"kv attention nan {q_len} {prefix} {dtype}")
+    s = Setup(35, 64, 2, 2, 16, [700, 300], q_len, prefix, dtype)
+    want = s.run()
+    s.q.view(2 * q_len, 4, 64)[q_len, 3, 5] = float("nan")
+    got = s.run()
+    a, b = got.view(2 * q_len, 4, 64), want.view(2 * q_len, 4, 64).clone()
+    assert torch.isnan(a[q_len, 3]).all()
+    b[q_len, 3] = a[q_len, 3]
+    assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))

@@ -128,6 +128,30 @@ def test_extreme_rows():
         assert np.array_equal(k.cpu().numpy()[normal], want.astype(np.float32)[normal])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_elements_that_are_not_finite(dtype):
+    """They read back as NaN; a NaN leaves the rest of its row as it would be
+    without it, and other rows are untouched."""
+    say(f"kv pages not finite {dtype}")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((40, 2 * 64), generator=g, device=DEV).to(dtype)
+    y = x.clone()
+    bad = torch.zeros(x.shape, dtype=torch.bool, device=DEV)
+    for r, c, v in ((0, 3, float("nan")), (17, 64, float("nan")), (17, 100, float("inf")), (30, 9, float("-inf"))):
+        y[r, c], bad[r, c] = v, True
+    x[0, 3] = x[17, 64] = 0
+    a, b = (nv.empty_kv_pages(4, 2, 64, 16) for _ in range(2))
+    slots = torch.arange(3, 43, device=DEV)
+    nv.kv_pages_write(a, x, x, slots)
+    nv.kv_pages_write(b, y, y, slots)
+    same = torch.ones(40, 2, dtype=torch.bool, device=DEV)
+    same[17, 1] = same[30, 0] = False  # heads with an infinity have its scale
+    same = same.repeat_interleave(64, 1)
+    for want, got in zip(nv.kv_pages_read(a, slots, F32), nv.kv_pages_read(b, slots, F32)):
+        assert torch.isnan(got[bad]).all() and torch.isfinite(got[~bad]).all()
+        assert torch.equal(want[same & ~bad], got[same & ~bad])
+
+
 # ------------------------------------------------------------- attention
 
 class Setup:

@@ -127,3 +127,24 @@ def test_binding_refuses_host_tensors():
                  lambda: nv.kv_pages_attention(x, c)):
         with pytest.raises(nv.NVFP4Error):
             call()
+
+
+@pytest.mark.parametrize("kw,q_heads,taken", [
+    (dict(max_len=1 << 30, cols=1 << 28), 4, False), (dict(prefix_len=1 << 30), 4, False),
+    (dict(max_len=(1 << 30) - 1, cols=1 << 28, prefix_len=(1 << 30) - 1), 4, True),
+    (dict(q_len=1 << 28, batch=1), 4, False), (dict(q_len=(1 << 28) - 1, batch=1), 4, True),
+    (dict(batch=1 << 23, q_len=1), 2, False), (dict(batch=(1 << 23) - 1, q_len=64), 2, True), (dict(batch=1 << 23, q_len=64), 2, False),
+])
+def test_largest_shapes(kw, q_heads, taken):
+    """The plan of the largest shapes stays within its integers: the workspace
+    is 0 where a shape is refused, and otherwise below the partial results of
+    every row and of every share (2 passes of at most 2048 shares of 128 rows)."""
+    b = batch(**kw)
+    heads, dim = 2, 128
+    got = need(pages(heads=heads, dim=dim), b, q_heads)
+    rows = b.batch * b.q_len * q_heads
+    if not taken:
+        assert got == 0 and attention(pages(heads=heads, dim=dim), b, q_heads=q_heads, ldq=dim * q_heads, ldo=dim * q_heads, wsb=1 << 50) == -11
+    else:
+        tiles = 2 * (-(-rows // 16) + b.batch * heads)  # a ragged last tile in each
+        assert 0 < got <= 4 * (dim + 4) * (2 * rows + 128 * tiles + 2 * 2048 * 128)
