@@ -51,6 +51,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kStep = 64;       // tokens of one wave's step (16-row tiles)
 constexpr int kTileRows = 16;
+// The running maximum is one of log2 units up to kSlack ago: accumulators are
+// rescaled when a row's maximum has grown by more (weights reach 2^6, with the
+// same relative rounding).  At every growth of any of 32 rows it would be more
+// than half of the steps of a few thousand tokens.
+constexpr float kSlack = 6.0f;
 constexpr float kLowest = -3.0e38f;  // stands for "no token yet"; finite, so differences are never NaN
 
 // One pass over tiles of rows: what the stream kernel and the join share.
@@ -505,7 +510,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m)) {
+      if (__any(mn > m + kSlack)) {
         const float f = __builtin_amdgcn_exp2f(m - mn);
         l *= f;
 #pragma unroll
@@ -858,7 +863,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
         for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[t][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m)) {
+      if (__any(mn > m + kSlack)) {
         const float f = __builtin_amdgcn_exp2f(m - mn);
         l *= f;
 #pragma unroll
@@ -1214,7 +1219,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
         for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m)) {
+      if (__any(mn > m + kSlack)) {
         const float f = __builtin_amdgcn_exp2f(m - mn);
         l *= f;
 #pragma unroll

@@ -10,7 +10,7 @@ import torch
 
 import bit_linear_layer_amd as nv
 from tests.gpu_util import DEV, say
-from tests.test_gpu_kv_pages import BF16, F32, Setup
+from tests.test_gpu_kv_pages import BF16, F32, Setup, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,26 @@ def test_a_query_that_is_not_a_number(q_len, prefix, dtype):
     assert torch.isnan(a[q_len, 3]).all()
     b[q_len, 3] = a[q_len, 3]
     assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+
+@pytest.mark.parametrize("growth", [0.01, 0.3, 20.0, -0.3])
+@pytest.mark.parametrize("dim,group,q_len,prefix,dtype", [
+    (128, 1, 1, 0, BF16), (64, 2, 1, 0, F32), (64, 2, 10, 0, BF16), (128, 1, 40, 0, BF16), (128, 2, 40, 0, BF16),
+    (256, 2, 40, 0, BF16), (64, 1, 1, 300, BF16)])
+def test_scores_that_grow(dim, group, q_len, prefix, dtype, growth):
+    """Every token's score exceeds the last one's, by little or by much (or
+    falls): the running maximum lags behind, is caught up, or stays."""
+    say(f"kv attention growth {dim} {group} {q_len} {prefix} {dtype} {growth}")
+    s = Setup(36, dim, 1, group, 16, [600, 330], q_len, prefix, dtype)
+    u = s.rng.choice([-1.0, 1.0], dim)
+    # scale * q . k = growth * t for q = u, k = growth * t * u / sqrt(dim)
+    lists = [(s.prefix_pages, prefix, 0)] + [(s.table[b], int(n), prefix) for b, n in enumerate(s.lens)]
+    for ids, n, t0 in lists:
+        t = np.arange(n)
+        if n:
+            k = (growth * (t0 + t) * dim ** -0.5)[:, None] * u[None, :]
+            v = s.rng.standard_normal((n, dim))
+            s.host.write(k.astype(np.float32), v.astype(np.float32), [int(ids[i // 16]) * 16 + i % 16 for i in t])
+    s.dev = to_dev(s.host)
+    s.q = torch.from_numpy(np.tile(u.astype(np.float32), (s.q.shape[0], group))).to(dtype).to(DEV)
+    s.check(s.run())
