@@ -776,6 +776,8 @@ def kv_pages_read(pages: KVPages, slots: torch.Tensor, out_dtype=torch.bfloat16)
 def kv_pages_attention_workspace(q: torch.Tensor, pages: KVPages, batch: int, q_len: int = 1, max_len: int = 0,
                                  prefix_len: int = 0) -> torch.Tensor:
     """A workspace for ``kv_pages_attention`` calls of this shape."""
+    if q.dim() != 2:
+        raise NVFP4Error(f"q must be [batch * q_len, q_heads * {pages.head_dim}], got {list(q.shape)}")
     n = nvfp4_kv_pages_attention_workspace_bytes(pages, batch, q.shape[1] // pages.head_dim, q.dtype, q_len, max_len,
                                                  prefix_len)
     if n == 0:
@@ -790,6 +792,8 @@ def kv_pages_attention(q: torch.Tensor, pages: KVPages, table: torch.Tensor | No
     """Attention of q [batch * q_len, q_heads * head_dim] over the cache (see
     ``nvfp4_kv_pages_attention``); scale head_dim^-1/2 unless given.  Without
     ``out``, rows of places that hold no sequence are unspecified."""
+    if q.dim() != 2 or q_len < 1 or q.shape[0] % q_len != 0:
+        raise NVFP4Error(f"q must be [batch * {q_len}, q_heads * {pages.head_dim}], got {list(q.shape)}")
     batch = q.shape[0] // q_len
     if max_len is None:
         max_len = 0 if table is None else table.shape[1] * pages.page_size

@@ -51,10 +51,13 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kStep = 64;       // tokens of one wave's step (16-row tiles)
 constexpr int kTileRows = 16;
-// The running maximum is one of log2 units up to kSlack ago: accumulators are
-// rescaled when a row's maximum has grown by more (weights reach 2^6, with the
-// same relative rounding).  At every growth of any of 32 rows it would be more
-// than half of the steps of a few thousand tokens.
+// Larger tiles rescale their accumulators only when a row's maximum has grown by
+// more than 2^kSlack: at every growth of any of 32 rows it would be more than
+// half of the steps of a few thousand tokens (512-token chunks of four prompts
+// 213 -> 203 us).  Weights then reach 2^6 and round to bf16 as any others, also the
+// largest one, which would otherwise be 1: the error against 64 bits is 0.0021
+// of the output's root mean square instead of 0.0018, the output's own rounding
+// 0.0017.  16-row tiles wait for memory and keep the maximum exact.
 constexpr float kSlack = 6.0f;
 constexpr float kLowest = -3.0e38f;  // stands for "no token yet"; finite, so differences are never NaN
 
@@ -510,7 +513,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m + kSlack)) {
+      if (__any(mn > m)) {
         const float f = __builtin_amdgcn_exp2f(m - mn);
         l *= f;
 #pragma unroll

@@ -202,3 +202,19 @@ def test_scores_that_grow(dim, group, q_len, prefix, dtype, growth):
     s.dev = to_dev(s.host)
     s.q = torch.from_numpy(np.tile(u.astype(np.float32), (s.q.shape[0], group))).to(dtype).to(DEV)
     s.check(s.run())
+
+
+@pytest.mark.parametrize("q_len,prefix,dtype", [(1, 300, BF16), (1, 100, BF16), (50, 300, BF16), (80, 257, BF16), (3, 300, F32)])
+def test_only_a_prefix(q_len, prefix, dtype):
+    """No tokens of the sequences' own: neither table nor lengths are given."""
+    say(f"kv attention prefix only {q_len} {prefix} {dtype}")
+    s = Setup(37, 64, 2, 1, 16, [0, 0, 0], q_len, prefix, dtype)
+    out = nv.kv_pages_attention(s.q, s.dev, q_len=q_len, prefix_pages=s.args()["prefix_pages"], prefix_len=prefix)
+    # every query sees the whole prefix and nothing else
+    s.check(out)
+
+
+def test_the_largest_pages():
+    say("kv attention pages of 4096")
+    for q_len, prefix in ((1, 300), (40, 0)):
+        run(38, 128, 1, 2, 4096, [4200, 300], q_len, prefix, BF16, False)

@@ -148,3 +148,14 @@ def test_largest_shapes(kw, q_heads, taken):
     else:
         tiles = 2 * (-(-rows // 16) + b.batch * heads)  # a ragged last tile in each
         assert 0 < got <= 4 * (dim + 4) * (2 * rows + 128 * tiles + 2 * 2048 * 128)
+
+
+@pytest.mark.parametrize("shape,q_len", [((4, 128), 0), ((4, 128), -1), ((4, 128), 3), ((512,), 1), ((2, 2, 128), 1)])
+def test_binding_refuses_rows_that_are_no_batch(shape, q_len):
+    t = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    c = nv.KVPages(t(4, 2 * 16 * 64), t(4, 2 * 16 * 64), t(4, 32), t(4, 32), 2, 64, 16)
+    with pytest.raises(nv.NVFP4Error):
+        nv.kv_pages_attention(torch.zeros(shape, dtype=torch.bfloat16), c, q_len=q_len)
+    if len(shape) != 2:
+        with pytest.raises(nv.NVFP4Error):
+            nv.kv_pages_attention_workspace(torch.zeros(shape, dtype=torch.bfloat16), c, 4)
