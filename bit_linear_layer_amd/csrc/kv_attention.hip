@@ -1576,7 +1576,17 @@ Plan make_plan(const KvAttnArgs& a) {
   own.rows = a.q_len * a.group;
   own.lens = a.lens;
   own.max_len = a.max_len;
-  const bool share = a.batch > 1 && a.prefix_len >= 256 && own.rows < 128;
+  // Computing the prefix for all sequences at once saves reading and
+  // converting it for each and costs partial results and their join.  Measured
+  // (8 kv heads of 128), for each -> at once: few rows, prefix 512 of 4, 16, 64 and
+  // 256 sequences 12.0 -> 12.7, 13.4 -> 13.5, 17.5 -> 23.4, 41.6 -> 39.8 us, 1024
+  // 12.5 -> 13.0, 18.1 -> 14.1, 22.4 -> 28.0, 56 -> 44, 2048 14.3 -> 13.5, 20.3 -> 14.3,
+  // 31.2 -> 27.8, 88 -> 47.  More rows of their own fill larger tiles and cost
+  // another launch: 20 and 48 rows, 3000 of 32 46 -> 63 and 60 -> 68, 10000 of 32
+  // 113 -> 79 and 130 -> 115; 64 rows 129 -> 137.
+  const int64_t prefix_tokens = (int64_t)a.batch * a.c.heads * a.prefix_len;
+  const bool share = a.batch > 1 && (own.rows <= kTileRows ? a.prefix_len >= 1024
+                                                           : own.rows <= 48 && prefix_tokens >= 3 << 19);
   own.prefix_len = share ? 0 : a.prefix_len;
   own.direct = !share;
   shape_pass(a, own, kTileRows);

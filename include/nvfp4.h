@@ -531,8 +531,8 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
  *   workspace  DEVICE, >= nvfp4_kv_pages_attention_workspace_bytes bytes,
  *              16-byte aligned, contents arbitrary; calls that may overlap in
  *              time need one each.
- * A prefix of 256 tokens or more is computed once for all sequences where
- * each has fewer than 128 query rows a kv head (q_len * q_heads / kv_heads).
+ * A long prefix (1024 tokens, or more where each sequence has more than 16
+ * query rows a kv head) is computed once for all sequences.
  * Products of bf16 queries are exact, sums and the softmax are float32; with NVFP4_DTYPE_
  * BF16 each softmax weight enters its product with the values rounded to
  * bf16, with NVFP4_DTYPE_F32 queries and weights enter as three bf16 terms

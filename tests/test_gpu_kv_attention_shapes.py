@@ -41,11 +41,11 @@ def run(seed, dim, heads, group, page, lens, q_len, prefix, dtype, bad):
 
 MANY = [
     # dim, kv heads, group, page, batch, longest, q_len, prefix, dtype: at least 1024 tiles of 16 rows
-    (64, 8, 2, 16, 140, 200, 1, 300, BF16),   # with the prefix's 128-row tiles in one launch
+    (64, 8, 2, 16, 140, 200, 1, 300, BF16),   # with a prefix of their own pass
     (128, 8, 1, 32, 130, 130, 1, 256, BF16),
     (128, 8, 1, 16, 40, 70, 8, 257, BF16),    # fewer tiles: a workgroup to each
-    (256, 16, 1, 16, 64, 70, 1, 256, BF16),   # ... 64-row tiles
-    (256, 16, 2, 64, 65, 70, 1, 260, BF16),   # ... 128-row tiles of 256 dimensions
+    (256, 16, 1, 16, 64, 70, 1, 256, BF16),
+    (256, 16, 2, 64, 65, 70, 1, 260, BF16),
     (128, 8, 1, 16, 130, 130, 1, 0, BF16),    # own tokens only
     (64, 4, 3, 64, 257, 64, 1, 0, BF16),      # ... a step each
     (256, 16, 1, 16, 64, 130, 2, 20, BF16),   # ... with a short prefix
@@ -78,9 +78,9 @@ ROWS = [
     (256, 1, 2, 64, [3000], 40, 0),
     (64, 1, 2, 64, [4100], 20, 100),
     (64, 1, 1, 16, [9, 40], 12, 2000),          # the prefix of 24 rows, with the own tokens
-    (128, 1, 5, 16, [9, 40, 0, 77, 3], 2, 1500),  # ... of 50
-    (256, 2, 1, 16, [9, 40, 0, 77, 3, 33, 1, 18, 90, 5, 2, 60], 8, 700),  # ... of 96
-    (64, 1, 4, 16, [150, 40, 70], 12, 600),     # 48 own rows: two launches
+    (128, 1, 5, 16, [9, 40, 0, 77, 3], 2, 1500),  # ... 50
+    (256, 2, 1, 16, [9, 40, 0, 77, 3, 33, 1, 18, 90, 5, 2, 60], 8, 700),
+    (64, 1, 4, 16, [150, 40, 70], 12, 600),
 ]
 
 
@@ -122,7 +122,7 @@ LARGE = [
     (128, 8, 4, 64, 96, 4096, 0, BF16),    # a workgroup to a tile, several units
     (256, 4, 6, 64, 96, 4096, 0, BF16),
     (64, 8, 1, 128, 96, 4096, 0, F32),
-    (128, 8, 4, 64, 300, 300, 2100, BF16), # with a prefix: the launch divides itself
+    (128, 8, 4, 64, 300, 300, 2100, BF16), # with a shared prefix: the launch divides itself
     (256, 4, 6, 64, 64, 1000, 3000, BF16),
     (64, 8, 4, 64, 64, 3000, 700, BF16),
     (128, 8, 1, 64, 24, 5000, 3000, BF16),
@@ -218,3 +218,59 @@ def test_the_largest_pages():
     say("kv attention pages of 4096")
     for q_len, prefix in ((1, 300), (40, 0)):
         run(38, 128, 1, 2, 4096, [4200, 300], q_len, prefix, BF16, False)
+
+
+SHARED = [
+    # dim, kv heads, group, page, lens or (batch, longest), q_len, prefix, dtype: the prefix for all at once
+    (64, 8, 2, 16, (140, 200), 1, 1030, BF16),   # 128-row tiles beside a wave to each own tile
+    (128, 8, 1, 32, (130, 130), 1, 1024, BF16),
+    (256, 16, 2, 64, (65, 70), 1, 1024, BF16),
+    (256, 16, 1, 16, (64, 70), 1, 1024, BF16),   # 64-row tiles
+    (64, 16, 1, 16, (64, 70), 1, 1025, BF16),
+    (128, 16, 1, 64, (64, 70), 1, 1025, BF16),
+    (64, 16, 1, 16, (64, 70), 1, 1025, F32),     # 16-row tiles
+    (256, 16, 1, 64, (64, 65), 1, 1024, F32),
+    (128, 8, 1, 16, (40, 70), 8, 1100, BF16),    # a workgroup to each own tile
+    (64, 1, 5, 16, [9, 40, 0, 77, 3], 2, 1100, BF16),
+    (256, 1, 5, 16, [9, 40, -1, 77, 3], 2, 1100, BF16),
+    (256, 2, 1, 16, [9, 40, 0, 77, 3, 33, 1, 18, 90, 5, 2, 60], 8, 1100, BF16),
+    (64, 1, 16, 16, [20] * 40, 1, 1040, BF16),
+    (128, 2, 4, 16, [1, 0, 33, 128, 5], 1, 1025, BF16),
+    (256, 2, 2, 32, [30, 0, 50], 2, 1200, BF16),
+    (128, 2, 4, 16, [1, 0, 33, 128, 5], 1, 1030, F32),
+    (64, 16, 1, 64, (64, 40), 17, 1600, BF16),   # 17 own rows: two launches
+]
+
+
+@pytest.mark.parametrize("bad", [False, True], ids=["", "bad-pages"])
+@pytest.mark.parametrize("case", SHARED, ids=[str(c[:7]).replace(" ", "") + str(c[7])[6:] for c in SHARED])
+def test_a_shared_prefix(case, bad):
+    dim, heads, group, page, lens, q_len, prefix, dtype = case
+    say(f"kv attention shared {case} {bad}")
+    if isinstance(lens, tuple):
+        lens = ragged(np.random.default_rng(39), *lens)
+    run(39, dim, heads, group, page, lens, q_len, prefix, dtype, bad)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_shared_prefix_in_a_graph(dtype):
+    """Lengths change between replays, and with them the division of the launch."""
+    say(f"kv attention shared graph {dtype}")
+    s = Setup(40, 64, 8, 2, 16, [200] * 72, 1, 1100, dtype)
+    args, out = s.args(), torch.zeros_like(s.q)
+    ws = nv.kv_pages_attention_workspace(s.q, s.dev, 72, 1, s.table.shape[1] * 16, 1100)
+    s.run(out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.kv_pages_attention(s.q, s.dev, out=out, workspace=ws, **args)
+    for i in range(4):
+        s.q.copy_(torch.randn_like(s.q, dtype=F32))
+        args["lens"].copy_(torch.randint(-1, (200, 1, 60, 200)[i] + 1, (72,), dtype=torch.int32))
+        out.fill_(9.0)
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        want = torch.full_like(out, 9.0)
+        nv.kv_pages_attention(s.q, s.dev, out=want, **args)
+        assert torch.equal(want, got)

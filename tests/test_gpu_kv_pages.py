@@ -229,14 +229,14 @@ CASES = [
     (128, 2, 4, 64, [255, 256, 257, 0, 300, 3], 1, 0),
     (256, 1, 6, 64, [700], 1, 0),
     (256, 2, 3, 32, [129, 64], 1, 100),          # one pass over prefix and own tokens
-    (128, 2, 4, 16, [1, 0, 33, 128, 5], 1, 257),  # the prefix for all at once
+    (128, 2, 4, 16, [1, 0, 33, 128, 5], 1, 257),
     (128, 1, 8, 128, [40] * 9, 1, 513),
     (64, 3, 5, 32, [70, 9, 200], 4, 0),          # drafted tokens, 20 rows a head
     (64, 1, 2, 16, [3, 7, 0], 7, 300),           # more queries than own tokens
     (64, 1, 2, 16, [3, 7], 7, 0),                # ... and rows that see nothing
     (256, 1, 2, 64, [90, 75], 33, 40),           # a chunk
     (128, 1, 1, 16, [50, 200], 50, 333),
-    (64, 1, 16, 16, [20] * 40, 1, 1000),         # 640 rows share the prefix
+    (64, 1, 16, 16, [20] * 40, 1, 1000),
 ]
 
 
