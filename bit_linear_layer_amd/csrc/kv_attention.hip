@@ -295,6 +295,69 @@ __device__ inline uint32_t keep_bytes(int n) {
   return c == 4 ? 0xFFFFFFFFu : (1u << (8 * c)) - 1u;
 }
 
+// A token's value may hold NaN codes.  Where only some rows of a tile see the
+// token, its weight is 0 for the others, and 0 * NaN would reach them: so in
+// the steps that hold such tokens the NaN codes are taken out of the bytes
+// before the product (drop_nan), and the rows that see one get the NaN when
+// their results are in memory (put_nan, from the cache once more; without NaN
+// codes in these few tokens it is not called).
+
+// Bit 7 of every byte that is a NaN code (0x7F, 0xFF).
+__device__ inline uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ inline uint32_t nan_bytes(const uint4& v) { return nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w); }
+
+// Takes the NaN codes out of 16 codes; not zero if there were any.
+__device__ inline uint32_t drop_nan(uint4& v) {
+  uint32_t any = 0;
+  auto word = [&](uint32_t& w) {
+    asm("" : "+v"(w));  // what a test before computed is not kept: it would take as many registers again
+    const uint32_t n = nan_bytes(w);
+    w &= ~(n | (n - (n >> 7)));
+    any |= n;
+  };
+  word(v.x);
+  word(v.y);
+  word(v.z);
+  word(v.w);
+  return any;
+}
+
+// A query row that this lane has results of: its tokens are those below
+// `limit`, its results in dimensions d, d + 1, d + 2, d + 3 for d = first,
+// first + stride ..
+struct LaneRow {
+  int seq, kvh, head, limit, first, stride;
+  int64_t token;
+};
+
+// Writes NaN into the row's result in each dimension that has a NaN code among
+// the row's tokens from the first step (of STEP tokens) on that only some rows
+// see: `least` and `most` are the limits of the rows.  partial: the row in the
+// workspace, or null for the output.
+template <int DT, int STEP>
+__device__ __attribute__((always_inline)) inline void put_nan(const KvAttnArgs& a, const LaneRow& row, int least, int most, float* partial) {
+  const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
+  const int* const list = a.table + row.seq * a.ld_table;
+#pragma unroll 1
+  for (int block = max(least, 0) / STEP * (STEP / 16); 16 * block < most; ++block) {
+    const int id = list[block >> page_blocks_shift];
+    if ((unsigned)id >= (unsigned)a.c.n_pages) continue;
+    const int64_t at = (int64_t)((row.kvh << a.c.page_shift) + (block & page_blocks_mask) * 16) * a.c.dim;
+    const uint8_t* const src = a.c.vc + (uint64_t)(unsigned)id * (uint64_t)a.c.ld_codes + at;
+    const int sees = row.limit - 16 * block;
+#pragma unroll 1
+    for (int e = 0; e < 4 * (a.c.dim / row.stride); ++e) {
+      const int d = row.first + (e >> 2) * row.stride + (e & 3);
+      const uint4 v = *reinterpret_cast<const uint4*>(src + d * 16);
+      if (nan_bytes(make_uint4(v.x & keep_bytes(sees), v.y & keep_bytes(sees - 4), v.z & keep_bytes(sees - 8), v.w & keep_bytes(sees - 12))) == 0)
+        continue;
+      if (partial != nullptr) partial[d] = __builtin_nanf("");
+      else if constexpr (DT == NVFP4_DTYPE_BF16) ((uint16_t*)a.out)[row.token * a.ld_out + (int64_t)row.head * a.c.dim + d] = 0x7FC0;
+      else ((float*)a.out)[row.token * a.ld_out + (int64_t)row.head * a.c.dim + d] = __builtin_nanf("");
+    }
+  }
+}
+
 // 1 / l, 0 for a row without tokens.
 __device__ inline float inverse_sum(float l) { return l > 0.0f ? 1.0f / l : 0.0f; }
 
@@ -324,6 +387,7 @@ struct StreamLds {
   uint4* q;                // [kTerms][D / 32][64], SOLO: for each wave
   float (*ml)[32][2];
   int64_t* line;
+  int* nan_tile;           // the tile whose values had NaN codes taken out (any other number: perhaps none)
 };
 
 // PAIR: two workgroups share a CU, i.e. 256 registers a wave.
@@ -428,6 +492,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       page_ids(s, pk, pv);
       load_keys(s, pk);
     }
+    bool nan = false;  // NaN codes were taken out
     if constexpr (!SOLO) __syncthreads();  // the queries are in LDS
     while (s >= 0) {
       const Where w = where(s);
@@ -505,6 +570,25 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
           vq[d].z &= keep[2];
           vq[d].w &= keep[3];
         }
+        if (!prefix && limit_first < limit_last && w.base + kStep > limit_first) {
+          uint32_t any = 0;
+          if constexpr (kLate) {  // (tested first, as below, it would spill 100 registers more)
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) {
+              any |= drop_nan(vq[d]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            nan |= __any(any != 0);
+          } else {
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) any |= nan_bytes(vq[d]);
+            if (__builtin_expect(__any(any != 0), 0)) {
+              nan = true;
+#pragma unroll
+              for (int d = 0; d < DT16; ++d) drop_nan(vq[d]);
+            }
+          }
+        }
       }
 
       float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
@@ -553,6 +637,8 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       pv = pvn;
     }
 
+    if (!SOLO && nan) *lds.nan_tile = tile;
+
     // Join the four waves, register by register: 2 and 3 hand theirs to 0 and
     // 1, then 1 to 0.
     l += __shfl_xor(l, 16);
@@ -582,9 +668,10 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       if (wave == 0) take(lds.part_b, 1);
     }
     if (SOLO || wave == 0) {
+      const bool whole = p.direct && t.whole();
+      const int64_t at = ((int64_t)tile + t.wg) * kTileRows + i;
       if (row0 + i < p.rows) {
-        if (!(p.direct && t.whole())) {
-          const int64_t at = ((int64_t)tile + t.wg) * kTileRows + i;
+        if (!whole) {
           if (g == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
 #pragma unroll
           for (int d = 0; d < DT16; ++d) *reinterpret_cast<f32x4*>(p.o + at * D + 16 * d + 4 * g) = o[d];
@@ -596,6 +683,10 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
             store_out4<DT>(a, (int)token, head, 16 * d + 4 * g, v);
           }
         }
+      }
+      if (__builtin_expect(SOLO ? nan : __builtin_amdgcn_readfirstlane(*lds.nan_tile) == tile, 0)) {
+        if (row0 + i < p.rows)
+          put_nan<DT, kStep>(a, LaneRow{seq, kvh, head, limit, 4 * g, 16, token}, limit_first, limit_last, whole ? nullptr : p.o + at * D);
       }
     }
     if constexpr (!SOLO) __syncthreads();  // the queries and the hand-over are read
@@ -613,7 +704,8 @@ __global__ __launch_bounds__(kThreads, (kPaired<DT, D>) ? 2 : 1) void kv_attenti
   __shared__ uint4 q[kTerms<DT> * (D / 32) * 64 * (SOLO ? kWaves : 1)];
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[2 * kWaves];
-  stream_body<DT, D, kPaired<DT, D>, SOLO>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line});
+  __shared__ int nan_tile;
+  stream_body<DT, D, kPaired<DT, D>, SOLO>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line, &nan_tile});
 }
 
 // The same for more rows (bf16): tiles of 32 * WM rows (WM = 1, 2; with D =
@@ -659,6 +751,7 @@ struct RowsLds {
   float (*ml)[32][2];
   int64_t* line;
   uint4* q;  // [kWaves][kQueriesLds][64]
+  int* nan_tile;  // see StreamLds
 };
 
 template <int D, int WM>
@@ -689,6 +782,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
     const int64_t token = (int64_t)seq * p.q_len + row_token;
     const int limit = len - p.q_len + 1 + row_token;  // first own token that this row does not see
     const int limit_first = len - p.q_len + 1 + min(row0 + 32 * wm, p.rows - 1) / p.group;
+    const int limit_tile = len - p.q_len + 1 + row0 / p.group;  // ... that the tile's first row does not see
     const int limit_last = len - p.q_len + 1 + (min(row0 + C::kRows, p.rows) - 1) / p.group;
     const int steps = prefix_steps + ceil_div(max(limit_last, 0), C::kStepTokens);  // with a visible token
     const int u_end = min(u1, ceil_div(steps, C::kWT));
@@ -716,11 +810,11 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
 
     struct Where {
       const int* list;
-      int base, n;
+      int base, n, all;  // the step's first token; tokens of the list that any row sees, that all rows of the tile see
     };
     auto where = [&](int s) __attribute__((always_inline)) {
-      if (s < prefix_steps) return Where{a.prefix_pages, s * C::kStepTokens, p.prefix_len};
-      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * C::kStepTokens, limit_last};
+      if (s < prefix_steps) return Where{a.prefix_pages, s * C::kStepTokens, p.prefix_len, p.prefix_len};
+      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * C::kStepTokens, limit_last, limit_tile};
     };
     // Step of this region in unit u; past the last one, that one again (so
     // every wave copies as much, and nothing reads it).
@@ -776,6 +870,32 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       value_scales[lane] = __uint_as_float(value_scale << 23);
       bad = bad_next;
     };
+    // Bytes that hold no token that any row sees may be NaN codes, and their
+    // scales infinite (0 * NaN): each wave clears those of the pieces that it
+    // copied, and takes out the NaN codes that only some rows see.
+    auto clear = [&](int u, uint8_t* stage) __attribute__((always_inline)) {
+      const int s = u * C::kWT + wt;
+      const Where w = where(min(s, steps - 1));
+      if (bad == 0 && s < steps && w.base + C::kStepTokens <= w.all) return;
+      asm volatile("");  // a real branch: the steps that take it are few
+      uint8_t* const values = stage + wt * (2 * C::kHalf) + C::kHalf + wm * PW * 1024 + lane * 16;
+      uint32_t any = 0;
+      if (w.all < w.n && w.base + C::kStepTokens > w.all) {
+#pragma unroll
+        for (int k = 0; k < PW; ++k) any |= nan_bytes(*reinterpret_cast<const uint4*>(values + k * 1024));
+        any = __any(any != 0);
+        if (any == 0 && bad == 0 && s < steps && w.base + C::kStepTokens <= w.n) return;
+      }
+      for (int k = 0; k < PW; ++k) {
+        const int block = 32 * (NT == 1 ? wm * PW / D32 : k / D32) + 16 * h;
+        const int holds = s >= steps || (bad >> block & 1u) ? 0 : w.n - (w.base + block);
+        uint4 v = *reinterpret_cast<const uint4*>(values + k * 1024);
+        v = make_uint4(v.x & keep_bytes(holds), v.y & keep_bytes(holds - 4), v.z & keep_bytes(holds - 8), v.w & keep_bytes(holds - 12));
+        if (any != 0) drop_nan(v);
+        *reinterpret_cast<uint4*>(values + k * 1024) = v;
+      }
+      if (any != 0) *lds.nan_tile = tile;
+    };
 
     // One step.  The fragments (keys, then values) are read kAhead before
     // their use and converted one ahead, and the order is pinned
@@ -795,22 +915,8 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       uint8_t* const values = keys + C::kHalf;
 
       if (masked) {
-        // Bytes that hold no token that any row sees may be NaN codes, and
-        // their scales infinite (0 * NaN): clear them.  The waves of a region
-        // write the same zeros, each before it reads.
-        asm volatile("");  // a real branch: the steps that take it are few
+        asm volatile("");
         if (lane < 32 * TT && (base + lane >= held || (bad >> lane & 1u))) value_scales[lane] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const int holds = (bad >> (32 * t + 16 * h) & 1u) ? 0 : held - (base + 32 * t + 16 * h);
-          uint32_t keep[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) keep[e] = keep_bytes(holds - 4 * e);
-          for (int d = 0; d < D32; ++d) {
-            u32x4* const v = reinterpret_cast<u32x4*>(values + (t * D32 + d) * 1024);
-            *v = *v & u32x4{keep[0], keep[1], keep[2], keep[3]};
-          }
-        }
       }
 
       floatx16 sc[TT];
@@ -913,7 +1019,9 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       load_pages(u0 + 1);
       for (int u = u0; u < u_end; ++u) {
         wait_vmem<0>();
+        asm volatile("" ::: "memory");  // only the wait says that the bytes read below are there
         put_scales();
+        clear(u, stages + (u & 1) * C::kStageBytes);
         barrier_lds();
         copy(u + 1, stages + (~u & 1) * C::kStageBytes);
         load_pages(u + 2);
@@ -959,10 +1067,10 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       }
     }
     const int r = 32 * wm + i;  // row of the tile
+    const bool whole = p.direct && t.whole();
+    const int64_t at = ((int64_t)tile + t.wg) * C::kRows + r;
     if (wt == 0 && row0 + r < p.rows) {
-      const bool whole = p.direct && t.whole();
       if (!whole) {
-        const int64_t at = ((int64_t)tile + t.wg) * C::kRows + r;
         if (h == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
 #pragma unroll
         for (int d = 0; d < D32; ++d)
@@ -981,6 +1089,11 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
           }
       }
     }
+    if (__builtin_expect(wt == 0 && __builtin_amdgcn_readfirstlane(*lds.nan_tile) == tile, 0)) {
+      if (row0 + r < p.rows)
+        put_nan<NVFP4_DTYPE_BF16, C::kStepTokens>(a, LaneRow{seq, kvh, kvh * p.group + row - row_token * p.group, limit, 4 * h, 8, token},
+                                                  limit_tile, limit_last, whole ? nullptr : p.o + at * D);
+    }
     barrier_lds();
   } while (t.next(p));
 }
@@ -993,7 +1106,8 @@ __global__ __launch_bounds__(kThreads, WM == 1 ? 1 : 2) void kv_attention_rows_k
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[2 * kWaves];
   __shared__ uint4 q[C::kQueriesLds * kWaves * 64 + 1];
-  rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stages, scales, ml, line, q});
+  __shared__ int nan_tile;
+  rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stages, scales, ml, line, q, &nan_tile});
 }
 
 // Tiles of 128 rows, D <= 128: the four waves own 32 each and all work on the same
@@ -1021,6 +1135,7 @@ struct WideLds {
   float (*scales)[kStep];   // values' scales of each stage
   uint64_t* bad;            // of each stage: bit t for token t if its page does not exist
   int64_t* line;
+  int* nan_tile;            // see StreamLds; [2], tiles in turn
 };
 
 template <int D>
@@ -1039,6 +1154,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
   const int key_src = (i >> 3) * (4 * D) + h * 64 + (lane & 3) * 16 + my_col * 128;
   const int value_src = i * 16 + my_col * 512;
   const int scale_token = lane & (ST - 1);
+  int turn = 0;
 
   Walk<false> t(a, p, wg, lds.line);
   if (!t.any) return;
@@ -1050,6 +1166,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
     const int64_t token = (int64_t)seq * p.q_len + row_token;
     const int limit = len - p.q_len + 1 + row_token;  // first own token that this row does not see
     const int limit_first = len - p.q_len + 1 + min(row0 + 32 * wave, p.rows - 1) / p.group;
+    const int limit_tile = len - p.q_len + 1 + row0 / p.group;  // ... that the tile's first row does not see
     const int limit_last = len - p.q_len + 1 + (min(row0 + C::kRows, p.rows) - 1) / p.group;
     const int steps = prefix_steps + ceil_div(max(limit_last, 0), ST);  // with a visible token
     const int u_end = min(u1, steps);
@@ -1069,12 +1186,12 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
 
     struct Where {
       const int* list;
-      int base, n;
+      int base, n, all;  // see rows_body
     };
     auto where = [&](int u) __attribute__((always_inline)) {
       const int s = min(u, steps - 1);
-      if (s < prefix_steps) return Where{a.prefix_pages, s * ST, p.prefix_len};
-      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * ST, limit_last};
+      if (s < prefix_steps) return Where{a.prefix_pages, s * ST, p.prefix_len, p.prefix_len};
+      return Where{a.table + seq * a.ld_table, (s - prefix_steps) * ST, limit_last, limit_tile};
     };
     auto block_of = [&](const Where& w, int b) { return min((w.base >> 4) + b, (w.n - 1) >> 4); };
     auto slot_of = [&](int blk) { return (kvh << a.c.page_shift) + (blk & page_blocks_mask) * 16; };
@@ -1127,19 +1244,29 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
       for (int part = 0; part < kPutParts; ++part) put_part(stage, part);
     };
     // Bytes that hold no token that any row sees may be NaN codes, and their
-    // scales infinite (0 * NaN): zeros instead.
+    // scales infinite (0 * NaN): zeros instead; and NaN codes that only some
+    // rows see are taken out.
     auto clear = [&](const Where& w, int stage) __attribute__((always_inline)) {
-      if (w.base + ST > w.n || __any(value_gone)) {
-        uint8_t* const to = lds.stages + stage * C::kStageBytes + C::kHalf + to_frag;
-        const int holds = value_gone ? 0 : w.n - (w.base + 32 * my_tile + 16 * h);
+      const bool gone = __any(value_gone);
+      if (!gone && w.base + ST <= w.all) return;
+      uint32_t any = 0;
+      if (w.all < w.n && w.base + ST > w.all) {
 #pragma unroll
-        for (int k = 0; k < PW; ++k) {
-          const uint4 v = make_uint4(vraw[k].x & keep_bytes(holds), vraw[k].y & keep_bytes(holds - 4),
-                                     vraw[k].z & keep_bytes(holds - 8), vraw[k].w & keep_bytes(holds - 12));
-          *reinterpret_cast<bf16x8*>(to + k * 2048) = decode8(v.x, v.y, 1.0f);
-          *reinterpret_cast<bf16x8*>(to + k * 2048 + 1024) = decode8(v.z, v.w, 1.0f);
-        }
+        for (int k = 0; k < PW; ++k) any |= nan_bytes(vraw[k]);
+        any = __any(any != 0);
+        if (any == 0 && !gone && w.base + ST <= w.n) return;
       }
+      uint8_t* const to = lds.stages + stage * C::kStageBytes + C::kHalf + to_frag;
+      const int holds = value_gone ? 0 : w.n - (w.base + 32 * my_tile + 16 * h);
+#pragma unroll
+      for (int k = 0; k < PW; ++k) {
+        uint4 v = make_uint4(vraw[k].x & keep_bytes(holds), vraw[k].y & keep_bytes(holds - 4),
+                             vraw[k].z & keep_bytes(holds - 8), vraw[k].w & keep_bytes(holds - 12));
+        if (any != 0) drop_nan(v);
+        *reinterpret_cast<bf16x8*>(to + k * 2048) = decode8(v.x, v.y, 1.0f);
+        *reinterpret_cast<bf16x8*>(to + k * 2048 + 1024) = decode8(v.z, v.w, 1.0f);
+      }
+      if (any != 0) lds.nan_tile[turn] = tile;
     };
     // The values' scales, by wave 0, another step ahead: lane t's token t.
     int scale_page = 0;
@@ -1266,6 +1393,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
       if (wave == 0) put_scales(next, stage ^ 1);
     };
 
+    bool nan = false;  // NaN codes were taken out
     if (u0 < u_end) {
       Where w = where(u0), next = where(u0 + 1);
       load_pages(w);
@@ -1293,13 +1421,16 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
         next = after;
         barrier_lds();  // the other stage is full, and no wave reads this one any more
       }
+      nan = __builtin_amdgcn_readfirstlane(lds.nan_tile[turn]) == tile;
+      turn ^= 1;  // (a wave is at most one tile with a step ahead of the others)
     }
 
     l += __shfl_xor(l, 32);
     const int r = 32 * wave + i;  // row of the tile
+    const bool whole = p.direct && t.whole();
+    const int64_t at = ((int64_t)tile + t.wg) * C::kRows + r;
     if (row0 + r < p.rows) {
-      if (!(p.direct && t.whole())) {
-        const int64_t at = ((int64_t)tile + t.wg) * C::kRows + r;
+      if (!whole) {
         if (h == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(m, l);
 #pragma unroll
         for (int d = 0; d < D32; ++d)
@@ -1318,6 +1449,11 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
           }
       }
     }
+    if (__builtin_expect(nan, 0)) {
+      if (row0 + r < p.rows)
+        put_nan<NVFP4_DTYPE_BF16, ST>(a, LaneRow{seq, kvh, kvh * p.group + row - row_token * p.group, limit, 4 * h, 8, token},
+                                      limit_tile, limit_last, whole ? nullptr : p.o + at * D);
+    }
   } while (t.next(p));
 }
 
@@ -1328,7 +1464,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
   __shared__ __attribute__((aligned(16))) float scales[2][kStep];
   __shared__ uint64_t bad[2];
   __shared__ int64_t line[2 * kWaves];
-  wide_body<D>(a, p, blockIdx.x, WideLds{stages, scales, bad, line});
+  __shared__ int nan_tile[2];
+  wide_body<D>(a, p, blockIdx.x, WideLds{stages, scales, bad, line, nan_tile});
 }
 
 // The shared prefix and the sequences' own tokens in one launch: the first is
@@ -1373,6 +1510,7 @@ __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_a
   __shared__ uint4 q[kRowsQ + 1];
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[2 * kWaves];
+  __shared__ int nan_tile[2];
   const int b = blockIdx.x;
   bool first = b < shared.workgroups;
   int wg = first ? b : b - shared.workgroups;
@@ -1384,15 +1522,15 @@ __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_a
     shared.workgroups = n;
     own.workgroups = split.slots - n;
   }
-  const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), (uint4*)(stages + 2 * kPart), ml, line};
+  const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), (uint4*)(stages + 2 * kPart), ml, line, nan_tile};
   if (!first) {
     stream_body<DT, D, DT == NVFP4_DTYPE_BF16, SOLO>(a, own, wg, stream);
   } else if constexpr (WM == 0) {
     stream_body<DT, D, DT == NVFP4_DTYPE_BF16, false>(a, shared, wg, stream);
   } else if constexpr (kWide) {
-    wide_body<D>(a, shared, wg, WideLds{stages, scales[0], bad, line});
+    wide_body<D>(a, shared, wg, WideLds{stages, scales[0], bad, line, nan_tile});
   } else {
-    rows_body<D, WM>(a, shared, wg, RowsLds{stages, scales, ml, line, q});
+    rows_body<D, WM>(a, shared, wg, RowsLds{stages, scales, ml, line, q, nan_tile});
   }
 }
 

@@ -524,7 +524,8 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
  * to the first lens[b] - q_len + 1 + j tokens of its sequence:
  *   out = sum_t softmax_t(scale * q . k_t) v_t.
  * A row that sees no token gets zeros.  Rows of a sequence of negative length
- * are left as they were.
+ * are left as they were.  A NaN code in a key or value reaches the rows that
+ * see its token (a value's: in its dimension) and no other row.
  *   q, out     DEVICE [batch * q_len, q_heads * head_dim], row strides ld_q,
  *              ld_out in elements, rows 16-byte aligned; both of `dtype`.
  *   scale      finite and > 0 (head_dim^-1/2 as a rule).
