@@ -1593,7 +1593,10 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
       float mn = fmaxf(m, ml.x);
 #pragma unroll
       for (int off = LR / 2; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor(mn, off));
-      const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - mn);  // a piece without tokens holds nothing
+      // A piece without tokens (weight 0) holds nothing.  One whose tokens have no
+      // weight left (-0) adds nothing but its NaN: 0 * NaN.
+      const float e = __builtin_amdgcn_exp2f(ml.x - mn);
+      const float f = ml.y == 0.0f ? 0.0f : e == 0.0f ? -0.0f : e;
       float sum = ml.y * f;
 #pragma unroll
       for (int off = LR / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
@@ -1612,10 +1615,15 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
           wq[b] = q0 + b < LR ? wf : 0.0f;
           bool is_own;
           const int64_t at = place(min(c + q * S + part, max(n - 1, 0)), is_own);
-          v[b] = wq[b] != 0.0f ? *reinterpret_cast<const f32x4*>((is_own ? own.o : shared.o) + at * D + 4 * k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          v[b] = __float_as_uint(wq[b]) != 0 ? *reinterpret_cast<const f32x4*>((is_own ? own.o : shared.o) + at * D + 4 * k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) acc += v[b] * wq[b];
+        for (int b = 0; b < kBatch; ++b) {
+          if (wq[b] == 0.0f)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[b][x] = v[b][x] == v[b][x] ? 0.0f : v[b][x];
+          acc += v[b] * wq[b];
+        }
       }
     }
     if constexpr (S > 1) {

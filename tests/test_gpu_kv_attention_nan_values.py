@@ -144,3 +144,33 @@ def test_drafted_tokens_as_they_are_written():
     expected = torch.zeros_like(nan)
     expected[0, 5:, 0, :, 3] = expected[1, 5:, 1, :, 5] = expected[1, 4:, 0, :, 9] = True
     assert int((nan != expected).sum()) == 0
+
+
+@pytest.mark.parametrize("dim,group,lens,q_len,prefix,dtype", [
+    (64, 1, [4000], 1, 0, BF16), (128, 2, [3000, 700], 1, 0, F32), (64, 2, [300, 200, 150], 1, 1100, BF16),
+    (128, 1, [900], 40, 0, BF16), (128, 2, [1000], 80, 0, BF16), (256, 1, [900], 80, 0, BF16)])
+def test_a_token_of_no_weight(dim, group, lens, q_len, prefix, dtype):
+    """Scores grow so much that the first tokens' weights are 0 in float32, as
+    are those of whole pieces of the sequence.  A NaN in one of their values
+    stays a NaN wherever the sequence is cut (0 * NaN)."""
+    say(f"kv attention nan values, no weight {dim} {group} {lens} {q_len} {prefix} {dtype}")
+    s = Setup(54, dim, 1, group, 16, lens, q_len, prefix, dtype)
+    u = s.rng.choice([-1.0, 1.0], dim)
+    for ids, n, t0 in [(s.prefix_pages, prefix, 0)] + [(s.table[b], n, prefix) for b, n in enumerate(lens)]:
+        if n:  # scale * q . k = 4 t for token t
+            k = (4.0 * (t0 + np.arange(n)) * dim ** -0.5)[:, None] * u[None, :]
+            slots = [int(ids[t // 16]) * 16 + t % 16 for t in range(n)]
+            s.host.write(k.astype(np.float32), s.rng.standard_normal((n, dim)).astype(np.float32), slots)
+    s.q = torch.from_numpy(np.tile(u.astype(np.float32), (s.q.shape[0], group))).to(dtype).to(DEV)
+    s.dev = to_dev(s.host)
+    if prefix:
+        want = s.run()
+        page, block, o, _ = s.host._at(int(s.prefix_pages[0]) * 16 + 5, 0)
+        s.host.v_codes[page, block + P.value_index(o, 3)] = 0x7F
+        s.dev = to_dev(s.host)
+        got = s.run().view(-1, dim)
+        assert torch.isnan(got[:, 3]).all()
+        keep = torch.arange(dim, device=DEV) != 3
+        assert int((got[:, keep] != want.view(-1, dim)[:, keep]).sum()) == 0
+    else:
+        check(s, [(b, 7 * b + 2, 0, 5 * b + 1) for b in range(len(lens))] + [(0, lens[0] // 3, 0, 0), (0, lens[0] - 1, 0, dim - 1)])
