@@ -14,7 +14,7 @@ namespace {
 
 constexpr int64_t kIndexLimit = (int64_t)1 << 31;
 constexpr int64_t kLengthLimit = (int64_t)1 << 30;  // tokens and rows round up to whole steps and tiles in 32 bits
-constexpr int64_t kRowLimit = (int64_t)1 << 28;  // 16 threads a row in a grid of less than 2^32
+constexpr int64_t kRowLimit = ((int64_t)1 << 28) - 15;  // workgroups of 256 threads for 16 rows each, in a grid of less than 2^32
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 

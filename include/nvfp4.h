@@ -468,7 +468,7 @@ typedef struct {
  * a mixture of them).  Runs of 16 rows that fill one aligned block of slots
  * are written whole; others byte by byte.
  *   ld_k, ld_v  elements, >= kv_heads * head_dim, rows 16-byte aligned.
- * One launch.  rows = 0 is a valid call that does nothing; rows < 2^28.
+ * One launch.  rows = 0 is a valid call that does nothing; rows <= 2^28 - 16.
  */
 int nvfp4_kv_pages_write(const nvfp4_kv_pages* cache, const void* k, int64_t ld_k, const void* v,
                          int64_t ld_v, int x_dtype, int64_t rows, const int64_t* slots, void* stream);
