@@ -498,12 +498,13 @@ class KVPages:
             raise NVFP4Error(f"cache tensors must be uint8 [n_pages, >= {per * self.head_dim}] (codes) and "
                              f"[n_pages, >= {per}] (scales)")
         (ldc, one), (lds, one_s) = kc.stride(), ks.stride()
-        if one != 1 or one_s != 1 or vc.stride() != (ldc, 1) or vs.stride() != (lds, 1):
+        if one != 1 or one_s != 1 or vc.stride(1) != 1 or vs.stride(1) != 1 or \
+                cs[0] > 1 and (vc.stride(0) != ldc or vs.stride(0) != lds):
             raise NVFP4Error("cache tensors must have contiguous rows, keys and values with one row stride")
         if device.type != "cuda" or vc.device != device or ks.device != device or vs.device != device:
             raise NVFP4Error("cache tensors must live on one GPU")
-        if cs[0] == 1:  # a single row may carry any stride
-            ldc, lds = max(ldc, cs[1]), max(lds, ss[1])
+        if cs[0] == 1:  # a single page may carry any stride, which is not used
+            ldc, lds = per * self.head_dim, per
         return _KVPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), cs[0], ldc, lds, self.kv_heads,
                         self.head_dim, self.page_size)
 
@@ -523,7 +524,7 @@ def _on(t: torch.Tensor, device: torch.device, what: str) -> None:
 
 def _row_stride(t: torch.Tensor, rows: int, cols: int, device: torch.device, what: str) -> int:
     """Row stride (elements) of a [rows, cols] matrix with contiguous rows on
-    ``device``; a single row may carry any stride."""
+    ``device``; a single row may carry any stride, which is not used."""
     if t.shape != (rows, cols):
         raise NVFP4Error(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
     ld, one = t.stride()
@@ -531,7 +532,7 @@ def _row_stride(t: torch.Tensor, rows: int, cols: int, device: torch.device, wha
         raise NVFP4Error(f"{what} must have contiguous rows")
     if t.device != device:
         raise NVFP4Error(f"{what} must live on {device}, got {t.device}")
-    return ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else cols
 
 
 def _kv_slots(slots: torch.Tensor, device: torch.device) -> int:
