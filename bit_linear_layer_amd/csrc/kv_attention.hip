@@ -1485,9 +1485,9 @@ struct Split {
   float own_unit_time; // ... for a unit of an own tile
 };
 
-// Fewer workgroups make a long tail of the prefix where the sequences have most
-// of the work: 256 of up to 512 tokens after 256 took 57 us with 24 of them,
-// 40 with 64.
+// The prefix has this many at least (a multiple of 8), also where the sequences
+// have nearly all of the work.  24, 64 and 112 took the same time in 52 shapes (64 to 256
+// sequences of up to 64 and 512 tokens after 1024 to 4096).
 constexpr int kSharedLeast = 64;
 
 __device__ inline int shared_slots(const KvAttnArgs& a, const Split& split, const Pass& shared, const Pass& own, int64_t* scratch) {
@@ -1723,16 +1723,31 @@ Plan make_plan(const KvAttnArgs& a) {
   own.lens = a.lens;
   own.max_len = a.max_len;
   // Computing the prefix for all sequences at once saves reading and
-  // converting it for each and costs partial results and their join.  Measured
-  // (8 kv heads of 128), for each -> at once: few rows, prefix 512 of 4, 16, 64 and
-  // 256 sequences 12.0 -> 12.7, 13.4 -> 13.5, 17.5 -> 23.4, 41.6 -> 39.8 us, 1024
-  // 12.5 -> 13.0, 18.1 -> 14.1, 22.4 -> 28.0, 56 -> 44, 2048 14.3 -> 13.5, 20.3 -> 14.3,
-  // 31.2 -> 27.8, 88 -> 47.  More rows of their own fill larger tiles and cost
-  // another launch: 20 and 48 rows, 3000 of 32 46 -> 63 and 60 -> 68, 10000 of 32
-  // 113 -> 79 and 130 -> 115; 64 rows 129 -> 137.
-  const int64_t prefix_tokens = (int64_t)a.batch * a.c.heads * a.prefix_len;
-  const bool share = a.batch > 1 && (own.rows <= kTileRows ? a.prefix_len >= 1024
-                                                           : own.rows <= 48 && prefix_tokens >= 3 << 19);
+  // converting it for each and costs partial results and their join.  Measured,
+  // us for each -> at once, 4 query rows a kv head, own lengths up to 64 (400):
+  //   128 dimensions, 8 kv heads      prefix 512               1024                      2048
+  //   2 sequences               12.1 -> 12.8              12.8 -> 13.1              13.6 -> 13.5 (13.8 -> 13.9)
+  //   8                         12.5 -> 13.0              14.4 -> 13.6 (14.9, 14.8) 19.7 -> 15.2 (21.5 -> 15.6)
+  //   16                        13.9 -> 17.1              18.6 -> 17.9 (19.7, 17.9) 20.4 -> 18.9 (22.7 -> 18.2)
+  //   64                        17.3 -> 24.1 (25.0, 24.1) 21.5 -> 28.0 (29.7, 28.7) 30.8 -> 27.2 (39.5 -> 28.1)
+  //   256                       34.5 -> 30.4              52.8 -> 35.7              84.5 -> 40.8
+  // So: from 1024 tokens on (512 with 2048 own tiles, one per sequence and kv
+  // head; with 1024 27.6 against 25.1), and where sequences, kv heads and prefix tokens
+  // multiply to 2^16 (fewer are 0.3 to 1 us slower).  With 512 to 1023 own tiles
+  // each place of the chip has a whole one, which nothing has to join: there from
+  // 1536 tokens on (26.5 -> 26.1; 64 dimensions 20.9 -> 21.7, 2048 24.0 -> 24.0).
+  // 256 dimensions (1024 tokens: 44.6 -> 41.7) and float32 (36.4 -> 31.0) gain before
+  // that.  It remains slower with 2 kv heads and own lengths of 64: 128 dimensions,
+  // 64 sequences after 2048 19.2 -> 21.2; 256 dimensions, 32 to 128 sequences after 1024
+  // to 2048 up to 1.28 times.  More rows of their own fill larger tiles and cost
+  // another launch: 20 and 48 rows of 8 kv heads, 32 sequences after 4096 53 -> 53 and
+  // 66 -> 69, after 8192 84 -> 64 and 106 -> 97; 16 after 8192 (2^20) 56 -> 53 and
+  // 64 -> 66; 64 rows 129 -> 137.
+  const int64_t tiles = (int64_t)a.batch * a.c.heads, shared_tokens = tiles * a.prefix_len;
+  const bool whole_tiles = a.dtype == NVFP4_DTYPE_BF16 && a.c.dim <= 128 && tiles >= 512 && tiles < kSoloTiles;
+  const int least = whole_tiles ? 1536 : tiles >= 2048 ? 512 : 1024;
+  const bool share = a.batch > 1 && (own.rows <= kTileRows ? a.prefix_len >= least && shared_tokens >= 1 << 16
+                                                           : own.rows <= 48 && shared_tokens >= 3 << 19);
   own.prefix_len = share ? 0 : a.prefix_len;
   own.direct = !share;
   shape_pass(a, own, kTileRows);

@@ -532,8 +532,9 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
  *   workspace  DEVICE, >= nvfp4_kv_pages_attention_workspace_bytes bytes,
  *              16-byte aligned, contents arbitrary; calls that may overlap in
  *              time need one each.
- * A long prefix (1024 tokens, or more where each sequence has more than 16
- * query rows a kv head) is computed once for all sequences.
+ * A long prefix (512 to 1536 tokens at least, by the number of sequences and kv
+ * heads, and more with few of them or with more than 16 query rows a kv head)
+ * is computed once for all sequences.
  * Products of bf16 queries are exact, sums and the softmax are float32; with NVFP4_DTYPE_
  * BF16 each softmax weight enters its product with the values rounded to
  * bf16, with NVFP4_DTYPE_F32 queries and weights enter as three bf16 terms
