@@ -84,7 +84,7 @@ CASES = [
     (128, 2, 4, 16, [300, 40, 129], 33, 70, BF16),
     (128, 1, 1, 16, [700, 128], 128, 0, BF16),
     (256, 1, 2, 64, [400, 65], 66, 33, BF16),
-    (64, 1, 5, 16, [9, 40, 0, 77, 3], 2, 1100, BF16),    # a prefix for all at once
+    (64, 1, 5, 16, [9, 40, 0, 77, 3], 2, 1100, BF16),    # after a long prefix
     (128, 2, 1, 16, [9, 40, 0, 77, 3, 33, 1, 18, 90, 5, 2, 60], 8, 1100, BF16),
     (256, 1, 2, 16, [9, 40, -1, 77, 3], 2, 1100, BF16),
     (64, 16, 1, 64, [40, 3, 17, 0] * 16, 17, 1600, BF16),
