@@ -61,6 +61,30 @@ constexpr int kTileRows = 16;
 constexpr float kSlack = 6.0f;
 constexpr float kLowest = -3.0e38f;  // stands for "no token yet"; finite, so differences are never NaN
 
+// A weight is 2^(c x - M), its exponent one fma of the score x.  M = c max(x) is
+// rounded, so even the largest score's exponent is off by up to 2^-25 |M|, which
+// the sum l and the output o share.  From |M| = 2^28 on that could be more than a
+// float's exponent holds (scores around 2^32: sums of 0 or infinity), while a score's
+// own rounding is 2^4 and more in the exponent.  There a score whose exponent
+// is within the rounding of M counts as the largest (weight 1).
+constexpr float kHuge = 0x1p28f;
+
+// Replaces the scores by their weights' exponents (of lanes whose M is not huge
+// by the same ones as ever); `c` and `m` become 1 and 0.
+template <int N, class V>
+__device__ __attribute__((always_inline)) inline void huge_exponents(V* x, float& c, float& m) {
+  const float step = fabsf(m) >= kHuge ? fabsf(m) * 0x1p-23f : -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < (int)(sizeof(V) / sizeof(float)); ++r) {
+      const float e = fmaf(x[i][r], c, -m);
+      x[i][r] = e > -step ? 0.0f : e;
+    }
+  c = 1.0f;
+  m = 0.0f;
+}
+
 // One pass over tiles of rows: what the stream kernel and the join share.
 struct Pass {
   int batch;      // sequences (1 where the rows of all share their tokens)
@@ -604,13 +628,15 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
         for (int d = 0; d < DT16; ++d) o[d] *= f;
         m = mn;
       }
+      float c = a.scale_log2, off = m;
+      if (__builtin_expect(__any(fabsf(m) >= kHuge), 0)) huge_exponents<4>(sc, c, off);
       float wt[16];
       const uint32_t vw[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][r], a.scale_log2, -m));
+          const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][r], c, -off));
           l += e;
           wt[4 * t + r] = e * byte_scale(vw[t], r);
         }
@@ -979,13 +1005,15 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
         for (int d = 0; d < D32; ++d) o[d] *= f;
         m = mn;
       }
+      float c = a.scale_log2, off = m;
+      if (__builtin_expect(__any(fabsf(m) >= kHuge), 0)) huge_exponents<TT>(sc, c, off);
       bf16x8 pf[TT][2];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         float e[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          e[r] = __builtin_amdgcn_exp2f(fmaf(sc[t][r], a.scale_log2, -m));
+          e[r] = __builtin_amdgcn_exp2f(fmaf(sc[t][r], c, -off));
           l += e[r];
         }
 #pragma unroll
@@ -1356,10 +1384,12 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
         for (int d = 0; d < D32; ++d) o[d] *= f;
         m = mn;
       }
+      float c = a.scale_log2, off = m;
+      if (__builtin_expect(__any(fabsf(m) >= kHuge), 0)) huge_exponents<TT>(sc, c, off);
       uint32_t pf[TT][8];  // pairs of weights as bf16
       auto weight_pair = [&](int k, int r) __attribute__((always_inline)) {
-        const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[k][r], a.scale_log2, -m));
-        const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[k][r + 1], a.scale_log2, -m));
+        const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[k][r], c, -off));
+        const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[k][r + 1], c, -off));
         l += e0;
         l += e1;
         pf[k][r >> 1] = pack_bf16x2(e0 * vs[k][r >> 2][r & 3], e1 * vs[k][r >> 2][(r & 3) + 1]);
