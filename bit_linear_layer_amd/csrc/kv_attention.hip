@@ -61,29 +61,32 @@ constexpr int kTileRows = 16;
 constexpr float kSlack = 6.0f;
 constexpr float kLowest = -3.0e38f;  // stands for "no token yet"; finite, so differences are never NaN
 
-// A weight is 2^(c x - M), its exponent one fma of the score x.  M = c max(x) is
-// rounded, so even the largest score's exponent is off by up to 2^-25 |M|, which
-// the sum l and the output o share.  From |M| = 2^28 on that could be more than a
-// float's exponent holds (scores around 2^32: sums of 0 or infinity), while a score's
-// own rounding is 2^4 and more in the exponent.  There a score whose exponent
-// is within the rounding of M counts as the largest (weight 1).
-constexpr float kHuge = 0x1p28f;
-
-// Replaces the scores by their weights' exponents (of lanes whose M is not huge
-// by the same ones as ever); `c` and `m` become 1 and 0.
-template <int N, class V>
-__device__ __attribute__((always_inline)) inline void huge_exponents(V* x, float& c, float& m) {
-  const float step = fabsf(m) >= kHuge ? fabsf(m) * 0x1p-23f : -__builtin_inff();
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int r = 0; r < (int)(sizeof(V) / sizeof(float)); ++r) {
-      const float e = fmaf(x[i][r], c, -m);
-      x[i][r] = e > -step ? 0.0f : e;
-    }
-  c = 1.0f;
-  m = 0.0f;
-}
+// The running maximum M of a row and its weights' exponents c x - M, x a score.
+// M = c max(x) is rounded, so even the largest score's exponent is off by up to
+// 2^-25 |M|, which the sum l and the output o share.  From |M| = 2^28 on that would
+// soon be more than a float's exponent holds (scores around 2^32: sums of 0 or
+// infinity), while a score's own rounding is 2^4 and more in the exponent.
+// There c and M are kept scaled by the power of two that brings M below 2^28: a
+// score n roundings below the largest then has a weight of 2^(-8 n) at most, as
+// good as nothing, though not as little as it should.  Only a new maximum
+// changes the scale, so a step without one costs nothing.
+struct Maximum {
+  float c, m;  // scaled
+  __device__ explicit Maximum(float scale) : c(scale), m(kLowest) {}
+  __device__ float exponent(float x) const { return fmaf(x, c, -m); }
+  __device__ bool passed(float top, float slack) const { return top * c > m + slack; }
+  // M, not scaled
+  __device__ float value(float scale) const { return ldexpf(m, __builtin_amdgcn_frexp_expf(scale) - __builtin_amdgcn_frexp_expf(c)); }
+  // M becomes at least that of a score `top`: what that multiplies l and o by.
+  __device__ float raise(float scale, float top) {
+    const float old = value(scale), now = fmaxf(old, top * scale);
+    // |M| < 2^128 scale bounds the exponent, also where M is still kLowest
+    const int k = min(max(__builtin_amdgcn_frexp_expf(now) - 28, 0), max(__builtin_amdgcn_frexp_expf(scale) + 100, 0));
+    c = ldexpf(scale, -k);
+    m = ldexpf(now, -k);
+    return __builtin_amdgcn_exp2f(old - now);
+  }
+};
 
 // One pass over tiles of rows: what the stream kernel and the join share.
 struct Pass {
@@ -285,6 +288,11 @@ struct Walk {
   }
 };
 
+// v of the lane with number at / 4 (__shfl computes that number anew at each use).
+__device__ inline float from_lane(int at, float v) {
+  return __int_as_float(__builtin_amdgcn_ds_bpermute(at, __float_as_int(v)));
+}
+
 // 8 E4M3 bytes -> 8 bf16 values times the power of two `s` (exact).
 __device__ inline bf16x8 decode8(uint32_t a, uint32_t b, float s) {
   const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, s, false);
@@ -346,38 +354,41 @@ __device__ inline uint32_t drop_nan(uint4& v) {
   return any;
 }
 
-// A query row that this lane has results of: its tokens are those below
-// `limit`, its results in dimensions d, d + 1, d + 2, d + 3 for d = first,
-// first + stride ..
-struct LaneRow {
-  int seq, kvh, head, limit, first, stride;
-  int64_t token;
-};
-
-// Writes NaN into the row's result in each dimension that has a NaN code among
-// the row's tokens from the first step (of STEP tokens) on that only some rows
-// see: `least` and `most` are the limits of the rows.  partial: the row in the
-// workspace, or null for the output.
-template <int DT, int STEP>
-__device__ __attribute__((always_inline)) inline void put_nan(const KvAttnArgs& a, const LaneRow& row, int least, int most, float* partial) {
+// Writes NaN into the results of row r of the tile, in each dimension that has a
+// NaN code among the tokens that the row sees, from the first step (of STEP
+// tokens) on that some row of the tile does not see.  This lane has the
+// dimensions d .. d + 3 of d = first, first + stride ..
+template <int DT, int D, int ROWS, int STEP, class W>
+__device__ __attribute__((always_inline)) inline void put_nan(const KvAttnArgs& a, const Pass& p, const W& t, int r, int first, int stride) {
+  // All is worked out anew from these: what the tile began with would have to
+  // be kept in scalar registers, of which there are too few.
+  int seq = t.seq, kvh = t.kvh, rt = t.rt, len = t.len;
+  asm("" : "+v"(seq), "+v"(kvh), "+v"(rt), "+v"(len));
+  const int row = rt * ROWS + r;
+  if (row >= p.rows) return;
+  const int row_token = row / p.group, limit = len - p.q_len + 1 + row_token;
+  const int64_t token = (int64_t)seq * p.q_len + row_token;
+  const int64_t at_out = token * a.ld_out + (int64_t)(kvh * p.group + row - row_token * p.group) * D;
+  float* const partial = p.direct && t.whole() ? nullptr : p.o + (((int64_t)t.tile + t.wg) * ROWS + r) * D;
   const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
-  const int* const list = a.table + row.seq * a.ld_table;
+  const int* const list = a.table + seq * a.ld_table;
+  // (the tile's rows are ROWS tokens apart at most)
 #pragma unroll 1
-  for (int block = max(least, 0) / STEP * (STEP / 16); 16 * block < most; ++block) {
+  for (int block = max(limit - ROWS, 0) / STEP * (STEP / 16); 16 * block < limit; ++block) {
     const int id = list[block >> page_blocks_shift];
     if ((unsigned)id >= (unsigned)a.c.n_pages) continue;
-    const int64_t at = (int64_t)((row.kvh << a.c.page_shift) + (block & page_blocks_mask) * 16) * a.c.dim;
+    const int64_t at = (int64_t)((kvh << a.c.page_shift) + (block & page_blocks_mask) * 16) * D;
     const uint8_t* const src = a.c.vc + (uint64_t)(unsigned)id * (uint64_t)a.c.ld_codes + at;
-    const int sees = row.limit - 16 * block;
+    const int sees = limit - 16 * block;
 #pragma unroll 1
-    for (int e = 0; e < 4 * (a.c.dim / row.stride); ++e) {
-      const int d = row.first + (e >> 2) * row.stride + (e & 3);
+    for (int e = 0; e < 4 * (D / stride); ++e) {
+      const int d = first + (e >> 2) * stride + (e & 3);
       const uint4 v = *reinterpret_cast<const uint4*>(src + d * 16);
       if (nan_bytes(make_uint4(v.x & keep_bytes(sees), v.y & keep_bytes(sees - 4), v.z & keep_bytes(sees - 8), v.w & keep_bytes(sees - 12))) == 0)
         continue;
       if (partial != nullptr) partial[d] = __builtin_nanf("");
-      else if constexpr (DT == NVFP4_DTYPE_BF16) ((uint16_t*)a.out)[row.token * a.ld_out + (int64_t)row.head * a.c.dim + d] = 0x7FC0;
-      else ((float*)a.out)[row.token * a.ld_out + (int64_t)row.head * a.c.dim + d] = __builtin_nanf("");
+      else if constexpr (DT == NVFP4_DTYPE_BF16) ((uint16_t*)a.out)[at_out + d] = 0x7FC0;
+      else ((float*)a.out)[at_out + d] = __builtin_nanf("");
     }
   }
 }
@@ -418,7 +429,8 @@ struct StreamLds {
 // SOLO: each wave has tiles of its own, from its queries to its result: for
 // many short tiles, where four waves to a tile would mostly wait for each
 // other and for the hand-over of their sums.
-template <int DT, int D, bool PAIR, bool SOLO>
+// OWN: the sequences' own tokens are among the pass's, not the shared prefix alone.
+template <int DT, int D, bool PAIR, bool SOLO, bool OWN>
 __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnArgs& a, const Pass& p, const int wg,
                                                                   const StreamLds<DT, D>& lds) {
   constexpr int T = kTerms<DT>;
@@ -428,6 +440,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
+  const int lane16 = 4 * (lane ^ 16), lane32 = 4 * (lane ^ 32);  // see from_lane
   const int prefix_steps = ceil_div(p.prefix_len, kStep);
   const int page_blocks_shift = a.c.page_shift - 4, page_blocks_mask = (1 << page_blocks_shift) - 1;
 
@@ -461,7 +474,8 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       }
     }
 
-    float m = kLowest, l = 0.0f;
+    Maximum most(a.scale_log2);
+    float l = 0.0f;
     f32x4 o[DT16];
 #pragma unroll
     for (int d = 0; d < DT16; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -594,7 +608,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
           vq[d].z &= keep[2];
           vq[d].w &= keep[3];
         }
-        if (!prefix && limit_first < limit_last && w.base + kStep > limit_first) {
+        if (OWN && !prefix && limit_first < limit_last && w.base + kStep > limit_first) {
           uint32_t any = 0;
           if constexpr (kLate) {  // (tested first, as below, it would spill 100 registers more)
 #pragma unroll
@@ -618,25 +632,21 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
 #pragma unroll
       for (int t = 1; t < 4; ++t) top = fmaxf(top, fmaxf(fmaxf(sc[t][0], sc[t][1]), fmaxf(sc[t][2], sc[t][3])));
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m)) {
-        const float f = __builtin_amdgcn_exp2f(m - mn);
+      top = fmaxf(top, from_lane(lane16, top));
+      top = fmaxf(top, from_lane(lane32, top));
+      if (__any(most.passed(top, 0.0f))) {
+        const float f = most.raise(a.scale_log2, top);
         l *= f;
 #pragma unroll
         for (int d = 0; d < DT16; ++d) o[d] *= f;
-        m = mn;
       }
-      float c = a.scale_log2, off = m;
-      if (__builtin_expect(__any(fabsf(m) >= kHuge), 0)) huge_exponents<4>(sc, c, off);
       float wt[16];
       const uint32_t vw[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][r], c, -off));
+          const float e = __builtin_amdgcn_exp2f(most.exponent(sc[t][r]));
           l += e;
           wt[4 * t + r] = e * byte_scale(vw[t], r);
         }
@@ -663,6 +673,7 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
       pv = pvn;
     }
 
+    float m = most.value(a.scale_log2);
     if (!SOLO && nan) *lds.nan_tile = tile;
 
     // Join the four waves, register by register: 2 and 3 hand theirs to 0 and
@@ -710,10 +721,9 @@ __device__ __attribute__((always_inline)) inline void stream_body(const KvAttnAr
           }
         }
       }
-      if (__builtin_expect(SOLO ? nan : __builtin_amdgcn_readfirstlane(*lds.nan_tile) == tile, 0)) {
-        if (row0 + i < p.rows)
-          put_nan<DT, kStep>(a, LaneRow{seq, kvh, head, limit, 4 * g, 16, token}, limit_first, limit_last, whole ? nullptr : p.o + at * D);
-      }
+      if constexpr (OWN)
+        if (__builtin_expect(SOLO ? nan : __builtin_amdgcn_readfirstlane(*lds.nan_tile) == tile, 0))
+          put_nan<DT, D, kTileRows, kStep>(a, p, t, i, 4 * g, 16);
     }
     if constexpr (!SOLO) __syncthreads();  // the queries and the hand-over are read
   } while (t.next(p));
@@ -731,7 +741,7 @@ __global__ __launch_bounds__(kThreads, (kPaired<DT, D>) ? 2 : 1) void kv_attenti
   __shared__ float ml[kWaves][32][2];
   __shared__ int64_t line[2 * kWaves];
   __shared__ int nan_tile;
-  stream_body<DT, D, kPaired<DT, D>, SOLO>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line, &nan_tile});
+  stream_body<DT, D, kPaired<DT, D>, SOLO, true>(a, p, blockIdx.x, StreamLds<DT, D>{part_a, part_b, q, ml, line, &nan_tile});
 }
 
 // The same for more rows (bf16): tiles of 32 * WM rows (WM = 1, 2; with D =
@@ -780,7 +790,7 @@ struct RowsLds {
   int* nan_tile;  // see StreamLds
 };
 
-template <int D, int WM>
+template <int D, int WM, bool OWN>  // OWN: see stream_body
 __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs& a, const Pass& p, const int wg, const RowsLds& lds) {
   typedef RowsShape<D, WM> C;
   constexpr int TT = C::kTT, D32 = C::kD32, PW = C::kPieces, NT = C::kTiles;
@@ -829,7 +839,8 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       return j < QR ? qf[j < QR ? j : 0] : __builtin_bit_cast(bf16x8, queries[(j < QR ? 0 : j - QR) * 64]);
     };
 
-    float m = kLowest, l = 0.0f;
+    Maximum most(a.scale_log2);
+    float l = 0.0f;
     floatx16 o[D32];
 #pragma unroll
     for (int d = 0; d < D32; ++d) o[d] = floatx16{};
@@ -839,7 +850,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       int base, n, all;  // the step's first token; tokens of the list that any row sees, that all rows of the tile see
     };
     auto where = [&](int s) __attribute__((always_inline)) {
-      if (s < prefix_steps) return Where{a.prefix_pages, s * C::kStepTokens, p.prefix_len, p.prefix_len};
+      if (!OWN || s < prefix_steps) return Where{a.prefix_pages, s * C::kStepTokens, p.prefix_len, p.prefix_len};
       return Where{a.table + seq * a.ld_table, (s - prefix_steps) * C::kStepTokens, limit_last, limit_tile};
     };
     // Step of this region in unit u; past the last one, that one again (so
@@ -906,7 +917,7 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       asm volatile("");  // a real branch: the steps that take it are few
       uint8_t* const values = stage + wt * (2 * C::kHalf) + C::kHalf + wm * PW * 1024 + lane * 16;
       uint32_t any = 0;
-      if (w.all < w.n && w.base + C::kStepTokens > w.all) {
+      if (OWN && w.all < w.n && w.base + C::kStepTokens > w.all) {
 #pragma unroll
         for (int k = 0; k < PW; ++k) any |= nan_bytes(*reinterpret_cast<const uint4*>(values + k * 1024));
         any = __any(any != 0);
@@ -997,23 +1008,19 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[t][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m + kSlack)) {
-        const float f = __builtin_amdgcn_exp2f(m - mn);
+      if (__any(most.passed(top, kSlack))) {
+        const float f = most.raise(a.scale_log2, top);
         l *= f;
 #pragma unroll
         for (int d = 0; d < D32; ++d) o[d] *= f;
-        m = mn;
       }
-      float c = a.scale_log2, off = m;
-      if (__builtin_expect(__any(fabsf(m) >= kHuge), 0)) huge_exponents<TT>(sc, c, off);
       bf16x8 pf[TT][2];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         float e[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          e[r] = __builtin_amdgcn_exp2f(fmaf(sc[t][r], c, -off));
+          e[r] = __builtin_amdgcn_exp2f(most.exponent(sc[t][r]));
           l += e[r];
         }
 #pragma unroll
@@ -1057,6 +1064,8 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
       }
       wait_vmem<0>();  // copies past the last unit
     }
+
+    float m = most.value(a.scale_log2);
 
     // Join the regions: waves of wt > 0 hand theirs to the wave of wt = 0
     // with the same rows (register by register).
@@ -1117,11 +1126,9 @@ __device__ __attribute__((always_inline)) inline void rows_body(const KvAttnArgs
           }
       }
     }
-    if (__builtin_expect(wt == 0 && __builtin_amdgcn_readfirstlane(*lds.nan_tile) == tile, 0)) {
-      if (row0 + r < p.rows)
-        put_nan<NVFP4_DTYPE_BF16, C::kStepTokens>(a, LaneRow{seq, kvh, kvh * p.group + row - row_token * p.group, limit, 4 * h, 8, token},
-                                                  limit_tile, limit_last, whole ? nullptr : p.o + at * D);
-    }
+    if constexpr (OWN)
+      if (__builtin_expect(wt == 0 && __builtin_amdgcn_readfirstlane(*lds.nan_tile) == tile, 0))
+        put_nan<NVFP4_DTYPE_BF16, D, C::kRows, C::kStepTokens>(a, p, t, r, 4 * h, 8);
     barrier_lds();
   } while (t.next(p));
 }
@@ -1135,7 +1142,7 @@ __global__ __launch_bounds__(kThreads, WM == 1 ? 1 : 2) void kv_attention_rows_k
   __shared__ int64_t line[2 * kWaves];
   __shared__ uint4 q[C::kQueriesLds * kWaves * 64 + 1];
   __shared__ int nan_tile;
-  rows_body<D, WM>(a, p, blockIdx.x, RowsLds{stages, scales, ml, line, q, &nan_tile});
+  rows_body<D, WM, true>(a, p, blockIdx.x, RowsLds{stages, scales, ml, line, q, &nan_tile});
 }
 
 // Tiles of 128 rows, D <= 128: the four waves own 32 each and all work on the same
@@ -1166,7 +1173,7 @@ struct WideLds {
   int* nan_tile;            // see StreamLds; [2], tiles in turn
 };
 
-template <int D>
+template <int D, bool OWN>  // OWN: see stream_body
 __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs& a, const Pass& p, const int wg, const WideLds& lds) {
   typedef WideShape<D> C;
   static_assert(D <= 128, "no registers for wider heads");
@@ -1207,7 +1214,8 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
         qf[j] = *reinterpret_cast<const bf16x8*>((const uint16_t*)a.q + at + (j >> 1) * 32 + 8 * (j & 1));
     }
 
-    float m = kLowest, l = 0.0f;
+    Maximum most(a.scale_log2);
+    float l = 0.0f;
     floatx16 o[D32];
 #pragma unroll
     for (int d = 0; d < D32; ++d) o[d] = floatx16{};
@@ -1218,7 +1226,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
     };
     auto where = [&](int u) __attribute__((always_inline)) {
       const int s = min(u, steps - 1);
-      if (s < prefix_steps) return Where{a.prefix_pages, s * ST, p.prefix_len, p.prefix_len};
+      if (!OWN || s < prefix_steps) return Where{a.prefix_pages, s * ST, p.prefix_len, p.prefix_len};
       return Where{a.table + seq * a.ld_table, (s - prefix_steps) * ST, limit_last, limit_tile};
     };
     auto block_of = [&](const Where& w, int b) { return min((w.base >> 4) + b, (w.n - 1) >> 4); };
@@ -1278,7 +1286,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
       const bool gone = __any(value_gone);
       if (!gone && w.base + ST <= w.all) return;
       uint32_t any = 0;
-      if (w.all < w.n && w.base + ST > w.all) {
+      if (OWN && w.all < w.n && w.base + ST > w.all) {
 #pragma unroll
         for (int k = 0; k < PW; ++k) any |= nan_bytes(vraw[k]);
         any = __any(any != 0);
@@ -1376,20 +1384,16 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float mn = fmaxf(m, top * a.scale_log2);
-      if (__any(mn > m + kSlack)) {
-        const float f = __builtin_amdgcn_exp2f(m - mn);
+      if (__any(most.passed(top, kSlack))) {
+        const float f = most.raise(a.scale_log2, top);
         l *= f;
 #pragma unroll
         for (int d = 0; d < D32; ++d) o[d] *= f;
-        m = mn;
       }
-      float c = a.scale_log2, off = m;
-      if (__builtin_expect(__any(fabsf(m) >= kHuge), 0)) huge_exponents<TT>(sc, c, off);
       uint32_t pf[TT][8];  // pairs of weights as bf16
       auto weight_pair = [&](int k, int r) __attribute__((always_inline)) {
-        const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[k][r], c, -off));
-        const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[k][r + 1], c, -off));
+        const float e0 = __builtin_amdgcn_exp2f(most.exponent(sc[k][r]));
+        const float e1 = __builtin_amdgcn_exp2f(most.exponent(sc[k][r + 1]));
         l += e0;
         l += e1;
         pf[k][r >> 1] = pack_bf16x2(e0 * vs[k][r >> 2][r & 3], e1 * vs[k][r >> 2][(r & 3) + 1]);
@@ -1454,6 +1458,7 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
       nan = __builtin_amdgcn_readfirstlane(lds.nan_tile[turn]) == tile;
       turn ^= 1;  // (a wave is at most one tile with a step ahead of the others)
     }
+    const float m = most.value(a.scale_log2);
 
     l += __shfl_xor(l, 32);
     const int r = 32 * wave + i;  // row of the tile
@@ -1479,11 +1484,8 @@ __device__ __attribute__((always_inline)) inline void wide_body(const KvAttnArgs
           }
       }
     }
-    if (__builtin_expect(nan, 0)) {
-      if (row0 + r < p.rows)
-        put_nan<NVFP4_DTYPE_BF16, ST>(a, LaneRow{seq, kvh, kvh * p.group + row - row_token * p.group, limit, 4 * h, 8, token},
-                                      limit_tile, limit_last, whole ? nullptr : p.o + at * D);
-    }
+    if constexpr (OWN)
+      if (__builtin_expect(nan, 0)) put_nan<NVFP4_DTYPE_BF16, D, C::kRows, ST>(a, p, t, r, 4 * h, 8);
   } while (t.next(p));
 }
 
@@ -1495,7 +1497,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
   __shared__ uint64_t bad[2];
   __shared__ int64_t line[2 * kWaves];
   __shared__ int nan_tile[2];
-  wide_body<D>(a, p, blockIdx.x, WideLds{stages, scales, bad, line, nan_tile});
+  wide_body<D, true>(a, p, blockIdx.x, WideLds{stages, scales, bad, line, nan_tile});
 }
 
 // The shared prefix and the sequences' own tokens in one launch: the first is
@@ -1554,13 +1556,13 @@ __global__ __launch_bounds__(kThreads, DT == NVFP4_DTYPE_BF16 ? 2 : 1) void kv_a
   }
   const StreamLds<DT, D> stream{(float*)stages, (float*)(stages + kPart), (uint4*)(stages + 2 * kPart), ml, line, nan_tile};
   if (!first) {
-    stream_body<DT, D, DT == NVFP4_DTYPE_BF16, SOLO>(a, own, wg, stream);
+    stream_body<DT, D, DT == NVFP4_DTYPE_BF16, SOLO, true>(a, own, wg, stream);
   } else if constexpr (WM == 0) {
-    stream_body<DT, D, DT == NVFP4_DTYPE_BF16, false>(a, shared, wg, stream);
+    stream_body<DT, D, DT == NVFP4_DTYPE_BF16, false, false>(a, shared, wg, stream);
   } else if constexpr (kWide) {
-    wide_body<D>(a, shared, wg, WideLds{stages, scales[0], bad, line, nan_tile});
+    wide_body<D, false>(a, shared, wg, WideLds{stages, scales[0], bad, line, nan_tile});
   } else {
-    rows_body<D, WM>(a, shared, wg, RowsLds{stages, scales, ml, line, q, nan_tile});
+    rows_body<D, WM, false>(a, shared, wg, RowsLds{stages, scales, ml, line, q, nan_tile});
   }
 }
 
@@ -1649,9 +1651,10 @@ __global__ __launch_bounds__(kThreads) void kv_attention_join_kernel(KvAttnArgs 
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          if (wq[b] == 0.0f)
+          if (__builtin_expect(__any(__float_as_uint(wq[b]) == 0x80000000u), 0)) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) v[b][x] = v[b][x] == v[b][x] ? 0.0f : v[b][x];
+            for (int x = 0; x < 4; ++x) v[b][x] = wq[b] == 0.0f && v[b][x] == v[b][x] ? 0.0f : v[b][x];
+          }
           acc += v[b] * wq[b];
         }
       }
