@@ -1153,7 +1153,10 @@ __global__ __launch_bounds__(kThreads, WM == 1 ? 1 : 2) void kv_attention_rows_k
 // tokens) of the values, 1 KB each, lane l's 8 values at 16 l.  The bytes go
 // through registers: asked for a step ahead, converted after the step's
 // products, one barrier a step.  (With D = 256 the accumulators and queries
-// take 192 of 256 registers and this form spills; it stays with rows_body.)
+// take 192 of 256 registers, and this form spills 120; it stays with rows_body.
+// That spills too there: 14 registers with 128 rows, none of them used within a
+// step, 35 with 64 rows, of which a step reloads 7, behind the copies of the
+// next one; in the joint launch 34 to 64.)
 template <int D>
 struct WideShape {
   static constexpr int kTT = 2;                           // 32-token tiles of a step
@@ -1507,7 +1510,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_wide_kernel(KvAttnAr
 // both passes take, which depends on the lengths: so the workgroups divide it
 // themselves, each finding the same number.  The two kinds are spread among
 // each other by eights, since workgroups are dealt to the 8 XCDs in turn.
-// (64 sequences of 64 to 1024 tokens after 16384, 256 dimensions: 69 us and join;
+// (64 sequences of 64 to 1024 tokens after 16384, 256 dimensions: 66 us and join;
 // divided on the host for half of the longest length, with further own
 // workgroups that follow as places became free, 71 to 84 from run to run.)
 // WM = 0: 16-row tiles for the prefix as well.

@@ -538,7 +538,10 @@ size_t nvfp4_kv_pages_attention_workspace_bytes(const nvfp4_kv_pages* cache, con
  * Products of bf16 queries are exact, sums and the softmax are float32; with NVFP4_DTYPE_
  * BF16 each softmax weight enters its product with the values rounded to
  * bf16, with NVFP4_DTYPE_F32 queries and weights enter as three bf16 terms
- * (24 bits).  The result does not depend on timing: the same call on the same
+ * (24 bits).  Numbers that leave the normal range on the way are not held to
+ * that: a weight times a value's scale below 2^-126 loses bits (values below
+ * about 2^-103 in float32 work, 2^-113 with bf16), and sums of values beyond
+ * about 2^110 may overflow.  The result does not depend on timing: the same call on the same
  * data gives the same bits.  1 <= q_len, batch * q_len < 2^30 / q_heads,
  * max_len and prefix_len < 2^30, batch * kv_heads < 2^24; q_heads a multiple
  * of kv_heads.  At most three launches.  batch = 0 is a valid call that does

@@ -109,3 +109,28 @@ def test_large_scores_with_a_shared_prefix(case, power, sign):
             seen = torch.cat([torch.ones_like(f, dtype=torch.bool), torch.arange(n, device=DEV) < n - s.q_len + 1 + j])
             want, scale, k = mean_of_the_best(torch.cat([f, own]), values, seen, sign)
             check(out[b, j], want[:, None], scale[:, None], k, s.dtype)
+
+
+@pytest.mark.parametrize("q_len,dtype", [(1, BF16), (5, F32), (20, BF16), (40, BF16), (80, BF16)])
+def test_a_tiny_scale(q_len, dtype):
+    """scale as small as a float: every token that a row sees has the same
+    weight, and a row that sees none gets zeros beside rows that do."""
+    say(f"kv attention tiny scale {q_len} {dtype}")
+    dim, n = 64, q_len - 3 if q_len > 3 else 50
+    g = torch.Generator(device=DEV).manual_seed(73)
+    pages = nv.empty_kv_pages(8, 1, dim, 16)
+    slots = torch.arange(n, device=DEV)
+    k, v = (torch.randn((n, dim), generator=g, device=DEV) for _ in range(2))
+    nv.kv_pages_write(pages, k, v, slots)
+    values = nv.kv_pages_read(pages, slots, F32)[1].double()
+    q = torch.randn((q_len, dim), generator=g, device=DEV).to(dtype)
+    table = torch.arange(8, device=DEV).int()[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    for scale in (1e-12, 1e-20, 1e-30, 1e-38, 1e-45):
+        out = nv.kv_pages_attention(q, pages, table, lens, q_len=q_len, scale=scale)
+        for j in range(q_len):
+            seen = n - q_len + 1 + j
+            if seen <= 0:
+                assert torch.all(out[j] == 0)
+            else:
+                check(out[j], values[:seen].mean(0), values[:seen].abs().mean(0), seen, dtype)
