@@ -59,3 +59,22 @@ def test_one_page_of_a_padded_buffer(pad):
         for got, w in zip(nv.kv_pages_read(pages, slots), want):
             assert torch.equal(got, w)
     assert all(torch.all(t[1:] == 0xFF) for t in tensors)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_calls_with_nothing_in_them(dtype):
+    """No rows, no sequences, a table without pages, nothing to attend to."""
+    say(f"kv empty calls {dtype}")
+    pages = nv.empty_kv_pages(3, 2, 64, 16)
+    for t in (pages.k_codes, pages.v_codes, pages.k_scales, pages.v_scales):
+        t.fill_(0xFF)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    empty, slots = torch.empty((0, 128), dtype=dtype, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV)
+    nv.kv_pages_write(pages, empty, empty, slots)
+    assert [tuple(t.shape) for t in nv.kv_pages_read(pages, slots, dtype)] == [(0, 128)] * 2
+    assert nv.kv_pages_attention(torch.empty((0, 256), dtype=dtype, device=DEV), pages, none.view(0, 1)[:, :0], none).shape == (0, 256)
+    q = torch.ones((4, 256), dtype=dtype, device=DEV)
+    assert torch.all(nv.kv_pages_attention(q, pages, q_len=2) == 0)
+    lens = torch.zeros(4, dtype=torch.int32, device=DEV)
+    assert torch.all(nv.kv_pages_attention(q, pages, torch.zeros((4, 0), dtype=torch.int32, device=DEV), lens) == 0)
+    assert torch.all(nv.kv_pages_attention(q, pages, torch.zeros((4, 2), dtype=torch.int32, device=DEV), lens) == 0)
