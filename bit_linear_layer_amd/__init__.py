@@ -25,11 +25,15 @@ __all__ = [
     "KVPages", "empty_kv_pages", "nvfp4_kv_pages_write", "nvfp4_kv_pages_read", "nvfp4_kv_pages_attention",
     "nvfp4_kv_pages_attention_workspace_bytes", "kv_pages_write", "kv_pages_read", "kv_pages_attention",
     "kv_pages_attention_workspace",
+    "FP8Tensor", "empty_fp8", "nvfp4_fp8_quantize", "nvfp4_fp8_gemm", "nvfp4_fp8_linear", "nvfp4_fp8_linear_workspace_bytes",
+    "fp8_quantize", "fp8_gemm", "fp8_linear", "fp8_linear_workspace", "Rope", "nvfp4_qk_norm_rope", "qk_norm_rope",
+    "nvfp4_causal_conv", "causal_conv", "nvfp4_gdn_step", "gdn_step", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "DTYPE_BF16", "DTYPE_F32", "SCALE_DYNAMIC", "SCALE_STATIC", "AMAX_PRECOMPUTED", "MAX_SEGMENTS",
 ]
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 SCALE_DYNAMIC, SCALE_STATIC, AMAX_PRECOMPUTED = 0, 1, 2
+FP8_SCALE_F32, FP8_SCALE_POW2 = 0, 1
 MAX_SEGMENTS = 16
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4.so")
@@ -72,6 +76,29 @@ class _KVBatch(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("q_len", ctypes.c_int64), ("lens", ctypes.c_void_p),
                 ("max_len", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_cols", ctypes.c_int64),
                 ("ld_table", ctypes.c_int64), ("prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int64)]
+
+
+class _FP8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld_codes", ctypes.c_int64), ("ld_scales", ctypes.c_int64), ("block_rows", ctypes.c_int)]
+
+
+class _HeadRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("head_x", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("ld_out", ctypes.c_int64), ("head_out", ctypes.c_int64), ("weight", ctypes.c_void_p), ("heads", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("ld_positions", ctypes.c_int64), ("inv_freq", ctypes.c_void_p),
+                ("axis", ctypes.c_void_p), ("axes", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class _Conv(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("batch", ctypes.c_int64), ("width", ctypes.c_int), ("silu", ctypes.c_int), ("starts", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("n_states", ctypes.c_int64), ("ld_state", ctypes.c_int64),
+                ("slots", ctypes.c_void_p), ("fresh", ctypes.c_void_p)]
 
 
 _lib = None
@@ -143,6 +170,24 @@ def load() -> ctypes.CDLL:
         lib.nvfp4_kv_pages_attention.argtypes = [pages, batch, _P, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_float, _P,
                                                  _I64, _P, ctypes.c_size_t, _P]
         lib.nvfp4_kv_pages_attention.restype = ctypes.c_int
+        fp8 = ctypes.POINTER(_FP8)
+        lib.nvfp4_fp8_quantize.argtypes = [_P, ctypes.c_int, _I64, fp8, ctypes.c_int, _P]
+        lib.nvfp4_fp8_quantize.restype = ctypes.c_int
+        lib.nvfp4_fp8_gemm.argtypes = [fp8, fp8, _P, ctypes.c_int, _I64, _P]
+        lib.nvfp4_fp8_gemm.restype = ctypes.c_int
+        lib.nvfp4_fp8_linear_workspace_bytes.argtypes = [_I64, _I64]
+        lib.nvfp4_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
+        lib.nvfp4_fp8_linear.argtypes = [_P, ctypes.c_int, _I64, _I64, fp8, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
+        lib.nvfp4_fp8_linear.restype = ctypes.c_int
+        heads = ctypes.POINTER(_HeadRows)
+        lib.nvfp4_qk_norm_rope.argtypes = [heads, heads, ctypes.c_int, _I64, ctypes.c_int, ctypes.c_float, ctypes.c_float,
+                                           ctypes.POINTER(_Rope), _P]
+        lib.nvfp4_qk_norm_rope.restype = ctypes.c_int
+        lib.nvfp4_causal_conv.argtypes = [ctypes.POINTER(_Conv), ctypes.c_int, _P]
+        lib.nvfp4_causal_conv.restype = ctypes.c_int
+        lib.nvfp4_gdn_step.argtypes = [ctypes.POINTER(_GdnInputs), ctypes.c_int, _I64, _I64, ctypes.c_int, ctypes.c_int,
+                                       ctypes.c_int, _P, _I64, _I64, _P, _P, _P, ctypes.c_int, _I64, _P]
+        lib.nvfp4_gdn_step.restype = ctypes.c_int
         lib.nvfp4_status_string.argtypes = [ctypes.c_int]
         lib.nvfp4_status_string.restype = ctypes.c_char_p
         lib.nvfp4_version.argtypes = []
@@ -638,6 +683,231 @@ def nvfp4_kv_pages_attention(q: torch.Tensor, pages: KVPages, out: torch.Tensor,
                     workspace.nbytes), "nvfp4_kv_pages_attention")
 
 
+@dataclass
+class FP8Tensor:
+    """An E4M3 matrix [rows, cols] with a float32 scale per block of
+    block_rows (1 or 128) x 128: codes uint8 [rows, >= cols], scales
+    [ceil(rows / block_rows), >= ceil(cols / 128)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+    block_rows: int = 1
+
+    def descriptor(self) -> _FP8:
+        c, s, rows, cols = self.codes, self.scales, self.rows, self.cols
+        high, wide = -(-rows // self.block_rows) if self.block_rows > 0 else 0, -(-cols // 128)
+        if c.dtype is not torch.uint8 or c.dim() != 2 or c.shape[0] != rows or c.shape[1] < cols or c.stride(1) != 1:
+            raise NVFP4Error(f"codes must be uint8 [{rows}, >= {cols}] with contiguous rows")
+        if s.dtype is not torch.float32 or s.dim() != 2 or s.shape[0] != high or s.shape[1] < wide or s.stride(1) != 1:
+            raise NVFP4Error(f"scales must be float32 [{high}, >= {wide}] with contiguous rows")
+        if c.device.type != "cuda" or s.device != c.device:
+            raise NVFP4Error("codes and scales must live on one GPU")
+        return _FP8(c.data_ptr(), s.data_ptr(), rows, cols, c.stride(0) if rows > 1 else _round_up(cols, 16),
+                    s.stride(0) if high > 1 else wide, self.block_rows)
+
+
+def empty_fp8(rows: int, cols: int, block_rows: int = 1, device="cuda") -> FP8Tensor:
+    """An uninitialized E4M3 matrix."""
+    return FP8Tensor(torch.empty((rows, _round_up(cols, 16)), dtype=torch.uint8, device=device),
+                     torch.empty((-(-rows // block_rows), -(-cols // 128)), dtype=torch.float32, device=device),
+                     rows, cols, block_rows)
+
+
+def nvfp4_fp8_quantize(x: torch.Tensor, q: FP8Tensor, flags: int = FP8_SCALE_F32, stream=None) -> None:
+    """C ``nvfp4_fp8_quantize``: x (bf16 or float32, rows may be strided) into q."""
+    d, device = q.descriptor(), q.codes.device
+    ld = _row_stride(x, q.rows, q.cols, device, "x")
+    _check(_call_on(device, stream, load().nvfp4_fp8_quantize, x.data_ptr(), _dtype_code(x), ld, ctypes.byref(d), flags),
+           "nvfp4_fp8_quantize")
+
+
+def nvfp4_fp8_gemm(a: FP8Tensor, w: FP8Tensor, out: torch.Tensor, stream=None) -> None:
+    """C ``nvfp4_fp8_gemm``: out[M, N] = A W^T, a by rows, w by blocks of 128 rows."""
+    da, dw, device = a.descriptor(), w.descriptor(), w.codes.device
+    _on(a.codes, device, "a")
+    ld = _row_stride(out, a.rows, w.rows, device, "out")
+    _check(_call_on(device, stream, load().nvfp4_fp8_gemm, ctypes.byref(da), ctypes.byref(dw), out.data_ptr(), _dtype_code(out),
+                    ld), "nvfp4_fp8_gemm")
+
+
+def nvfp4_fp8_linear_workspace_bytes(rows: int, cols: int) -> int:
+    """C ``nvfp4_fp8_linear_workspace_bytes``; 0 for a shape that the layer does not take."""
+    return int(load().nvfp4_fp8_linear_workspace_bytes(rows, cols))
+
+
+def nvfp4_fp8_linear(x: torch.Tensor, w: FP8Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """C ``nvfp4_fp8_linear``: x [rows, w.cols] (bf16 or float32) quantized by
+    rows and multiplied with w into out [rows, w.rows]."""
+    d, device = w.descriptor(), w.codes.device
+    if x.dim() != 2:
+        raise NVFP4Error(f"x must be [rows, {w.cols}], got {list(x.shape)}")
+    rows = x.shape[0]
+    ld_x, ld_o = _row_stride(x, rows, w.cols, device, "x"), _row_stride(out, rows, w.rows, device, "out")
+    if not workspace.is_contiguous():
+        raise NVFP4Error("workspace must be contiguous")
+    _on(workspace, device, "workspace")
+    _check(_call_on(device, stream, load().nvfp4_fp8_linear, x.data_ptr(), _dtype_code(x), rows, ld_x, ctypes.byref(d),
+                    out.data_ptr(), _dtype_code(out), ld_o, workspace.data_ptr(), workspace.nbytes), "nvfp4_fp8_linear")
+
+
+@dataclass
+class Rope:
+    """The rotation of ``nvfp4_qk_norm_rope``: float32 inv_freq [rotary_dim /
+    2], and with more than one position axis the uint8 axis of each pair;
+    interleaved: pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)."""
+    inv_freq: torch.Tensor
+    axis: torch.Tensor | None = None
+    interleaved: bool = False
+
+    def descriptor(self, positions: torch.Tensor, tokens: int, device: torch.device) -> _Rope:
+        f, axis = self.inv_freq, self.axis
+        if f.dtype is not torch.float32 or f.dim() != 1 or not f.is_contiguous():
+            raise NVFP4Error("inv_freq must be a contiguous 1-D float32 tensor")
+        _on(f, device, "inv_freq")
+        if axis is not None:
+            if axis.dtype is not torch.uint8 or axis.shape != f.shape or not axis.is_contiguous():
+                raise NVFP4Error(f"axis must be a contiguous uint8 [{f.shape[0]}] tensor")
+            _on(axis, device, "axis")
+        if positions.dtype is not torch.int64 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens \
+                or tokens > 1 and positions.stride(-1) != 1:
+            raise NVFP4Error(f"positions must be int64 [{tokens}] or [axes, {tokens}] with contiguous rows")
+        _on(positions, device, "positions")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if axis is None and axes != 1:
+            raise NVFP4Error("positions with more than one axis need a Rope with axis")
+        ld = positions.stride(0) if positions.dim() == 2 and axes > 1 else tokens
+        return _Rope(positions.data_ptr(), ld, f.data_ptr(), _ptr(axis), axes, 2 * f.shape[0], int(self.interleaved))
+
+
+def _heads_of(x: torch.Tensor, tokens: int, head_dim: int, device: torch.device, what: str):
+    """(heads, row stride, head stride) of [tokens, heads * head_dim] or [tokens, heads, head_dim]."""
+    if x.dim() == 3:
+        if x.shape[0] != tokens or x.shape[2] != head_dim or x.shape[1] == 0 or x.stride(2) != 1:
+            raise NVFP4Error(f"{what} must be [{tokens}, heads, {head_dim}] with contiguous heads, got {list(x.shape)}")
+        _on(x, device, what)
+        heads, head = x.shape[1], x.stride(1) if x.shape[1] > 1 else head_dim
+        return heads, x.stride(0) if tokens > 1 else (heads - 1) * head + head_dim, head
+    if x.dim() != 2 or x.shape[1] == 0 or x.shape[1] % head_dim != 0:
+        raise NVFP4Error(f"{what} must be [{tokens}, heads * {head_dim}], got {list(x.shape)}")
+    return x.shape[1] // head_dim, _row_stride(x, tokens, x.shape[1], device, what), head_dim
+
+
+def _head_rows(x, out, weight, tokens: int, head_dim: int, dtype, device: torch.device, what: str):
+    if x is None:
+        return None
+    if out is None or out.shape != x.shape or x.dtype != dtype or out.dtype != dtype:
+        raise NVFP4Error(f"{what} and its output must share shape and dtype, queries and keys one dtype")
+    heads, ld, head = _heads_of(x, tokens, head_dim, device, what)
+    _, ld_o, head_o = _heads_of(out, tokens, head_dim, device, what + "_out")
+    if weight is not None:
+        if weight.dtype is not torch.float32 or weight.shape != (head_dim,) or not weight.is_contiguous():
+            raise NVFP4Error(f"the weight of {what} must be a contiguous float32 [{head_dim}] tensor")
+        _on(weight, device, f"the weight of {what}")
+    return ctypes.byref(_HeadRows(x.data_ptr(), ld, head, out.data_ptr(), ld_o, head_o, _ptr(weight), heads))
+
+
+def nvfp4_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None, k_out: torch.Tensor | None,
+                       head_dim: int, positions: torch.Tensor | None = None, rope: Rope | None = None,
+                       q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                       weight_offset: float = 0.0, stream=None) -> None:
+    """C ``nvfp4_qk_norm_rope``: q and k (either may be None) [tokens, heads *
+    head_dim] or [tokens, heads, head_dim], any row and head stride; the
+    outputs may be the inputs; positions int64 [tokens] or [axes, tokens]."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise NVFP4Error("one of q and k is needed")
+    tokens, device = lead.shape[0], lead.device
+    if device.type != "cuda":
+        raise NVFP4Error("q and k must live on a GPU")
+    dt = _dtype_code(lead)
+    if (rope is None) != (positions is None):
+        raise NVFP4Error("rope and positions come together")
+    hq = _head_rows(q, q_out, q_weight, tokens, head_dim, lead.dtype, device, "q")
+    hk = _head_rows(k, k_out, k_weight, tokens, head_dim, lead.dtype, device, "k")
+    r = None if rope is None else ctypes.byref(rope.descriptor(positions, tokens, device))
+    _check(_call_on(device, stream, load().nvfp4_qk_norm_rope, hq, hk, dt, tokens, head_dim, eps, weight_offset, r),
+           "nvfp4_qk_norm_rope")
+
+
+def _per_sequence(t: torch.Tensor | None, n: int, dtype, device: torch.device, what: str):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise NVFP4Error(f"{what} must be a contiguous {str(dtype)[6:]} [{n}] tensor")
+    _on(t, device, what)
+    return t.data_ptr()
+
+
+def nvfp4_causal_conv(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, batch: int, starts: torch.Tensor | None = None,
+                      bias: torch.Tensor | None = None, silu: bool = True, state: torch.Tensor | None = None,
+                      slots: torch.Tensor | None = None, fresh: torch.Tensor | None = None, stream=None) -> None:
+    """C ``nvfp4_causal_conv``: x and y [tokens, channels] (rows may be
+    strided); weight float32 [channels, width]; starts int32 [batch + 1] or
+    None (tokens / batch rows each); state [n_states, width - 1, channels] of
+    x's dtype, updated in place; slots int32, fresh uint8 [batch]."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise NVFP4Error("x must be [tokens, channels], weight [channels, width]")
+    (tokens, channels), device = x.shape, x.device
+    if device.type != "cuda":
+        raise NVFP4Error("x must live on a GPU")
+    width = weight.shape[1]
+    ld_x, ld_y = _row_stride(x, tokens, channels, device, "x"), _row_stride(y, tokens, channels, device, "y")
+    if weight.dtype is not torch.float32 or weight.shape[0] != channels or not weight.is_contiguous():
+        raise NVFP4Error(f"weight must be a contiguous float32 [{channels}, width] tensor")
+    _on(weight, device, "weight")
+    if y.dtype != x.dtype:
+        raise NVFP4Error("y must have x's dtype")
+    n_states = ld_state = 0
+    if state is not None:
+        if state.dtype != x.dtype or state.dim() != 3 or state.shape[1:] != (width - 1, channels) \
+                or state.shape[0] == 0 or not state[0].is_contiguous():
+            raise NVFP4Error(f"state must be [n_states, {width - 1}, {channels}] of x's dtype, each state contiguous")
+        _on(state, device, "state")
+        n_states = state.shape[0]
+        ld_state = state.stride(0) if n_states > 1 else (width - 1) * channels
+    elif slots is not None or fresh is not None:
+        raise NVFP4Error("slots and fresh need a state")
+    i32 = torch.int32
+    c = _Conv(x.data_ptr(), ld_x, y.data_ptr(), ld_y, weight.data_ptr(), _per_sequence(bias, channels, torch.float32, device, "bias"),
+              tokens, channels, batch, width, int(silu), _per_sequence(starts, batch + 1, i32, device, "starts"), _ptr(state),
+              n_states, ld_state, _per_sequence(slots, batch, i32, device, "slots"),
+              _per_sequence(fresh, batch, torch.uint8, device, "fresh"))
+    _check(_call_on(device, stream, load().nvfp4_causal_conv, ctypes.byref(c), _dtype_code(x)), "nvfp4_causal_conv")
+
+
+def nvfp4_gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, g: torch.Tensor, o: torch.Tensor,
+                   k_heads: int, v_heads: int, states: torch.Tensor, slots: torch.Tensor | None = None, q_len: int = 1,
+                   normalize_qk: bool = True, fresh: torch.Tensor | None = None, stream=None) -> None:
+    """C ``nvfp4_gdn_step``: the next q_len tokens of each sequence; inputs as
+    ``nvfp4_gdn_recurrence`` takes them, [batch * q_len, ...]; states float32
+    [n_states, v_heads, 128, 128], updated in place; slots int32, fresh uint8
+    [batch]."""
+    if q.dim() != 2 or q_len < 1 or q.shape[0] % q_len != 0:
+        raise NVFP4Error(f"q must be [batch * {q_len}, {k_heads * 128}], got {list(q.shape)}")
+    rows, device, dt = q.shape[0], q.device, _dtype_code(q)
+    if device.type != "cuda":
+        raise NVFP4Error("q must live on a GPU")
+    batch = rows // q_len
+    if any(t.dtype != q.dtype for t in (k, v, beta, g)):
+        raise NVFP4Error("q, k, v, beta and g must share one dtype")
+    ins = []
+    for name, t, width in (("q", q, k_heads * 128), ("k", k, k_heads * 128), ("v", v, v_heads * 128), ("beta", beta, v_heads),
+                           ("g", g, v_heads)):
+        ins += [t.data_ptr(), _row_stride(t, rows, width, device, name)]
+    ld_o = _row_stride(o, rows, v_heads * 128, device, "o")
+    if states.dtype is not torch.float32 or states.dim() != 4 or states.shape[1:] != (v_heads, 128, 128) \
+            or states.shape[0] > 0 and not states[0].is_contiguous():
+        raise NVFP4Error(f"states must be float32 [n_states, {v_heads}, 128, 128], each state contiguous")
+    _on(states, device, "states")
+    ld_s = states.stride(0) if states.shape[0] > 1 else v_heads * 16384
+    _check(_call_on(device, stream, load().nvfp4_gdn_step, ctypes.byref(_GdnInputs(*ins)), dt, batch, q_len, k_heads, v_heads,
+                    int(normalize_qk), states.data_ptr(), states.shape[0], ld_s,
+                    _per_sequence(slots, batch, torch.int32, device, "slots"),
+                    _per_sequence(fresh, batch, torch.uint8, device, "fresh"), o.data_ptr(), _dtype_code(o), ld_o),
+           "nvfp4_gdn_step")
+
+
 # ----------------------------------------------------------- conveniences
 
 def quantize(x: torch.Tensor, static_scale: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -803,4 +1073,66 @@ def kv_pages_attention(q: torch.Tensor, pages: KVPages, table: torch.Tensor | No
     o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
     nvfp4_kv_pages_attention(q, pages, o, workspace, pages.head_dim ** -0.5 if scale is None else scale, batch, q_len, table,
                              lens, max_len, prefix_pages, prefix_len)
+    return o
+
+
+def fp8_quantize(x: torch.Tensor, block_rows: int = 1, flags: int = FP8_SCALE_F32, out: FP8Tensor | None = None) -> FP8Tensor:
+    """E4M3 codes and block scales of x: block_rows 1 for activations, 128 for a weight."""
+    if x.dim() != 2 or block_rows not in (1, 128):
+        raise NVFP4Error("x must be [rows, cols], block_rows 1 or 128")
+    q = out if out is not None else empty_fp8(x.shape[0], x.shape[1], block_rows, x.device)
+    nvfp4_fp8_quantize(x, q, flags)
+    return q
+
+
+def fp8_gemm(a: FP8Tensor, w: FP8Tensor, out_dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    o = out if out is not None else torch.empty((a.rows, w.rows), dtype=out_dtype, device=a.codes.device)
+    nvfp4_fp8_gemm(a, w, o)
+    return o
+
+
+def fp8_linear_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """A workspace for ``fp8_linear`` calls of up to ``rows`` rows."""
+    n = nvfp4_fp8_linear_workspace_bytes(rows, cols)
+    if n == 0:
+        raise NVFP4Error(f"the layer does not take [{rows}, {cols}] activations")
+    return torch.empty((n + 3) // 4, dtype=torch.float32, device=device)
+
+
+def fp8_linear(x: torch.Tensor, w: FP8Tensor, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """x [rows, w.cols] through the E4M3 layer w (see ``nvfp4_fp8_linear``)."""
+    if x.dim() != 2:
+        raise NVFP4Error(f"x must be [rows, {w.cols}], got {list(x.shape)}")
+    ws = workspace if workspace is not None else fp8_linear_workspace(x.shape[0], w.cols, x.device)
+    o = out if out is not None else torch.empty((x.shape[0], w.rows), dtype=out_dtype, device=x.device)
+    nvfp4_fp8_linear(x, w, o, ws)
+    return o
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, head_dim: int, positions: torch.Tensor | None = None, rope: Rope | None = None,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 weight_offset: float = 0.0):
+    """(queries, keys), normed per head and rotated, as new contiguous tensors."""
+    q_out, k_out = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    nvfp4_qk_norm_rope(q, k, q_out, k_out, head_dim, positions, rope, q_weight, k_weight, eps, weight_offset)
+    return q_out, k_out
+
+
+def causal_conv(x: torch.Tensor, weight: torch.Tensor, batch: int = 1, starts: torch.Tensor | None = None,
+                bias: torch.Tensor | None = None, silu: bool = True, state: torch.Tensor | None = None,
+                slots: torch.Tensor | None = None, fresh: torch.Tensor | None = None) -> torch.Tensor:
+    """The short convolution of x (see ``nvfp4_causal_conv``); rows that belong to no sequence are unspecified."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    nvfp4_causal_conv(x, weight, y, batch, starts, bias, silu, state, slots, fresh)
+    return y
+
+
+def gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, g: torch.Tensor, k_heads: int, v_heads: int,
+             states: torch.Tensor, slots: torch.Tensor | None = None, q_len: int = 1, normalize_qk: bool = True,
+             fresh: torch.Tensor | None = None, out_dtype=torch.float32) -> torch.Tensor:
+    """Outputs [batch * q_len, v_heads * 128] (see ``nvfp4_gdn_step``); rows of
+    places that hold no sequence are unspecified."""
+    o = torch.empty((q.shape[0], v_heads * 128), dtype=out_dtype, device=q.device)
+    nvfp4_gdn_step(q, k, v, beta, g, o, k_heads, v_heads, states, slots, q_len, normalize_qk, fresh)
     return o

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "gemm_skinny.hip", "gemm_decode.hip", "glue.hip", "kv_fp8.hip", "harmonize.hip",
-           "gdn.hip", "noalloc.hip", "kv_pages.hip", "kv_attention.hip", "kv_pages_api.hip"]
+           "gdn.hip", "noalloc.hip", "kv_pages.hip", "kv_attention.hip", "kv_pages_api.hip",
+           "fp8_quant.hip", "fp8_gemm.hip", "qk_rope.hip", "causal_conv.hip", "gdn_step.hip", "layer_api.hip"]
 LIB = os.path.join(PKG, "libnvfp4.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,196 @@
+// The short causal convolution along the tokens of each channel:
+//     y[t] = act(bias + sum_{j < W} w[j] in[t - W + 1 + j]),  W = 2, 3 or 4,
+// over a batch of sequences; the last W - 1 inputs of each are kept in a state.
+// Bound: HBM (every element read and written once; W fmas per element).
+//
+// A thread takes 8 channels (16 bytes of bf16) and a run of neighbouring tokens,
+// the last W - 1 inputs in registers, so that an input is read once per run
+// (and W - 1 more at its start, from the cache).  Neighbouring threads take
+// neighbouring channels.
+//
+// The state is read and written in one launch without a race: what needs a
+// sequence's old state -- its first W - 1 tokens and the new state of a
+// sequence shorter than W - 1 -- is done by one thread per channel group, the
+// one whose run holds the sequence's first token.  It goes past the end of
+// its run for that where it has to, and the run that such tokens lie in leaves
+// them out.  The new state comes from x, which nobody writes.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_util.h"
+#include "e4m3.h"
+#include "internal.h"
+#include "layer_ops.h"
+
+namespace nvfp4 {
+
+namespace {
+
+using namespace dev;
+
+// 8 elements of type DT as they lie in memory.
+template <int DT>
+struct Eight;
+template <>
+struct Eight<NVFP4_DTYPE_BF16> {
+  u32x4 w;
+  __device__ static Eight load(const uint8_t* p) { return {*reinterpret_cast<const u32x4*>(p)}; }
+  __device__ void store(uint8_t* p) const { *reinterpret_cast<u32x4*>(p) = w; }
+  __device__ void floats(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static Eight of(const float v[8]) {
+    return {u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])}};
+  }
+  __device__ void stream(uint8_t* p) const { store_stream16(p, w[0], w[1], w[2], w[3]); }
+};
+template <>
+struct Eight<NVFP4_DTYPE_F32> {
+  u32x4 w, h;
+  __device__ static Eight load(const uint8_t* p) {
+    return {*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + 16)};
+  }
+  __device__ void store(uint8_t* p) const {
+    *reinterpret_cast<u32x4*>(p) = w;
+    *reinterpret_cast<u32x4*>(p + 16) = h;
+  }
+  __device__ void floats(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(w[i]);
+      v[4 + i] = __uint_as_float(h[i]);
+    }
+  }
+  __device__ static Eight of(const float v[8]) {
+    Eight r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.w[i] = __float_as_uint(v[i]);
+      r.h[i] = __float_as_uint(v[4 + i]);
+    }
+    return r;
+  }
+  __device__ void stream(uint8_t* p) const {
+    store_stream16(p, w[0], w[1], w[2], w[3]);
+    store_stream16(p + 16, h[0], h[1], h[2], h[3]);
+  }
+};
+
+// First row of sequence b (b = batch: the end of the last).
+__device__ inline int64_t start_of(const nvfp4_conv& c, int64_t each, int64_t b) {
+  if (c.starts == nullptr) return b * each;
+  return min(max((int64_t)c.starts[b], (int64_t)0), c.tokens);
+}
+
+template <int DT, int W>
+__global__ __launch_bounds__(kElemThreads) void causal_conv_kernel(const nvfp4_conv c, int64_t each, int run, int64_t threads) {
+  constexpr int kBytes = DT == NVFP4_DTYPE_BF16 ? 16 : 32, kOld = W - 1;
+  const int64_t id = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
+  if (id >= threads) return;
+  const int64_t chunks = c.channels / 8, chunk = id % chunks;
+  const int64_t r0 = id / chunks * run, r1 = min(r0 + run, c.tokens);
+  const uint8_t* x = (const uint8_t*)c.x + chunk * kBytes;
+  uint8_t* y = (uint8_t*)c.y + chunk * kBytes;
+  const int64_t ldx = c.ld_x * (kBytes / 8), ldy = c.ld_y * (kBytes / 8);
+
+  float w[8][W], bias[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[e][j] = c.weight[(chunk * 8 + e) * W + j];
+    bias[e] = c.bias != nullptr ? c.bias[chunk * 8 + e] : 0.0f;
+  }
+
+  // the last sequence that begins at r0 or before
+  int64_t b = 0;
+  for (int64_t lo = 0, hi = c.batch - 1; lo <= hi;) {
+    const int64_t mid = (lo + hi) / 2;
+    if (start_of(c, each, mid) <= r0) {
+      b = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  for (; b < c.batch; ++b) {
+    const int64_t first = start_of(c, each, b), last = start_of(c, each, b + 1);
+    if (first >= r1) break;
+    if (last <= first || last <= r0) continue;
+    // this thread's tokens of the sequence: its first kOld ones belong to the run that holds the first
+    const bool whole = first >= r0;
+    int64_t t = whole ? first : max(r0, min(first + kOld, last));
+    const int64_t end = whole ? min(max(r1, first + kOld), last) : min(r1, last);
+    if (t >= end) continue;
+    float in[W][8];  // in[j]: the input W - 1 - j tokens ago
+    if (whole) {
+      Eight<DT> old[kOld] = {};
+      const int64_t slot = c.state == nullptr ? -1 : c.slots != nullptr ? (int64_t)c.slots[b] : b;
+      uint8_t* st = (uint8_t*)c.state + slot * c.ld_state * (kBytes / 8) + chunk * kBytes;
+      if (slot >= 0 && slot < c.n_states) {
+        if (c.fresh == nullptr || c.fresh[b] == 0) {
+#pragma unroll
+          for (int j = 0; j < kOld; ++j) old[j] = Eight<DT>::load(st + j * chunks * kBytes);
+        }
+#pragma unroll
+        for (int j = 0; j < kOld; ++j) {
+          const int64_t at = last - first - kOld + j;  // token of the sequence, negative: an old input
+          Eight<DT> keep = {};
+          if (at >= 0) {
+            keep = Eight<DT>::load(x + (first + at) * ldx);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kOld; ++i)
+              if (i == at + kOld) keep = old[i];
+          }
+          keep.store(st + j * chunks * kBytes);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kOld; ++j) old[j].floats(in[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kOld; ++j) Eight<DT>::load(x + (t - kOld + j) * ldx).floats(in[j]);
+    }
+    for (; t < end; ++t) {
+      Eight<DT>::load(x + t * ldx).floats(in[W - 1]);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float u = bias[e];
+#pragma unroll
+        for (int j = 0; j < W; ++j) u = fmaf(w[e][j], in[j][e], u);
+        v[e] = c.silu ? silu(u) : u;
+      }
+      Eight<DT>::of(v).stream(y + t * ldy);
+#pragma unroll
+      for (int j = 0; j < kOld; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) in[j][e] = in[j + 1][e];
+    }
+  }
+}
+
+template <int DT>
+void launch(const nvfp4_conv& c, hipStream_t s) {
+  const int64_t each = c.tokens / c.batch, chunks = c.channels / 8;
+  const int run = c.tokens == c.batch ? 1 : 16;
+  const int64_t threads = (c.tokens + run - 1) / run * chunks;
+  const unsigned grid = (unsigned)((threads + kElemThreads - 1) / kElemThreads);
+  if (c.width == 2) causal_conv_kernel<DT, 2><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
+  else if (c.width == 3) causal_conv_kernel<DT, 3><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
+  else causal_conv_kernel<DT, 4><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
+}
+
+}  // namespace
+
+hipError_t launch_causal_conv(const nvfp4_conv& c, int dtype, hipStream_t s) {
+  if (dtype == NVFP4_DTYPE_BF16) launch<NVFP4_DTYPE_BF16>(c, s);
+  else launch<NVFP4_DTYPE_F32>(c, s);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -551,6 +551,211 @@ int nvfp4_kv_pages_attention(const nvfp4_kv_pages* cache, const nvfp4_kv_batch* 
                              int64_t ld_q, int dtype, int q_heads, float scale, void* out, int64_t ld_out,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Linear layers in 8-bit floating point, for the layers that 4 bits do not
+ * suit: E4M3 codes with one float32 scale per block of 128 columns, a block
+ * being one row's (activations, block_rows = 1) or that of 128 rows (weights,
+ * block_rows = 128).  Element (r, c) stands for
+ *     e4m3(codes[r * ld_codes + c]) * scales[(r / block_rows) * ld_scales + c / 128].
+ *   cols a multiple of 16 (the last block may be short), rows any number
+ *   (the last block of rows may be short);
+ *   codes   DEVICE uint8 [rows, ld_codes], ld_codes >= cols and a multiple of
+ *           16, below 2^22; 16-byte aligned;
+ *   scales  DEVICE float32 [ceil(rows / block_rows), ld_scales], ld_scales >=
+ *           ceil(cols / 128).
+ *   rows < 2^31; rows * ld_codes, and for activations rows * ld_scales, below 2^40.
+ */
+typedef struct {
+  uint8_t* codes;
+  float* scales;
+  int64_t rows, cols;
+  int64_t ld_codes, ld_scales;
+  int block_rows;
+} nvfp4_fp8_tensor;
+
+/* nvfp4_fp8_quantize flags. */
+enum {
+  NVFP4_FP8_SCALE_F32 = 0,  /* scale = fl32(amax / 448) */
+  NVFP4_FP8_SCALE_POW2 = 1  /* scale = 2^e, the least e >= -126 with amax <= 448 * 2^e */
+};
+
+/*
+ * nvfp4_fp8_quantize -- x [q->rows, q->cols] (bf16 or float32, row stride ld_x
+ * elements, rows 16-byte aligned) into q, whose codes and scales are written.
+ * Bit for bit: amax = the largest magnitude among the block's finite
+ * elements; the scale as the flag says; a code is the E4M3 byte nearest to the
+ * exact x / scale, ties to the even code, beyond 448 saturating, sign = IEEE
+ * sign bit (scale 0 gives magnitude 0).  An element that is not finite
+ * becomes the NaN code.  Bytes behind a row's cols are not written.  rows = 0
+ * is a valid call that does nothing.  One launch.
+ */
+int nvfp4_fp8_quantize(const void* x, int x_dtype, int64_t ld_x, const nvfp4_fp8_tensor* q, int flags, void* stream);
+
+/*
+ * nvfp4_fp8_gemm -- out[m, n] = sum over blocks b of 128 columns of
+ *     a_scale[m, b] * w_scale[n / 128, b] * sum_{k in b} e4m3(a[m, k]) e4m3(w[n, k])
+ * (out = A W^T), a = activations [M, K] (block_rows 1), w = weight [N, K]
+ * (block_rows 128).
+ *   out   DEVICE [M, ld_out] of out_dtype (bf16: round to nearest even),
+ *         ld_out >= N elements.
+ * Sums over a block and over blocks are float32.  With out_dtype F32 the
+ * products are exact (codes as fp16 on the matrix unit) and the result is within
+ * (K / 128 + 136) 2^-23 sum |a w| of the exact one.  With BF16 the 8-bit matrix
+ * instructions are used, which cut the products of 8 neighbouring k to
+ * multiples of 2^-13 of the largest's power of two before they add them: up
+ * to 2^-10 of the sum of their magnitudes more, 1.5e-5 of the result on normally
+ * distributed data, where bf16's own rounding is 1.7e-3.  A NaN code reaches
+ * its row (a) or column (w) only.
+ * The product of two scales is a float32: below 2^-126 it loses bits.
+ * M = 0 is a valid call that does nothing.  The same call gives the same bits.
+ */
+int nvfp4_fp8_gemm(const nvfp4_fp8_tensor* a, const nvfp4_fp8_tensor* w, void* out, int out_dtype, int64_t ld_out,
+                   void* stream);
+
+/* Bytes of device workspace nvfp4_fp8_linear needs for rows x cols
+ * activations; 0 for a shape that it does not take. */
+size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * nvfp4_fp8_linear -- the whole layer on dense activations x [rows, w->cols]
+ * (bf16 or float32): bit for bit nvfp4_fp8_quantize(x, NVFP4_FP8_SCALE_F32)
+ * by single rows and nvfp4_fp8_gemm.
+ *   workspace DEVICE, >= nvfp4_fp8_linear_workspace_bytes(rows, w->cols)
+ *             bytes, 16-byte aligned, contents arbitrary; calls that may
+ *             overlap in time need one each.
+ */
+int nvfp4_fp8_linear(const void* x, int x_dtype, int64_t rows, int64_t ld_x, const nvfp4_fp8_tensor* w, void* out,
+                     int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Heads of queries or keys as nvfp4_qk_norm_rope reads and writes them:
+ * element (t, h, d) at x[t * ld_x + h * head_x + d], its result at
+ * out[t * ld_out + h * head_out + d], so that a projection's columns, heads
+ * interleaved with something else among them, are taken as they are.  out may
+ * be x with the same strides.
+ *   weight  DEVICE float32 [head_dim], or NULL: no norm.
+ */
+typedef struct {
+  const void* x;
+  int64_t ld_x, head_x;
+  void* out;
+  int64_t ld_out, head_out;
+  const float* weight;
+  int heads;
+} nvfp4_head_rows;
+
+/*
+ * The rotation of a head's first rotary_dim dimensions, in rotary_dim / 2
+ * pairs: (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0.  Pair
+ * i turns by the angle positions[axis[i] * ld_positions + t] * inv_freq[i].
+ *   positions  DEVICE int64 [axes, ld_positions], ld_positions >= tokens:
+ *              one axis for text, three (time, height, width) for images and
+ *              video.  Angles are formed in 64 bits: far positions keep
+ *              float32's precision (below 2^31 times inv_freq <= 1).
+ *   inv_freq   DEVICE float32 [rotary_dim / 2].
+ *   axis       DEVICE uint8 [rotary_dim / 2], the axis of each pair; NULL:
+ *              axis 0.  A value beyond axes - 1 counts as axes - 1.
+ *   rotary_dim a multiple of 16, at most head_dim.
+ */
+typedef struct {
+  const int64_t* positions;
+  int64_t ld_positions;
+  const float* inv_freq;
+  const uint8_t* axis;
+  int axes, rotary_dim, interleaved;
+} nvfp4_rope;
+
+/*
+ * nvfp4_qk_norm_rope -- for every token and head, in float32 and rounded once:
+ *     z = x / sqrt(mean_d x_d^2 + eps) * (weight + weight_offset)   (weight != NULL)
+ *     out = z with the rotation applied                             (rope != NULL)
+ * (weight_offset 1 serves checkpoints that store weight - 1).  What
+ * nvfp4_kv_pages_write and nvfp4_kv_pages_attention take.
+ *   q, k      HOST; either may be NULL (only the other is done).
+ *   dtype     of x and out, bf16 or float32.
+ *   head_dim  64, 128 or 256.  1 <= heads <= 4096.  0 <= tokens < 2^24.
+ *   ld_x, head_x, ld_out, head_out: multiples of 16 bytes, below 2^31, x and
+ *   out 16-byte aligned.  No two places may overlap: either the heads of a
+ *   token lie together (head >= head_dim, ld >= (heads - 1) * head + head_dim)
+ *   or the tokens of a head do (ld >= head_dim, head >= (tokens - 1) * ld +
+ *   head_dim); a stride that is not used is not looked at.
+ *   eps       finite and > 0 (read where there is a weight).
+ * One launch.  tokens = 0 is a valid call that does nothing.
+ */
+int nvfp4_qk_norm_rope(const nvfp4_head_rows* q, const nvfp4_head_rows* k, int dtype, int64_t tokens, int head_dim,
+                       float eps, float weight_offset, const nvfp4_rope* rope, void* stream);
+
+/*
+ * The short causal convolution along the tokens of each channel that stands
+ * between a Gated DeltaNet layer's in-projection and its recurrence, over a
+ * batch of sequences:
+ *     y[t, c] = act(bias[c] + sum_{j < width} weight[c, j] * in[t - width + 1 + j, c])
+ * with act(u) = u or u * sigmoid(u) (silu != 0), in float32, rounded once.  in is
+ * the sequence's x; before its first token stand the width - 1 inputs kept in
+ * its state (zeros without one), and afterwards the state holds the last
+ * width - 1 of both.
+ *   x, y    DEVICE [tokens, channels], row strides ld_x, ld_y (elements), rows
+ *           16-byte aligned; they must not overlap.
+ *   weight  DEVICE float32 [channels, width], 16-byte aligned; bias DEVICE
+ *           float32 [channels] or NULL.
+ *   starts  DEVICE int32 [batch + 1], not decreasing, starts[0] >= 0: sequence
+ *           b has the rows starts[b] .. starts[b + 1] - 1 (none, where equal;
+ *           then its state stays as it is).  Rows outside
+ *           [starts[0], starts[batch]) are left as they were.  A value beyond
+ *           tokens counts as tokens.  NULL: tokens / batch rows each
+ *           (tokens a multiple of batch).
+ *   state   DEVICE [n_states, width - 1, channels] of x's type, ld_state elements
+ *           from one to the next, 16-byte aligned; or NULL: no states.
+ *   slots   DEVICE int32 [batch], the state of each sequence; one outside
+ *           [0, n_states): the sequence has none.  Two sequences must not
+ *           share one.  NULL: state b (batch <= n_states).
+ *   fresh   DEVICE uint8 [batch]: where nonzero the sequence begins with
+ *           zeros, whatever its state holds, which is then written.  NULL: none.
+ * width 2, 3 or 4; channels a multiple of 8; ld_x, ld_y, ld_state multiples of
+ * 16 bytes, below 2^31; tokens, batch, n_states < 2^31, channels < 2^20,
+ * tokens * channels < 2^36.  One launch.  tokens = 0 or batch = 0 is a valid call that does nothing.
+ */
+typedef struct {
+  const void* x;
+  int64_t ld_x;
+  void* y;
+  int64_t ld_y;
+  const float* weight;
+  const float* bias;
+  int64_t tokens, channels, batch;
+  int width, silu;
+  const int32_t* starts;
+  void* state;
+  int64_t n_states, ld_state;
+  const int32_t* slots;
+  const uint8_t* fresh;
+} nvfp4_conv;
+
+int nvfp4_causal_conv(const nvfp4_conv* c, int dtype, void* stream);
+
+/*
+ * nvfp4_gdn_step -- nvfp4_gdn_recurrence for the next q_len tokens of each of
+ * batch sequences, whose float32 states are kept in a pool and updated in
+ * place (q_len = 1: the decode step).  Rows b * q_len .. of the inputs and of
+ * o belong to sequence b.
+ *   states  DEVICE float32 [n_states, v_heads, 128, 128], ld_states floats
+ *           from one to the next (a multiple of 4), 16-byte aligned.
+ *   slots   DEVICE int32 [batch], the state of each sequence; one outside
+ *           [0, n_states) marks a place of a padded batch that holds no
+ *           sequence: its rows of o are left as they were.  Two sequences
+ *           must not share one.  NULL: state b (batch <= n_states).
+ *   fresh   DEVICE uint8 [batch]: where nonzero the sequence begins with a
+ *           zero state, whatever its state holds.  NULL: none.
+ * Inputs, normalization, heads and o as for nvfp4_gdn_recurrence; each token
+ * costs a pass over registers, not over memory, but the tokens of a sequence
+ * run one after another, so whole prompts belong to the recurrence.
+ * batch * q_len < 2^31, v_heads <= 4096.  One launch.  batch = 0 is a
+ * valid call that does nothing.
+ */
+int nvfp4_gdn_step(const nvfp4_gdn_inputs* in, int in_dtype, int64_t batch, int64_t q_len, int k_heads, int v_heads,
+                   int normalize_qk, float* states, int64_t n_states, int64_t ld_states, const int32_t* slots,
+                   const uint8_t* fresh, void* o, int o_dtype, int64_t ld_o, void* stream);
+
 /* Human-readable text of a status (and of the last HIP error, for NVFP4_ERR_HIP). */
 const char* nvfp4_status_string(int status);
 
