@@ -188,6 +188,233 @@ __global__ __launch_bounds__(WN * WM * 64) void fp8_tile_kernel(const Fp8GemmArg
   }
 }
 
+// Large products.  WN x WM = 4 waves, one per SIMD; a wave owns FN * 16
+// columns x FM * 16 tokens (256 x 256 tiles: 128 x 128, 256 accumulators a
+// lane).  Per block of 128 a wave reads FN + FM fragments of 2 KB from LDS for FN * FM
+// matrix instructions of 32 cycles; each instruction's four fmas (out += scale *
+// tmp) run two instructions later, beside the matrix unit.
+//
+// LDS holds two stages of a block: weight rows, activation rows (128 bytes each),
+// the tile's activation scales; all three come by LDS DMA.  16-byte pieces are
+// XOR-swizzled by the row, in the copies' addresses, so that the reads are free of
+// bank conflicts.  Pieces behind K and nothing else have an address behind the descriptor's
+// range: such lanes write zeros.
+//
+// A block's regions t = 0 .. FM - 1 (one activation fragment each):
+//   the weight's fragments stay in registers over a block; the next block's are
+//   read in the last region, each right after its last use, and the next
+//   activation fragment is read a region ahead;
+//   barrier 1 (end of region 1): every wave holds its weight fragments, so the
+//   stage's weight rows are free: the copies of the weight two blocks on go out in regions
+//   2-5;
+//   barrier 2 (end of the region before the last): every wave has read the stage's activations: the
+//   copies of the activations two blocks on go out in the last region and the next
+//   block's first three.  The same barrier certifies the next block, whose copies are
+//   then older than the FN * WN / 2 weight copies just sent.
+// Behind the last block the last one is copied again, so that the waits need no branches.
+template <int FN, int FM, int WN, int WM>
+struct Pipe {
+  static constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
+  static constexpr int kW = TN * 128, kX = TM * 128, kStage = kW + kX + TM * 4;
+  static constexpr int CW = TN / 32, CX = TM / 32;  // 1 KB copies of a wave
+  static_assert(WN * WM == 4 && CW % 4 == 0 && CX % 4 == 0 && FM == 8 && FN % 2 == 0, "the schedule's shares");
+};
+
+template <int FN, int FM, int WN, int WM>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
+  using T = Pipe<FN, FM, WN, WM>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+  const int n0 = n_lo + tn * T::TN, m0 = tm * T::TM;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave / WM, wm = wave % WM, li = lane & 15, lg = lane >> 4;
+  const int blocks = (p.K + 127) / 128;
+
+  // copies: lane l brings piece l % 8 of row l / 8 of a group of 8 rows
+  const i32x4 rw = buffer_rsrc(p.w.codes + (int64_t)n0 * p.w.ld_codes, (uint32_t)(T::TN * p.w.ld_codes));
+  const i32x4 rx = buffer_rsrc(p.a.codes + (int64_t)m0 * p.a.ld_codes, (uint32_t)(T::TM * p.a.ld_codes));
+  const int q = lane >> 3;
+  int vw[T::CW], vx[T::CX];
+  int pw[2];                              // the piece, by the parity of the group of rows
+  const int px = (lane & 7) ^ q;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) pw[c] = (lane & 7) ^ ((q & 3) + 4 * c);
+#pragma unroll
+  for (int c = 0; c < T::CW; ++c)
+    vw[c] = min((wave * T::CW + c) * 8 + q, p.N - 1 - n0) * (int)p.w.ld_codes + pw[c & 1] * 16;
+#pragma unroll
+  for (int c = 0; c < T::CX; ++c)
+    vx[c] = min((wave * T::CX + c) * 8 + q, p.M - 1 - m0) * (int)p.a.ld_codes + px * 16;
+  constexpr int kNowhere = (int)0x80000000;
+  auto copy_w = [&](int b, int c) __attribute__((always_inline)) {
+    const int last = min(b, blocks - 1);
+    const int off = last * 128 + pw[c & 1] * 16 < p.K ? vw[c] : kNowhere;
+    llvm_amdgcn_raw_buffer_load_lds(rw, (lds_u32_ptr)(smem + (b & 1) * T::kStage + (wave * T::CW + c) * 1024), 16, off, last * 128, 0, 0);
+  };
+  auto copy_x = [&](int b, int c) __attribute__((always_inline)) {
+    const int last = min(b, blocks - 1);
+    const int off = last * 128 + px * 16 < p.K ? vx[c] : kNowhere;
+    llvm_amdgcn_raw_buffer_load_lds(rx, (lds_u32_ptr)(smem + (b & 1) * T::kStage + T::kW + (wave * T::CX + c) * 1024), 16, off,
+                                    last * 128, 0, 0);
+  };
+  // the scales of rows 64 (wave % (TM / 64)) .. of the tile, one a lane
+  const int srow = wave % (T::TM / 64) * 64;
+  const float* sa = p.a.scales + (int64_t)min(m0 + srow + lane, p.M - 1) * p.a.scale_row;
+  auto copy_s = [&](int b) __attribute__((always_inline)) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(sa + (int64_t)min(b, blocks - 1) * p.a.scale_block),
+                                     (lds_u32_ptr)(smem + (b & 1) * T::kStage + T::kW + T::kX + srow * 4), 4, 0, 0);
+  };
+  const auto* sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)((n0 + wn * FN * 16) / 128) * p.w.scale_row);
+
+  // fragments: weight row (i, a = lane % 16) is column (i / 2) * 32 + (a / 4) * 8 + (i % 2) * 4 + a % 4 of the wave, so that a
+  // lane's results of fragments 2 i and 2 i + 1 are 8 neighbouring columns
+  const int wbase = (wn * FN * 16 + (li >> 2) * 8 + (li & 3)) * 128, xbase = T::kW + (wm * FM * 16 + li) * 128;
+  int wat[2], xat[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    wat[h] = wbase + (((lg + 4 * h) ^ (li & 7)) << 4);
+    xat[h] = xbase + (((lg + 4 * h) ^ (li & 7)) << 4);
+  }
+  auto read_w = [&](const uint8_t* st, int i) __attribute__((always_inline)) {
+    Frag f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) f.p[h] = *reinterpret_cast<const u32x4*>(st + wat[h] + (i >> 1) * 4096 + (i & 1) * 512);
+    return f;
+  };
+  auto read_x = [&](const uint8_t* st, int t) __attribute__((always_inline)) {
+    Frag f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) f.p[h] = *reinterpret_cast<const u32x4*>(st + xat[h] + t * 2048);
+    return f;
+  };
+  auto read_s = [&](const uint8_t* st, int t) __attribute__((always_inline)) {
+    return *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + t) * 16 + li) * 4);
+  };
+
+  floatx4 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+  for (int c = 0; c < T::CW; ++c) copy_w(0, c);
+#pragma unroll
+  for (int c = 0; c < T::CX; ++c) copy_x(0, c);
+  copy_s(0);
+#pragma unroll
+  for (int c = 0; c < T::CW; ++c) copy_w(1, c);
+#pragma unroll
+  for (int c = 0; c < T::CX / 4; ++c) copy_x(1, c);
+  copy_s(1);
+  wait_vmem<T::CW + T::CX / 4 + 1>();
+  barrier_lds();
+  Frag w[FN], x[2];
+  float sc[FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i) w[i] = read_w(smem, i);
+  x[0] = read_x(smem, 0);
+  {
+    const float s = sw[0];
+#pragma unroll
+    for (int t = 0; t < FM; ++t) sc[t] = read_s(smem, t) * s;
+  }
+  for (int b = 0; b < blocks; ++b) {
+    const uint8_t* st = smem + (b & 1) * T::kStage;
+    const uint8_t* nst = smem + ((b + 1) & 1) * T::kStage;
+    const float next_sw = sw[min(b + 1, blocks - 1) * p.w.scale_block];
+    float next_sc[FM];
+    floatx4 tmp[2];
+#pragma unroll
+    for (int t = 0; t < FM; ++t) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (t < FM - 1) {
+        x[(t + 1) & 1] = read_x(st, t + 1);
+      } else {
+        x[(t + 1) & 1] = read_x(nst, 0);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) next_sc[j] = read_s(nst, j) * next_sw;
+      }
+      if (t < 3) {
+#pragma unroll
+        for (int c = 0; c < T::CX / 4; ++c) copy_x(b + 1, (t + 1) * (T::CX / 4) + c);
+      }
+      if (t >= 2 && t < 6) {
+#pragma unroll
+        for (int c = 0; c < T::CW / 4; ++c) copy_w(b + 2, (t - 2) * (T::CW / 4) + c);
+      }
+      if (t == FM - 1) {
+#pragma unroll
+        for (int c = 0; c < T::CX / 4; ++c) copy_x(b + 2, c);
+        copy_s(b + 2);
+      }
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const int n = t * FN + i;
+        const floatx4 now = block_product<false>(w[i], x[t & 1]);
+        if (n >= 2) {
+          const int o = n - 2;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[o % FN][o / FN][r] = fmaf(tmp[n & 1][r], sc[o / FN], acc[o % FN][o / FN][r]);
+        }
+        tmp[n & 1] = now;
+        if (t == FM - 1) w[i] = read_w(nst, i);
+      }
+      if (t == FM - 1) {
+#pragma unroll
+        for (int o = FM * FN - 2; o < FM * FN; ++o)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[o % FN][o / FN][r] = fmaf(tmp[o & 1][r], sc[o / FN], acc[o % FN][o / FN][r]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (t == 1) barrier_lds();
+      if (t == FM - 2) {
+        wait_vmem<T::CW>();
+        barrier_lds();
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < FM; ++t) sc[t] = next_sc[t];
+  }
+  wait_vmem<0>();  // no copy may land after the workgroup's LDS is given away
+
+  const bool vec = p.ld_out % 8 == 0 && (uintptr_t)p.out % 16 == 0;
+  uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int m = m0 + (wm * FM + j) * 16 + li;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int i = 0; i < FN; i += 2) {
+      const int n = n0 + wn * FN * 16 + (i / 2) * 32 + lg * 8;
+      uint16_t* o = out + (int64_t)m * p.ld_out + n;
+      const floatx4 u = acc[i][j], v = acc[i + 1][j];
+      if (vec && n + 8 <= p.N) {
+        store_stream16(o, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (n + r < p.N) o[r] = (uint16_t)f32_to_bf16_bits(r < 4 ? u[r] : v[r - 4]);
+      }
+    }
+  }
+}
+
+template <int FN, int FM, int WN, int WM>
+hipError_t launch_pipe(const Fp8GemmArgs& g, int n_lo, int n_hi, hipStream_t s) {
+  using T = Pipe<FN, FM, WN, WM>;
+  Fp8GemmArgs h = g;
+  h.N = n_hi;
+  const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (n_hi - n_lo + T::TN - 1) / T::TN;
+  const auto fn = fp8_pipe_kernel<FN, FM, WN, WM>;
+  const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * T::kStage);
+  if (e != hipSuccess) return e;
+  fn<<<(unsigned)tiles_m * (unsigned)tiles_n, 256, 2 * T::kStage, s>>>(h, tiles_m, tiles_n, n_lo);
+  return hipGetLastError();
+}
+
 template <int FN, int FM, int WN, int WM>
 hipError_t launch_tiles(const Fp8GemmArgs& g, hipStream_t s) {
   constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
@@ -205,6 +432,9 @@ hipError_t launch_tiles(const Fp8GemmArgs& g, hipStream_t s) {
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t s) {
   if (g.M <= 16) return launch_tiles<1, 1, 2, 1>(g, s);
   if (g.M <= 64) return launch_tiles<2, 2, 2, 2>(g, s);
+  if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 256) {
+    return launch_pipe<8, 8, 2, 2>(g, 0, g.N, s);
+  }
   return launch_tiles<4, 4, 2, 2>(g, s);
 }
 
