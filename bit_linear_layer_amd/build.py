@@ -32,6 +32,10 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I" + os.path.join(ROOT, "include"),
 ]
+# The block-scaled product's results go from the matrix unit to float32 fmas,
+# which take vector registers only: left alone, the compiler lets a kernel of
+# one wave per SIMD put them into accumulation registers and moves each one.
+SOURCE_FLAGS = {"fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 _HOST_FEATURE_NOTE = "'-packed-fp32-ops' is not a recognized feature for this target (ignoring feature)"
 
 
@@ -47,7 +51,7 @@ def _run(cmd: list[str]) -> None:
 def build(verbose: bool = True, jobs: int | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     objs = [os.path.join(OBJ, os.path.splitext(s)[0] + ".o") for s in SOURCES]
-    cmds = [[HIPCC, *FLAGS, "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
+    cmds = [[HIPCC, *FLAGS, *SOURCE_FLAGS.get(s, []), "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
     if verbose:
         print(" ".join(cmds[0][:-4]) + " -c <source> -o <object>   # " + " ".join(SOURCES), flush=True)
     jobs = jobs or min(len(cmds), os.cpu_count() or 1, 16)

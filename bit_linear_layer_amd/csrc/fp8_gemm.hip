@@ -215,9 +215,10 @@ __global__ __launch_bounds__(WN * WM * 64) void fp8_tile_kernel(const Fp8GemmArg
 template <int FN, int FM, int WN, int WM>
 struct Pipe {
   static constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
-  static constexpr int kW = TN * 128, kX = TM * 128, kStage = kW + kX + TM * 4;
+  static constexpr int kW = TN * 128, kX = TM * 128, kStage = kW + kX + 1024;
   static constexpr int CW = TN / 32, CX = TM / 32;  // 1 KB copies of a wave
-  static_assert(WN * WM == 4 && CW % 4 == 0 && CX % 4 == 0 && FM == 8 && FN % 2 == 0, "the schedule's shares");
+  static constexpr int x_share(int k) { return (CX * k + 3) / 4; }  // of the activation copies, those before the k-th of 4 regions
+  static_assert(WN * WM == 4 && CW % 4 == 0 && FM >= 7 && FN % 2 == 0, "the schedule's shares");
 };
 
 template <int FN, int FM, int WN, int WM>
@@ -247,7 +248,7 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
 #pragma unroll
   for (int c = 0; c < T::CX; ++c)
     vx[c] = min((wave * T::CX + c) * 8 + q, p.M - 1 - m0) * (int)p.a.ld_codes + px * 16;
-  constexpr int kNowhere = (int)0x80000000;
+  constexpr int kNowhere = (int)0x80000000, kLag = 3;
   auto copy_w = [&](int b, int c) __attribute__((always_inline)) {
     const int last = min(b, blocks - 1);
     const int off = last * 128 + pw[c & 1] * 16 < p.K ? vw[c] : kNowhere;
@@ -259,8 +260,8 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
     llvm_amdgcn_raw_buffer_load_lds(rx, (lds_u32_ptr)(smem + (b & 1) * T::kStage + T::kW + (wave * T::CX + c) * 1024), 16, off,
                                     last * 128, 0, 0);
   };
-  // the scales of rows 64 (wave % (TM / 64)) .. of the tile, one a lane
-  const int srow = wave % (T::TM / 64) * 64;
+  // the scales of rows 64 wave .. of the tile, one a lane (of following rows where a tile has fewer than 256)
+  const int srow = wave * 64;
   const float* sa = p.a.scales + (int64_t)min(m0 + srow + lane, p.M - 1) * p.a.scale_row;
   auto copy_s = [&](int b) __attribute__((always_inline)) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(sa + (int64_t)min(b, blocks - 1) * p.a.scale_block),
@@ -307,9 +308,9 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
 #pragma unroll
   for (int c = 0; c < T::CW; ++c) copy_w(1, c);
 #pragma unroll
-  for (int c = 0; c < T::CX / 4; ++c) copy_x(1, c);
+  for (int c = 0; c < T::x_share(1); ++c) copy_x(1, c);
   copy_s(1);
-  wait_vmem<T::CW + T::CX / 4 + 1>();
+  wait_vmem<T::CW + T::x_share(1) + 1>();
   barrier_lds();
   Frag w[FN], x[2];
   float sc[FM];
@@ -324,59 +325,53 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
   for (int b = 0; b < blocks; ++b) {
     const uint8_t* st = smem + (b & 1) * T::kStage;
     const uint8_t* nst = smem + ((b + 1) & 1) * T::kStage;
-    const float next_sw = sw[min(b + 1, blocks - 1) * p.w.scale_block];
-    float next_sc[FM];
-    floatx4 tmp[2];
+    float next_sw = 0.0f, next_sc[FM];
+    floatx4 tmp[kLag + 1];
+    auto add = [&](int o) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[o % FN][o / FN][r] = fmaf(tmp[o % (kLag + 1)][r], sc[o / FN], acc[o % FN][o / FN][r]);
+    };
 #pragma unroll
     for (int t = 0; t < FM; ++t) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (t < FM - 1) {
-        x[(t + 1) & 1] = read_x(st, t + 1);
-      } else {
-        x[(t + 1) & 1] = read_x(nst, 0);
-#pragma unroll
-        for (int j = 0; j < FM; ++j) next_sc[j] = read_s(nst, j) * next_sw;
-      }
-      if (t < 3) {
-#pragma unroll
-        for (int c = 0; c < T::CX / 4; ++c) copy_x(b + 1, (t + 1) * (T::CX / 4) + c);
-      }
-      if (t >= 2 && t < 6) {
-#pragma unroll
-        for (int c = 0; c < T::CW / 4; ++c) copy_w(b + 2, (t - 2) * (T::CW / 4) + c);
-      }
-      if (t == FM - 1) {
-#pragma unroll
-        for (int c = 0; c < T::CX / 4; ++c) copy_x(b + 2, c);
-        copy_s(b + 2);
-      }
+      // copies of this region, one beside each of its first matrix instructions
+      const int x_lo = t == FM - 1 ? 0 : t < 3 ? T::x_share(t + 1) : 0, x_hi = t == FM - 1 ? T::x_share(1) : t < 3 ? T::x_share(t + 2) : 0;
+      const int w_lo = t >= 2 && t < 6 ? (t - 2) * (T::CW / 4) : 0, w_hi = t >= 2 && t < 6 ? (t - 1) * (T::CW / 4) : 0;
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
         const int n = t * FN + i;
-        const floatx4 now = block_product<false>(w[i], x[t & 1]);
-        if (n >= 2) {
-          const int o = n - 2;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[o % FN][o / FN][r] = fmaf(tmp[n & 1][r], sc[o / FN], acc[o % FN][o / FN][r]);
-        }
-        tmp[n & 1] = now;
+        if (i == 1) x[(t + 1) & 1] = t < FM - 1 ? read_x(st, t + 1) : read_x(nst, 0);
+        tmp[n % (kLag + 1)] = block_product<false>(w[i], x[t & 1]);
+        if (n >= kLag) add(n - kLag);
         if (t == FM - 1) w[i] = read_w(nst, i);
-      }
-      if (t == FM - 1) {
-#pragma unroll
-        for (int o = FM * FN - 2; o < FM * FN; ++o)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[o % FN][o / FN][r] = fmaf(tmp[o & 1][r], sc[o / FN], acc[o % FN][o / FN][r]);
+        const int c = i - 1;
+        if (c >= 0 && c < x_hi - x_lo) copy_x(t < 3 ? b + 1 : b + 2, x_lo + c);
+        else if (c >= 0 && c - (x_hi - x_lo) < w_hi - w_lo) copy_w(b + 2, w_lo + c - (x_hi - x_lo));
+        else if (t == FM - 1 && c == x_hi) copy_s(b + 2);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (t == 1) barrier_lds();
+      if (t == FM - 1) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j) next_sc[j] = read_s(nst, j);
+#pragma unroll
+        for (int o = FM * FN - kLag; o < FM * FN; ++o) add(o);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) next_sc[j] *= next_sw;
+      }
+      if (t == 1) {
+        next_sw = sw[min(b + 1, blocks - 1) * p.w.scale_block];
+        barrier_lds();
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // the barrier's lgkmcnt(0) again, seen by the compiler's own wait insertion
+      }
       if (t == FM - 2) {
         wait_vmem<T::CW>();
         barrier_lds();
+        __builtin_amdgcn_s_waitcnt(0xC07F);
       }
     }
 #pragma unroll
     for (int t = 0; t < FM; ++t) sc[t] = next_sc[t];
+    if constexpr (FM % 2 == 1) x[0] = x[1];
   }
   wait_vmem<0>();  // no copy may land after the workgroup's LDS is given away
 
@@ -433,7 +428,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t s) {
   if (g.M <= 16) return launch_tiles<1, 1, 2, 1>(g, s);
   if (g.M <= 64) return launch_tiles<2, 2, 2, 2>(g, s);
   if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 256) {
-    return launch_pipe<8, 8, 2, 2>(g, 0, g.N, s);
+    return launch_pipe<8, 7, 2, 2>(g, 0, g.N, s);
   }
   return launch_tiles<4, 4, 2, 2>(g, s);
 }
