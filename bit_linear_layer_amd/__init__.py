@@ -25,7 +25,8 @@ __all__ = [
     "KVPages", "empty_kv_pages", "nvfp4_kv_pages_write", "nvfp4_kv_pages_read", "nvfp4_kv_pages_attention",
     "nvfp4_kv_pages_attention_workspace_bytes", "kv_pages_write", "kv_pages_read", "kv_pages_attention",
     "kv_pages_attention_workspace",
-    "FP8Tensor", "empty_fp8", "nvfp4_fp8_quantize", "nvfp4_fp8_gemm", "nvfp4_fp8_linear", "nvfp4_fp8_linear_workspace_bytes",
+    "FP8Tensor", "empty_fp8", "nvfp4_fp8_quantize", "nvfp4_fp8_gemm", "nvfp4_fp8_linear", "nvfp4_fp8_gemm_workspace_bytes",
+    "nvfp4_fp8_linear_workspace_bytes", "fp8_gemm_workspace",
     "fp8_quantize", "fp8_gemm", "fp8_linear", "fp8_linear_workspace", "Rope", "nvfp4_qk_norm_rope", "qk_norm_rope",
     "nvfp4_causal_conv", "causal_conv", "nvfp4_gdn_step", "gdn_step", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "DTYPE_BF16", "DTYPE_F32", "SCALE_DYNAMIC", "SCALE_STATIC", "AMAX_PRECOMPUTED", "MAX_SEGMENTS",
@@ -173,8 +174,10 @@ def load() -> ctypes.CDLL:
         fp8 = ctypes.POINTER(_FP8)
         lib.nvfp4_fp8_quantize.argtypes = [_P, ctypes.c_int, _I64, fp8, ctypes.c_int, _P]
         lib.nvfp4_fp8_quantize.restype = ctypes.c_int
-        lib.nvfp4_fp8_gemm.argtypes = [fp8, fp8, _P, ctypes.c_int, _I64, _P]
+        lib.nvfp4_fp8_gemm.argtypes = [fp8, fp8, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
         lib.nvfp4_fp8_gemm.restype = ctypes.c_int
+        lib.nvfp4_fp8_gemm_workspace_bytes.argtypes = [_I64]
+        lib.nvfp4_fp8_gemm_workspace_bytes.restype = ctypes.c_size_t
         lib.nvfp4_fp8_linear_workspace_bytes.argtypes = [_I64, _I64]
         lib.nvfp4_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
         lib.nvfp4_fp8_linear.argtypes = [_P, ctypes.c_int, _I64, _I64, fp8, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
@@ -722,13 +725,25 @@ def nvfp4_fp8_quantize(x: torch.Tensor, q: FP8Tensor, flags: int = FP8_SCALE_F32
            "nvfp4_fp8_quantize")
 
 
-def nvfp4_fp8_gemm(a: FP8Tensor, w: FP8Tensor, out: torch.Tensor, stream=None) -> None:
+def nvfp4_fp8_gemm_workspace_bytes(rows: int) -> int:
+    """C ``nvfp4_fp8_gemm_workspace_bytes``; 0 for a number of rows that the product does not take."""
+    return int(load().nvfp4_fp8_gemm_workspace_bytes(rows))
+
+
+def _space(workspace: torch.Tensor, device: torch.device):
+    if not workspace.is_contiguous():
+        raise NVFP4Error("workspace must be contiguous")
+    _on(workspace, device, "workspace")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def nvfp4_fp8_gemm(a: FP8Tensor, w: FP8Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """C ``nvfp4_fp8_gemm``: out[M, N] = A W^T, a by rows, w by blocks of 128 rows."""
     da, dw, device = a.descriptor(), w.descriptor(), w.codes.device
     _on(a.codes, device, "a")
     ld = _row_stride(out, a.rows, w.rows, device, "out")
     _check(_call_on(device, stream, load().nvfp4_fp8_gemm, ctypes.byref(da), ctypes.byref(dw), out.data_ptr(), _dtype_code(out),
-                    ld), "nvfp4_fp8_gemm")
+                    ld, *_space(workspace, device)), "nvfp4_fp8_gemm")
 
 
 def nvfp4_fp8_linear_workspace_bytes(rows: int, cols: int) -> int:
@@ -744,11 +759,8 @@ def nvfp4_fp8_linear(x: torch.Tensor, w: FP8Tensor, out: torch.Tensor, workspace
         raise NVFP4Error(f"x must be [rows, {w.cols}], got {list(x.shape)}")
     rows = x.shape[0]
     ld_x, ld_o = _row_stride(x, rows, w.cols, device, "x"), _row_stride(out, rows, w.rows, device, "out")
-    if not workspace.is_contiguous():
-        raise NVFP4Error("workspace must be contiguous")
-    _on(workspace, device, "workspace")
     _check(_call_on(device, stream, load().nvfp4_fp8_linear, x.data_ptr(), _dtype_code(x), rows, ld_x, ctypes.byref(d),
-                    out.data_ptr(), _dtype_code(out), ld_o, workspace.data_ptr(), workspace.nbytes), "nvfp4_fp8_linear")
+                    out.data_ptr(), _dtype_code(out), ld_o, *_space(workspace, device)), "nvfp4_fp8_linear")
 
 
 @dataclass
@@ -1085,14 +1097,24 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, flags: int = FP8_SCALE_F3
     return q
 
 
-def fp8_gemm(a: FP8Tensor, w: FP8Tensor, out_dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+def fp8_gemm_workspace(rows: int, device="cuda") -> torch.Tensor:
+    """A workspace for ``fp8_gemm`` calls of this and any smaller number of rows."""
+    n = nvfp4_fp8_gemm_workspace_bytes(rows)
+    if n == 0:
+        raise NVFP4Error(f"the product does not take {rows} rows")
+    return torch.empty((n + 3) // 4, dtype=torch.float32, device=device)
+
+
+def fp8_gemm(a: FP8Tensor, w: FP8Tensor, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None) -> torch.Tensor:
+    ws = workspace if workspace is not None else fp8_gemm_workspace(a.rows, a.codes.device)
     o = out if out is not None else torch.empty((a.rows, w.rows), dtype=out_dtype, device=a.codes.device)
-    nvfp4_fp8_gemm(a, w, o)
+    nvfp4_fp8_gemm(a, w, o, ws)
     return o
 
 
 def fp8_linear_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
-    """A workspace for ``fp8_linear`` calls of up to ``rows`` rows."""
+    """A workspace for ``fp8_linear`` calls of this and any smaller number of rows."""
     n = nvfp4_fp8_linear_workspace_bytes(rows, cols)
     if n == 0:
         raise NVFP4Error(f"the layer does not take [{rows}, {cols}] activations")

@@ -61,7 +61,7 @@ __device__ inline floatx4 block_product(const Frag& w, const Frag& x) {
                      (int)w.p[1][0], (int)w.p[1][1], (int)w.p[1][2], (int)w.p[1][3]};
     const i32x8 b = {(int)x.p[0][0], (int)x.p[0][1], (int)x.p[0][2], (int)x.p[0][3],
                      (int)x.p[1][0], (int)x.p[1][1], (int)x.p[1][2], (int)x.p[1][3]};
-    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
   }
   return c;
 }
@@ -90,102 +90,206 @@ __device__ inline void store4(void* out, int64_t at, const floatx4& v, int left,
   }
 }
 
-// Tiles of FN * WN * 16 columns x FM * WM * 16 tokens, WN x WM waves; a block of
-// 128 columns per step through registers into one of two LDS stages, rows of
-// 128 bytes with their 16-byte pieces XOR-swizzled by the row so that the 8
-// rows a quarter-wave reads fall into distinct banks.  Takes any sizes: rows
-// behind the last are read as the last (their outputs are not stored), pieces
-// behind K as zeros.
-template <int FN, int FM, int WN, int WM, bool EXACT, int OUT>
-__global__ __launch_bounds__(WN * WM * 64) void fp8_tile_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n) {
-  constexpr int kThreads = WN * WM * 64, TN = FN * WN * 16, TM = FM * WM * 16;
-  constexpr int kPieces = (TN + TM) * 8 / kThreads;
-  static_assert((TN + TM) * 8 % kThreads == 0 && 128 % TN == 0, "whole pieces per thread, a tile in one weight block");
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2][(TN + TM) * 128];
+// Products with few tokens, or of too few tiles to fill the chip: bound by the
+// weight's bytes up to about 200 tokens.  256 workgroups of 8 waves, one per CU, share the
+// line of all (tile, block of 128) steps evenly, tile by tile; a workgroup's copies
+// run D - 1 steps ahead of its products, across the ends of tiles, so that the
+// stream from memory never drains.  A tile whose steps lie in one workgroup is stored; of one that a
+// cut divides each workgroup leaves its float32 sums in the workspace, and
+// fp8_join_kernel adds them in the order of the blocks: the result depends on the sizes only.
+//
+// A stage in LDS holds the weight's and the activations' rows of one block (128
+// bytes each, 16-byte pieces XOR-swizzled by the row so that fragment reads are free of bank
+// conflicts) and the activations' scales, all by LDS DMA.  Rows behind the last
+// and pieces behind K lie behind the descriptors' ranges: such lanes write zeros.
+// One barrier per step certifies its stage and frees the one before, into which the
+// copies D - 1 steps ahead then go.
+template <int FN, int FM, int WN, int WM, int D>
+struct Ring {
+  static constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
+  static constexpr int kW = TN * 128, kX = TM * 128;
+  static constexpr int NS = (TM + 63) / 64;                  // waves that copy 64 scales
+  static constexpr int CW = TN / 64, CX = TM / 64;           // copies of every wave
+  static constexpr int XR = TM / 8 % 8;                      // waves that copy one more group of activation rows
+  static constexpr int kBase = CW + CX;
+  static constexpr int kStage = kW + kX + NS * 256;
+  static_assert(WN * WM == 8 && TN % 64 == 0 && 128 % TN == 0 && XR + NS <= 8 && D * kStage <= 160 * 1024, "the copies' shares");
+  static_assert((D - 2) * (kBase + 1) < 64, "vmcnt's range");
+};
 
-  int tm, tn;
-  tile_of(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-  const int n0 = tn * TN, m0 = tm * TM;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+constexpr int kRingGroups = 256;
+
+// The steps of workgroup g: [first, last) of the line of all.
+struct Share {
+  int64_t first, last;
+  __host__ __device__ Share(int64_t steps, int groups, int g)
+      : first(steps * g / groups), last(steps * (g + 1) / groups) {}
+};
+
+template <int FN, int FM, int WN, int WM, int D, bool EXACT, int OUT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __restrict__ partial) {
+  using T = Ring<FN, FM, WN, WM, D>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / WM, wm = wave % WM, li = lane & 15, lg = lane >> 4;
   const int blocks = (p.K + 127) / 128;
+  const Share mine((int64_t)tiles_m * tiles_n * blocks, gridDim.x, blockIdx.x);
 
-  const uint8_t* src[kPieces];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int row = (tid + i * kThreads) >> 3, piece = tid & 7;
-    src[i] = (row < TN ? p.w.codes + (int64_t)min(n0 + row, p.N - 1) * p.w.ld_codes
-                       : p.a.codes + (int64_t)min(m0 + row - TN, p.M - 1) * p.a.ld_codes) + piece * 16;
-  }
-  u32x4 hold[kPieces];
-  auto load = [&](int b) {
-    const bool there = b * 128 + (tid & 7) * 16 < p.K;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      hold[i] = there ? *reinterpret_cast<const u32x4*>(src[i] + b * 128) : u32x4{0u, 0u, 0u, 0u};
+  // copies: lane l brings piece l % 8 (swizzled) of row l / 8 of a group of 8 rows
+  const int q = lane >> 3, piece = ((lane & 7) ^ q) * 16;
+  const int ldw = (int)p.w.ld_codes, lda = (int)p.a.ld_codes;
+  constexpr int kNowhere = (int)0x80000000;
+  struct Cursor {
+    int tile, block;
+    int64_t step;
+    i32x4 rw, rx;
+    const float* sa;
+  } at;
+  auto enter = [&](int tile) __attribute__((always_inline)) {
+    const int n0 = tile / tiles_m * T::TN, m0 = tile % tiles_m * T::TM;
+    at.rw = buffer_rsrc(p.w.codes + (int64_t)n0 * ldw, (uint32_t)(min(T::TN, p.N - n0) * ldw));
+    at.rx = buffer_rsrc(p.a.codes + (int64_t)m0 * lda, (uint32_t)(min(T::TM, p.M - m0) * lda));
+    at.sa = p.a.scales + (int64_t)min(m0 + max(wave - (8 - T::NS), 0) * 64 + lane, p.M - 1) * p.a.scale_row;
   };
-  auto put = [&](int st) {
+  auto copy = [&](uint8_t* stage) __attribute__((always_inline)) {
+    const int k = at.block * 128;
+    const bool there = k + piece < p.K;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int row = (tid + i * kThreads) >> 3, piece = tid & 7;
-      *reinterpret_cast<u32x4*>(&smem[st][row * 128 + ((piece ^ (row & 7)) << 4)]) = hold[i];
+    for (int c = 0; c < T::CW; ++c)
+      llvm_amdgcn_raw_buffer_load_lds(at.rw, (lds_u32_ptr)(stage + (wave * T::CW + c) * 1024), 16,
+                                      there ? ((wave * T::CW + c) * 8 + q) * ldw + piece : kNowhere, k, 0, 0);
+#pragma unroll
+    for (int c = 0; c < T::CX; ++c)
+      llvm_amdgcn_raw_buffer_load_lds(at.rx, (lds_u32_ptr)(stage + T::kW + (wave * T::CX + c) * 1024), 16,
+                                      there ? ((wave * T::CX + c) * 8 + q) * lda + piece : kNowhere, k, 0, 0);
+    if (wave < T::XR)
+      llvm_amdgcn_raw_buffer_load_lds(at.rx, (lds_u32_ptr)(stage + T::kW + (8 * T::CX + wave) * 1024), 16,
+                                      there ? ((8 * T::CX + wave) * 8 + q) * lda + piece : kNowhere, k, 0, 0);
+    if (wave >= 8 - T::NS)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(at.sa + (int64_t)at.block * p.a.scale_block),
+                                       (lds_u32_ptr)(stage + T::kW + T::kX + (wave - (8 - T::NS)) * 256), 4, 0, 0);
+  };
+  auto advance = [&]() __attribute__((always_inline)) {  // behind the last step the last one is copied again
+    if (at.step + 1 < mine.last) {
+      ++at.step;
+      if (++at.block == blocks) {
+        at.block = 0;
+        enter(++at.tile);
+      }
     }
   };
-  auto frag = [&](int st, int row) {
-    Frag f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      f.p[h] = *reinterpret_cast<const u32x4*>(&smem[st][row * 128 + (((lg + 4 * h) ^ (row & 7)) << 4)]);
-    return f;
-  };
-  const float* sa[FM];
-#pragma unroll
-  for (int j = 0; j < FM; ++j)
-    sa[j] = p.a.scales + (int64_t)min(m0 + (wm * FM + j) * 16 + li, p.M - 1) * p.a.scale_row;
-  const float* sw = p.w.scales + (int64_t)(n0 / 128) * p.w.scale_row;
 
+  int tile = (int)(mine.first / blocks), block = (int)(mine.first - (int64_t)tile * blocks);
+  at.tile = tile;
+  at.block = block;
+  at.step = mine.first;
+  enter(tile);
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) {
+    copy(smem + d * T::kStage);
+    advance();
+  }
   floatx4 acc[FN][FM];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < FN; ++i)
+    for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  load(0);
-  put(0);
-  __syncthreads();
-  for (int b = 0; b < blocks; ++b) {
-    if (b + 1 < blocks) load(b + 1);
-    float sc[FM];
-    const float s = sw[b * p.w.scale_block];
+      for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
+  const int key = li & 7;
+  const bool vec = p.ld_out % 4 == 0 && (uintptr_t)p.out % (OUT == NVFP4_DTYPE_BF16 ? 8 : 16) == 0;
+  int begun = block, stage = 0;  // begun: the tile's first block of this workgroup
+  const bool extra = wave < T::XR || wave >= 8 - T::NS;
+  for (int64_t step = mine.first; step < mine.last; ++step) {
+    const int n0 = tile / tiles_m * T::TN, m0 = tile % tiles_m * T::TM;
+    const auto* sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)(n0 / 128) * p.w.scale_row);
+    const float s = sw[block * p.w.scale_block];
+    if (extra) wait_vmem<(D - 2) * (T::kBase + 1)>();
+    else wait_vmem<(D - 2) * T::kBase>();
+    barrier_lds();
+    copy(smem + (stage == 0 ? D - 1 : stage - 1) * T::kStage);
+    advance();
+    const uint8_t* st = smem + stage * T::kStage;
+    auto frag = [&](int row) __attribute__((always_inline)) {
+      Frag f;
 #pragma unroll
-    for (int j = 0; j < FM; ++j) sc[j] = sa[j][b * p.a.scale_block] * s;
+      for (int h = 0; h < 2; ++h) f.p[h] = *reinterpret_cast<const u32x4*>(st + row * 128 + (((lg + 4 * h) ^ key) << 4));
+      return f;
+    };
     Frag w[FN];
 #pragma unroll
-    for (int i = 0; i < FN; ++i) w[i] = frag(b & 1, (wn * FN + i) * 16 + li);
+    for (int i = 0; i < FN; ++i) w[i] = frag((wn * FN + i) * 16 + li);
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const Frag x = frag(b & 1, TN + (wm * FM + j) * 16 + li);
+      const Frag x = frag(T::TN + (wm * FM + j) * 16 + li);
+      const float sc = *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + j) * 16 + li) * 4) * s;
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
         const floatx4 t = block_product<EXACT>(w[i], x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], sc[j], acc[i][j][r]);
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], sc, acc[i][j][r]);
       }
     }
-    if (b + 1 < blocks) put((b + 1) & 1);
-    __syncthreads();
-  }
-  const bool vec = p.ld_out % 4 == 0 && (uintptr_t)p.out % (OUT == NVFP4_DTYPE_BF16 ? 8 : 16) == 0;
+    stage = stage == D - 1 ? 0 : stage + 1;
+    ++block;
+    if (block == blocks || step + 1 == mine.last) {
+      if (block == blocks && begun == 0) {
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    const int m = m0 + (wm * FM + j) * 16 + li;
-    if (m >= p.M) continue;
+        for (int j = 0; j < FM; ++j) {
+          const int m = m0 + (wm * FM + j) * 16 + li;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const int n = n0 + (wn * FN + i) * 16 + 4 * lg;
-      store4<OUT>(p.out, (int64_t)m * p.ld_out + n, acc[i][j], p.N - n, vec);
+          for (int i = 0; i < FN; ++i) {
+            const int n = n0 + (wn * FN + i) * 16 + 4 * lg;
+            if (m < p.M) store4<OUT>(p.out, (int64_t)m * p.ld_out + n, acc[i][j], p.N - n, vec);
+          }
+        }
+      } else {  // the first slot: of a tile that an earlier workgroup began; the second: of one that this one begins
+        float* to = partial + ((int64_t)blockIdx.x * 2 + (begun == 0)) * (T::TN * T::TM);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j)
+            *reinterpret_cast<floatx4*>(to + (((wave * FN + i) * FM + j) * 64 + lane) * 4) = acc[i][j];
+      }
+      clear();
+      begun = block = 0;
+      ++tile;
     }
   }
+  wait_vmem<0>();  // no copy may land after the workgroup's LDS is given away
+}
+
+// The sums of tiles that more than one workgroup worked on; a thread per four columns of a token.
+template <int FN, int FM, int WN, int WM, int D, int OUT>
+__global__ __launch_bounds__(256) void fp8_join_kernel(const Fp8GemmArgs p, int tiles_m, int groups, int64_t steps,
+                                                       const float* __restrict__ partial) {
+  using T = Ring<FN, FM, WN, WM, D>;
+  const int tile = blockIdx.x, blocks = (p.K + 127) / 128;
+  const int64_t lo = (int64_t)tile * blocks, hi = lo + blocks;
+  // the workgroup of a step is the largest g with steps * g / groups <= step
+  auto group_of = [&](int64_t step) {
+    int g = (int)((step + 1) * groups / steps);
+    g = min(g, groups - 1);
+    while (g > 0 && Share(steps, groups, g).first > step) --g;
+    while (g + 1 < groups && Share(steps, groups, g + 1).first <= step) ++g;
+    return g;
+  };
+  const int g0 = group_of(lo), g1 = group_of(hi - 1);
+  if (g0 == g1) return;  // stored as it was finished
+  const int e = blockIdx.y * 256 + threadIdx.x;
+  if (e >= T::TN * T::TM / 4) return;
+  floatx4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = g0; g <= g1; ++g) {
+    const bool begins = Share(steps, groups, g).first <= lo;
+    sum += *reinterpret_cast<const floatx4*>(partial + ((int64_t)g * 2 + begins) * (T::TN * T::TM) + e * 4);
+  }
+  const int lane = e & 63, f = e >> 6, j = f % FM, i = f / FM % FN, wave = f / (FM * FN);
+  const int m = tile % tiles_m * T::TM + (wave % WM * FM + j) * 16 + (lane & 15);
+  const int n = tile / tiles_m * T::TN + (wave / WM * FN + i) * 16 + 4 * (lane >> 4);
+  const bool vec = p.ld_out % 4 == 0 && (uintptr_t)p.out % (OUT == NVFP4_DTYPE_BF16 ? 8 : 16) == 0;
+  if (m < p.M) store4<OUT>(p.out, (int64_t)m * p.ld_out + n, sum, p.N - n, vec);
 }
 
 // Large products.  WN x WM = 4 waves, one per SIMD; a wave owns FN * 16
@@ -410,27 +514,56 @@ hipError_t launch_pipe(const Fp8GemmArgs& g, int n_lo, int n_hi, hipStream_t s) 
   return hipGetLastError();
 }
 
-template <int FN, int FM, int WN, int WM>
-hipError_t launch_tiles(const Fp8GemmArgs& g, hipStream_t s) {
-  constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
-  const int tiles_m = (g.M + TM - 1) / TM, tiles_n = (g.N + TN - 1) / TN;
-  const dim3 grid((unsigned)tiles_m * (unsigned)tiles_n), block(WN * WM * 64);
-  if (g.out_dtype == NVFP4_DTYPE_BF16)
-    fp8_tile_kernel<FN, FM, WN, WM, false, NVFP4_DTYPE_BF16><<<grid, block, 0, s>>>(g, tiles_m, tiles_n);
-  else
-    fp8_tile_kernel<FN, FM, WN, WM, true, NVFP4_DTYPE_F32><<<grid, block, 0, s>>>(g, tiles_m, tiles_n);
+template <int FN, int FM, int WN, int WM, int D, bool EXACT, int OUT>
+hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
+  using T = Ring<FN, FM, WN, WM, D>;
+  static_assert(T::TN * T::TM <= 128 * 128, "a partial tile's room in the workspace");
+  const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (g.N + T::TN - 1) / T::TN, blocks = (g.K + 127) / 128;
+  const int64_t tiles = (int64_t)tiles_m * tiles_n, steps = tiles * blocks;
+  const int groups = (int)(steps < kRingGroups ? steps : kRingGroups);
+  const auto fn = fp8_ring_kernel<FN, FM, WN, WM, D, EXACT, OUT>;
+  hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, D * T::kStage);
+  if (e != hipSuccess) return e;
+  fn<<<groups, 512, D * T::kStage, s>>>(g, tiles_m, tiles_n, ws);
+  if ((e = hipGetLastError()) != hipSuccess || tiles % groups == 0) return e;  // whole tiles each: nothing to join
+  fp8_join_kernel<FN, FM, WN, WM, D, OUT><<<dim3((unsigned)tiles, (T::TN * T::TM / 4 + 255) / 256), 256, 0, s>>>(g, tiles_m, groups, steps, ws);
   return hipGetLastError();
+}
+
+template <int FN, int FM, int WN, int WM, int D>
+hipError_t launch_ring(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
+  return g.out_dtype == NVFP4_DTYPE_BF16 ? launch_ring_as<FN, FM, WN, WM, D, false, NVFP4_DTYPE_BF16>(g, ws, s)
+                                         : launch_ring_as<FN, FM, WN, WM, D, true, NVFP4_DTYPE_F32>(g, ws, s);
+}
+
+// Tokens of the ring kernel's tiles.
+int ring_tokens(int64_t m) {
+  if (m <= 16) return 16;
+  if (m <= 32) return 32;
+  if (m <= 64) return 64;
+  if (m <= 128) return 128;
+  return 224;
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t s) {
-  if (g.M <= 16) return launch_tiles<1, 1, 2, 1>(g, s);
-  if (g.M <= 64) return launch_tiles<2, 2, 2, 2>(g, s);
-  if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 256) {
+// Two partial tiles of each workgroup.  Never less for more tokens, so that one workspace serves smaller calls too.
+size_t fp8_gemm_workspace(int64_t m) {
+  const int tm = ring_tokens(m);
+  return (size_t)kRingGroups * 2 * 128 * (tm < 128 ? tm : 128) * sizeof(float);
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
+  if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 224) {
     return launch_pipe<8, 7, 2, 2>(g, 0, g.N, s);
   }
-  return launch_tiles<4, 4, 2, 2>(g, s);
+  switch (ring_tokens(g.M)) {
+    case 16: return launch_ring<1, 1, 8, 1, 8>(g, ws, s);
+    case 32: return launch_ring<1, 2, 8, 1, 7>(g, ws, s);
+    case 64: return launch_ring<1, 4, 8, 1, 6>(g, ws, s);
+    case 128: return launch_ring<2, 4, 4, 2, 4>(g, ws, s);
+    default: return launch_ring<1, 7, 4, 2, 4>(g, ws, s);
+  }
 }
 
 }  // namespace nvfp4

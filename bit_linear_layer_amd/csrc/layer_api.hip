@@ -76,8 +76,8 @@ int check_product(int64_t m, int64_t n, int64_t k, void* out, int out_dtype, int
   return NVFP4_OK;
 }
 
-// The workspace of nvfp4_fp8_linear: codes [rows, cols], then scales [pieces, rows].
-int64_t linear_codes_bytes(int64_t rows, int64_t cols) { return (rows * cols + 15) / 16 * 16; }
+// The workspace of nvfp4_fp8_linear: the product's, then codes [rows, cols], then scales [pieces, rows].
+int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 int check_heads(const nvfp4_head_rows* r, int64_t tokens, int head_dim, int esz) {
   if (r->heads < 1 || r->heads > 4096) return NVFP4_ERR_SHAPE;
@@ -129,20 +129,26 @@ int nvfp4_fp8_quantize(const void* x, int x_dtype, int64_t ld_x, const nvfp4_fp8
   return status_from_hip(launch_fp8_quantize_blocks(x, x_dtype, q->rows, q->cols, ld_x, m, pow2, (hipStream_t)stream));
 }
 
+size_t nvfp4_fp8_gemm_workspace_bytes(int64_t rows) {
+  return rows < 0 || rows >= kIndexLimit ? 0 : fp8_gemm_workspace(rows);
+}
+
 int nvfp4_fp8_gemm(const nvfp4_fp8_tensor* a, const nvfp4_fp8_tensor* w, void* out, int out_dtype, int64_t ld_out,
-                   void* stream) {
+                   void* workspace, size_t workspace_bytes, void* stream) {
   Fp8GemmArgs g{};
   int st = check_fp8(a, g.a);
   if (st != NVFP4_OK || (st = check_fp8(w, g.w)) != NVFP4_OK) return st;
   if (a->block_rows != 1 || w->block_rows != 128 || a->cols != w->cols) return NVFP4_ERR_SHAPE;
   if ((st = check_product(a->rows, w->rows, a->cols, out, out_dtype, ld_out, g)) != NVFP4_OK) return st;
   if (a->rows == 0) return NVFP4_OK;
-  return status_from_hip(launch_fp8_gemm(g, (hipStream_t)stream));
+  if (workspace == nullptr || workspace_bytes < nvfp4_fp8_gemm_workspace_bytes(a->rows)) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+  return status_from_hip(launch_fp8_gemm(g, (float*)workspace, (hipStream_t)stream));
 }
 
 size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t cols) {
   if (check_fp8_shape(rows, cols) != NVFP4_OK || rows >= kSizeLimit / cols) return 0;
-  return 16 + (size_t)(linear_codes_bytes(rows, cols) + rows * pieces_of(cols) * 4);
+  return fp8_gemm_workspace(rows) + (size_t)(up16(rows * cols) + rows * pieces_of(cols) * 4);
 }
 
 int nvfp4_fp8_linear(const void* x, int x_dtype, int64_t rows, int64_t ld_x, const nvfp4_fp8_tensor* w, void* out,
@@ -161,10 +167,11 @@ int nvfp4_fp8_linear(const void* x, int x_dtype, int64_t rows, int64_t ld_x, con
   if ((st = check_rows(x, rows, ld_x, w->cols, esz)) != NVFP4_OK) return st;
   if (workspace == nullptr || workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
-  g.a = Fp8Mat{(uint8_t*)workspace, (float*)((uint8_t*)workspace + linear_codes_bytes(rows, w->cols)), w->cols, 1, rows};
+  uint8_t* codes = (uint8_t*)workspace + up16((int64_t)fp8_gemm_workspace(rows));
+  g.a = Fp8Mat{codes, (float*)(codes + up16(rows * w->cols)), w->cols, 1, rows};
   const hipError_t e = launch_fp8_quantize_rows(x, x_dtype, rows, w->cols, ld_x, g.a, false, (hipStream_t)stream);
   if (e != hipSuccess) return status_from_hip(e);
-  return status_from_hip(launch_fp8_gemm(g, (hipStream_t)stream));
+  return status_from_hip(launch_fp8_gemm(g, (float*)workspace, (hipStream_t)stream));
 }
 
 int nvfp4_qk_norm_rope(const nvfp4_head_rows* q, const nvfp4_head_rows* k, int dtype, int64_t tokens, int head_dim, float eps,

@@ -29,7 +29,8 @@ struct Fp8GemmArgs {
   int out_dtype;
   int M, N, K;
 };
-hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t s);
+size_t fp8_gemm_workspace(int64_t m);  // bytes for products of up to 2^31 columns with m tokens
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s);
 
 struct RopeArgs {
   nvfp4_head_rows rows[2];  // queries, keys; heads 0 where absent

@@ -591,6 +591,10 @@ enum {
  */
 int nvfp4_fp8_quantize(const void* x, int x_dtype, int64_t ld_x, const nvfp4_fp8_tensor* q, int flags, void* stream);
 
+/* Bytes of device workspace nvfp4_fp8_gemm needs for a->rows rows (any
+ * weight): 4 MB up to 16 rows, 32 MB at most.  0 for a number it does not take. */
+size_t nvfp4_fp8_gemm_workspace_bytes(int64_t rows);
+
 /*
  * nvfp4_fp8_gemm -- out[m, n] = sum over blocks b of 128 columns of
  *     a_scale[m, b] * w_scale[n / 128, b] * sum_{k in b} e4m3(a[m, k]) e4m3(w[n, k])
@@ -607,10 +611,14 @@ int nvfp4_fp8_quantize(const void* x, int x_dtype, int64_t ld_x, const nvfp4_fp8
  * distributed data, where bf16's own rounding is 1.7e-3.  A NaN code reaches
  * its row (a) or column (w) only.
  * The product of two scales is a float32: below 2^-126 it loses bits.
+ *   workspace DEVICE, >= nvfp4_fp8_gemm_workspace_bytes(M) bytes, 16-byte
+ *             aligned, contents arbitrary; calls that may overlap in time need
+ *             one each.
  * M = 0 is a valid call that does nothing.  The same call gives the same bits.
+ * At most two launches.
  */
 int nvfp4_fp8_gemm(const nvfp4_fp8_tensor* a, const nvfp4_fp8_tensor* w, void* out, int out_dtype, int64_t ld_out,
-                   void* stream);
+                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace nvfp4_fp8_linear needs for rows x cols
  * activations; 0 for a shape that it does not take. */

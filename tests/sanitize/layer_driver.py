@@ -28,7 +28,8 @@ libc.free.argtypes = [P]
 def main(path):
     lib = ctypes.CDLL(path)
     lib.nvfp4_fp8_quantize.argtypes = [P, I32, I64, P, I32, P]
-    lib.nvfp4_fp8_gemm.argtypes = [P, P, P, I32, I64, P]
+    lib.nvfp4_fp8_gemm.argtypes = [P, P, P, I32, I64, P, SZ, P]
+    lib.nvfp4_fp8_gemm_workspace_bytes.argtypes, lib.nvfp4_fp8_gemm_workspace_bytes.restype = [I64], SZ
     lib.nvfp4_fp8_linear_workspace_bytes.argtypes, lib.nvfp4_fp8_linear_workspace_bytes.restype = [I64, I64], SZ
     lib.nvfp4_fp8_linear.argtypes = [P, I32, I64, I64, P, P, I32, I64, P, SZ, P]
     lib.nvfp4_qk_norm_rope.argtypes = [P, P, I32, I64, I32, F, F, P, P]
@@ -74,7 +75,8 @@ def main(path):
                 q = a if rng.random() < 0.5 else w
                 st = lib.nvfp4_fp8_quantize(at(), dt, odd(up(safe, 16)), block(q), rng.choice([0, 0, 1, 1, 2]), None)
             elif which == 1:
-                st = lib.nvfp4_fp8_gemm(block(a), block(w), at(), dt, odd(max(0, min(n, 1 << 40))), None)
+                st = lib.nvfp4_fp8_gemm(block(a), block(w), at(), dt, odd(max(0, min(n, 1 << 40))), at(),
+                                        max(0, lib.nvfp4_fp8_gemm_workspace_bytes(m) - (rng.random() < 0.02)), None)
                 want = (m, n, k)
             else:
                 need = lib.nvfp4_fp8_linear_workspace_bytes(m, k)

@@ -27,7 +27,8 @@ hipError_t launch_fp8_quantize_rows(const void*, int, int64_t rows, int64_t cols
 hipError_t launch_fp8_quantize_blocks(const void*, int, int64_t rows, int64_t cols, int64_t, const Fp8Mat& q, bool, hipStream_t) {
   return record(rows, cols, q.ld_codes, q.scale_block);
 }
-hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t) { return record(g.M, g.N, g.K, g.ld_out); }
+size_t fp8_gemm_workspace(int64_t m) { return (m <= 16 ? 1 : 8) << 22; }
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float*, hipStream_t) { return record(g.M, g.N, g.K, g.ld_out); }
 hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t) { return record(a.tokens, a.rows[0].heads, a.rows[1].heads, a.rope.rotary_dim); }
 hipError_t launch_causal_conv(const nvfp4_conv& c, int, hipStream_t) { return record(c.tokens, c.channels, c.batch, c.width); }
 hipError_t launch_gdn_step(const GdnStepArgs& a, hipStream_t) { return record(a.batch, a.q_len, a.hk, a.hv); }

@@ -116,7 +116,7 @@ def close(out, a, w, extra=0.0):
     assert bad.size == 0, f"{len(bad)} of {err.size} outside, first {bad[:3].tolist()}: {[(err[i, j], tol[i, j]) for i, j in bad[:3]]}"
 
 
-SHAPES = [(1, 1, 16), (1, 128, 128), (2, 130, 144), (3, 1000, 272), (5, 4096, 1040), (15, 64, 4096), (16, 129, 2064), (17, 257, 128),
+SHAPES = [(1, 1, 16), (4, 384, 6400), (16, 200, 17408), (30, 640, 3600), (100, 130, 6400), (130, 130, 9984), (224, 128, 16384), (225, 192, 400), (1, 128, 128), (2, 130, 144), (3, 1000, 272), (5, 4096, 1040), (15, 64, 4096), (16, 129, 2064), (17, 257, 128),
           (33, 100, 640), (64, 512, 1024), (65, 384, 2064), (77, 1000, 400), (128, 128, 128), (129, 640, 256), (200, 1111, 912),
           (257, 513, 384), (300, 256, 3200), (511, 1280, 512)]
 
@@ -158,11 +158,12 @@ def test_output_strides_and_neighbours(m, n):
     """Rows of the output at odd places, nothing written beside them."""
     say(f"fp8 gemm strides {m}x{n}")
     a, w = operands(np.random.default_rng(m + n), m, n, 272)
+    ws = nv.fp8_gemm_workspace(m)
     for out_dtype in (BF16, F32):
         whole = nv.fp8_gemm(a, w, out_dtype)
         for lead, pad in ((0, 8), (1, 0), (3, 2)):
             buf = torch.full((m + 1, lead + n + pad), -7.0, dtype=out_dtype, device=DEV)
-            nv.nvfp4_fp8_gemm(a, w, buf[:m, lead: lead + n])
+            nv.nvfp4_fp8_gemm(a, w, buf[:m, lead: lead + n], ws)
             assert torch.equal(buf[:m, lead: lead + n], whole)
             buf[:m, lead: lead + n] = -7
             assert bool((buf == -7).all())

@@ -29,11 +29,11 @@ def quantize(q=None, x=FAKE, dt=0, ld=272, flags=0):
     return nv.load().nvfp4_fp8_quantize(x, dt, ld, ref(q or fp8()), flags, None)
 
 
-def gemm(a=None, w=None, out=FAKE, dt=0, ld=130):
-    return nv.load().nvfp4_fp8_gemm(ref(a or fp8()), ref(w or fp8(rows=130, block=128)), out, dt, ld, None)
+def gemm(a=None, w=None, out=FAKE, dt=0, ld=130, ws=FAKE, wsb=1 << 30):
+    return nv.load().nvfp4_fp8_gemm(ref(a or fp8()), ref(w or fp8(rows=130, block=128)), out, dt, ld, ws, wsb, None)
 
 
-def linear(w=None, x=FAKE, dt=0, rows=5, ld=272, out=FAKE, odt=0, ldo=130, ws=FAKE, wsb=1 << 20):
+def linear(w=None, x=FAKE, dt=0, rows=5, ld=272, out=FAKE, odt=0, ldo=130, ws=FAKE, wsb=1 << 30):
     return nv.load().nvfp4_fp8_linear(x, dt, rows, ld, ref(w or fp8(rows=130, block=128)), out, odt, ldo, ws, wsb, None)
 
 
@@ -67,7 +67,8 @@ def test_bad_quantize(kw, status):
     (dict(a=fp8(block=128)), -2), (dict(w=fp8(rows=130)), -2), (dict(w=fp8(rows=130, block=128, cols=256)), -2),
     (dict(w=fp8(rows=0, block=128)), -2), (dict(ld=1 << 31), -11), (dict(a=fp8(rows=(1 << 31) - 1), ld=1 << 30), -11),
     (dict(w=fp8(rows=(1 << 31) - 1, block=128), ld=(1 << 31) - 1), -11),
-    (dict(a=fp8(rows=0, codes=None, scales=None), out=None), 0),
+    (dict(ws=None), -8), (dict(wsb=1000), -8), (dict(ws=FAKE + 8), -5),
+    (dict(a=fp8(rows=0, codes=None, scales=None), out=None, ws=None), 0),
 ])
 def test_bad_product(kw, status):
     assert gemm(**kw) == status
@@ -87,6 +88,10 @@ def test_linear_workspace():
     assert f(5, 272) >= 5 * 272 + 5 * 3 * 4 and f(0, 272) > 0
     assert f(-1, 272) == 0 and f(5, 271) == 0 and f(5, 0) == 0 and f(1 << 31, 272) == 0 and f(1 << 30, 1 << 20) == 0 and f(BIG, BIG) == 0
     assert linear(wsb=f(5, 272) - 1) == -8
+    f = nv.nvfp4_fp8_gemm_workspace_bytes
+    sizes = [f(n) for n in (0, 1, 16, 17, 64, 128, 129, 5000, (1 << 31) - 1)]
+    assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] <= 1 << 25 and f(-1) == 0 and f(1 << 31) == 0
+    assert gemm(wsb=f(5) - 1) == -8
     with pytest.raises(nv.NVFP4Error):
         nv.fp8_linear_workspace(5, 100, "cpu")
 
@@ -200,7 +205,7 @@ def test_the_binding_takes_gpu_tensors_only():
     refused(nv.nvfp4_fp8_quantize, x, q)
     refused(nv.fp8_quantize, x, 64)
     refused(nv.fp8_quantize, x[0])
-    refused(nv.nvfp4_fp8_gemm, q, nv.empty_fp8(128, 128, 128, "cpu"), x)
+    refused(nv.nvfp4_fp8_gemm, q, nv.empty_fp8(128, 128, 128, "cpu"), x, x)
     refused(nv.fp8_linear, x[0], q)
     refused(nv.nvfp4_qk_norm_rope, None, None, None, None, 64)
     refused(nv.qk_norm_rope, x, x, 64)
