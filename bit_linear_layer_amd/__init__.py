@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -79,27 +80,14 @@ class _KVBatch(ctypes.Structure):
                 ("ld_table", ctypes.c_int64), ("prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int64)]
 
 
-class _FP8(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
-                ("ld_codes", ctypes.c_int64), ("ld_scales", ctypes.c_int64), ("block_rows", ctypes.c_int)]
-
-
-class _HeadRows(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("head_x", ctypes.c_int64), ("out", ctypes.c_void_p),
-                ("ld_out", ctypes.c_int64), ("head_out", ctypes.c_int64), ("weight", ctypes.c_void_p), ("heads", ctypes.c_int)]
-
-
-class _Rope(ctypes.Structure):
-    _fields_ = [("positions", ctypes.c_void_p), ("ld_positions", ctypes.c_int64), ("inv_freq", ctypes.c_void_p),
-                ("axis", ctypes.c_void_p), ("axes", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
-
-
-class _Conv(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
-                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("channels", ctypes.c_int64),
-                ("batch", ctypes.c_int64), ("width", ctypes.c_int), ("silu", ctypes.c_int), ("starts", ctypes.c_void_p),
-                ("state", ctypes.c_void_p), ("n_states", ctypes.c_int64), ("ld_state", ctypes.c_int64),
-                ("slots", ctypes.c_void_p), ("fresh", ctypes.c_void_p)]
+# The structs of the 8-bit layers, the rotation and the convolution, as the
+# bytes that C sees (native alignment): building them costs a third of a
+# ctypes.Structure, which shows in calls of a few microseconds.
+_FP8 = struct.Struct("PPqqqqi4x").pack          # codes, scales, rows, cols, ld_codes, ld_scales, block_rows
+_HEAD_ROWS = struct.Struct("PqqPqqPi4x").pack   # x, ld_x, head_x, out, ld_out, head_out, weight, heads
+_ROPE = struct.Struct("PqPPiii4x").pack         # positions, ld_positions, inv_freq, axis, axes, rotary_dim, interleaved
+_CONV = struct.Struct("PqPqPPqqqiiPPqqPP").pack  # as nvfp4_conv
+_GDN_INPUTS = struct.Struct("PqPqPqPqPq").pack  # as nvfp4_gdn_inputs
 
 
 _lib = None
@@ -171,7 +159,7 @@ def load() -> ctypes.CDLL:
         lib.nvfp4_kv_pages_attention.argtypes = [pages, batch, _P, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_float, _P,
                                                  _I64, _P, ctypes.c_size_t, _P]
         lib.nvfp4_kv_pages_attention.restype = ctypes.c_int
-        fp8 = ctypes.POINTER(_FP8)
+        fp8 = _P
         lib.nvfp4_fp8_quantize.argtypes = [_P, ctypes.c_int, _I64, fp8, ctypes.c_int, _P]
         lib.nvfp4_fp8_quantize.restype = ctypes.c_int
         lib.nvfp4_fp8_gemm.argtypes = [fp8, fp8, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
@@ -182,13 +170,11 @@ def load() -> ctypes.CDLL:
         lib.nvfp4_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
         lib.nvfp4_fp8_linear.argtypes = [_P, ctypes.c_int, _I64, _I64, fp8, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]
         lib.nvfp4_fp8_linear.restype = ctypes.c_int
-        heads = ctypes.POINTER(_HeadRows)
-        lib.nvfp4_qk_norm_rope.argtypes = [heads, heads, ctypes.c_int, _I64, ctypes.c_int, ctypes.c_float, ctypes.c_float,
-                                           ctypes.POINTER(_Rope), _P]
+        lib.nvfp4_qk_norm_rope.argtypes = [_P, _P, ctypes.c_int, _I64, ctypes.c_int, ctypes.c_float, ctypes.c_float, _P, _P]
         lib.nvfp4_qk_norm_rope.restype = ctypes.c_int
-        lib.nvfp4_causal_conv.argtypes = [ctypes.POINTER(_Conv), ctypes.c_int, _P]
+        lib.nvfp4_causal_conv.argtypes = [_P, ctypes.c_int, _P]
         lib.nvfp4_causal_conv.restype = ctypes.c_int
-        lib.nvfp4_gdn_step.argtypes = [ctypes.POINTER(_GdnInputs), ctypes.c_int, _I64, _I64, ctypes.c_int, ctypes.c_int,
+        lib.nvfp4_gdn_step.argtypes = [_P, ctypes.c_int, _I64, _I64, ctypes.c_int, ctypes.c_int,
                                        ctypes.c_int, _P, _I64, _I64, _P, _P, _P, ctypes.c_int, _I64, _P]
         lib.nvfp4_gdn_step.restype = ctypes.c_int
         lib.nvfp4_status_string.argtypes = [ctypes.c_int]
@@ -593,7 +579,7 @@ def _kv_slots(slots: torch.Tensor, device: torch.device) -> int:
 def _call_on(device: torch.device, stream, f, *args) -> int:
     """f(*args, stream) with ``device`` as the current GPU, on ``stream`` or
     the device's current one."""
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         with torch.cuda.device(device):
             return _call_on(device, stream, f, *args)
     return f(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(device, stream))
@@ -697,14 +683,15 @@ class FP8Tensor:
     cols: int
     block_rows: int = 1
 
-    def descriptor(self) -> _FP8:
+    def descriptor(self) -> bytes:
         c, s, rows, cols = self.codes, self.scales, self.rows, self.cols
         high, wide = -(-rows // self.block_rows) if self.block_rows > 0 else 0, -(-cols // 128)
-        if c.dtype is not torch.uint8 or c.dim() != 2 or c.shape[0] != rows or c.shape[1] < cols or c.stride(1) != 1:
+        cs, ss, device = c.shape, s.shape, c.device
+        if c.dtype is not torch.uint8 or len(cs) != 2 or cs[0] != rows or cs[1] < cols or c.stride(1) != 1:
             raise NVFP4Error(f"codes must be uint8 [{rows}, >= {cols}] with contiguous rows")
-        if s.dtype is not torch.float32 or s.dim() != 2 or s.shape[0] != high or s.shape[1] < wide or s.stride(1) != 1:
+        if s.dtype is not torch.float32 or len(ss) != 2 or ss[0] != high or ss[1] < wide or s.stride(1) != 1:
             raise NVFP4Error(f"scales must be float32 [{high}, >= {wide}] with contiguous rows")
-        if c.device.type != "cuda" or s.device != c.device:
+        if device.type != "cuda" or s.device != device:
             raise NVFP4Error("codes and scales must live on one GPU")
         return _FP8(c.data_ptr(), s.data_ptr(), rows, cols, c.stride(0) if rows > 1 else _round_up(cols, 16),
                     s.stride(0) if high > 1 else wide, self.block_rows)
@@ -721,7 +708,7 @@ def nvfp4_fp8_quantize(x: torch.Tensor, q: FP8Tensor, flags: int = FP8_SCALE_F32
     """C ``nvfp4_fp8_quantize``: x (bf16 or float32, rows may be strided) into q."""
     d, device = q.descriptor(), q.codes.device
     ld = _row_stride(x, q.rows, q.cols, device, "x")
-    _check(_call_on(device, stream, load().nvfp4_fp8_quantize, x.data_ptr(), _dtype_code(x), ld, ctypes.byref(d), flags),
+    _check(_call_on(device, stream, load().nvfp4_fp8_quantize, x.data_ptr(), _dtype_code(x), ld, d, flags),
            "nvfp4_fp8_quantize")
 
 
@@ -742,8 +729,8 @@ def nvfp4_fp8_gemm(a: FP8Tensor, w: FP8Tensor, out: torch.Tensor, workspace: tor
     da, dw, device = a.descriptor(), w.descriptor(), w.codes.device
     _on(a.codes, device, "a")
     ld = _row_stride(out, a.rows, w.rows, device, "out")
-    _check(_call_on(device, stream, load().nvfp4_fp8_gemm, ctypes.byref(da), ctypes.byref(dw), out.data_ptr(), _dtype_code(out),
-                    ld, *_space(workspace, device)), "nvfp4_fp8_gemm")
+    _check(_call_on(device, stream, load().nvfp4_fp8_gemm, da, dw, out.data_ptr(), _dtype_code(out), ld,
+                    *_space(workspace, device)), "nvfp4_fp8_gemm")
 
 
 def nvfp4_fp8_linear_workspace_bytes(rows: int, cols: int) -> int:
@@ -759,11 +746,11 @@ def nvfp4_fp8_linear(x: torch.Tensor, w: FP8Tensor, out: torch.Tensor, workspace
         raise NVFP4Error(f"x must be [rows, {w.cols}], got {list(x.shape)}")
     rows = x.shape[0]
     ld_x, ld_o = _row_stride(x, rows, w.cols, device, "x"), _row_stride(out, rows, w.rows, device, "out")
-    _check(_call_on(device, stream, load().nvfp4_fp8_linear, x.data_ptr(), _dtype_code(x), rows, ld_x, ctypes.byref(d),
-                    out.data_ptr(), _dtype_code(out), ld_o, *_space(workspace, device)), "nvfp4_fp8_linear")
+    _check(_call_on(device, stream, load().nvfp4_fp8_linear, x.data_ptr(), _dtype_code(x), rows, ld_x, d, out.data_ptr(),
+                    _dtype_code(out), ld_o, *_space(workspace, device)), "nvfp4_fp8_linear")
 
 
-@dataclass
+@dataclass(frozen=True)
 class Rope:
     """The rotation of ``nvfp4_qk_norm_rope``: float32 inv_freq [rotary_dim /
     2], and with more than one position axis the uint8 axis of each pair;
@@ -772,51 +759,61 @@ class Rope:
     axis: torch.Tensor | None = None
     interleaved: bool = False
 
-    def descriptor(self, positions: torch.Tensor, tokens: int, device: torch.device) -> _Rope:
+    def __post_init__(self):
         f, axis = self.inv_freq, self.axis
         if f.dtype is not torch.float32 or f.dim() != 1 or not f.is_contiguous():
             raise NVFP4Error("inv_freq must be a contiguous 1-D float32 tensor")
-        _on(f, device, "inv_freq")
         if axis is not None:
             if axis.dtype is not torch.uint8 or axis.shape != f.shape or not axis.is_contiguous():
                 raise NVFP4Error(f"axis must be a contiguous uint8 [{f.shape[0]}] tensor")
-            _on(axis, device, "axis")
-        if positions.dtype is not torch.int64 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens \
+            _on(axis, f.device, "axis")
+
+    def descriptor(self, positions: torch.Tensor, tokens: int, device: torch.device) -> bytes:
+        f, axis, shape = self.inv_freq, self.axis, positions.shape
+        axes = shape[0] if len(shape) == 2 else 1
+        if positions.dtype is not torch.int64 or len(shape) not in (1, 2) or shape[-1] != tokens \
                 or tokens > 1 and positions.stride(-1) != 1:
             raise NVFP4Error(f"positions must be int64 [{tokens}] or [axes, {tokens}] with contiguous rows")
-        _on(positions, device, "positions")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions.device != device or f.device != device:
+            raise NVFP4Error(f"positions and inv_freq must live on {device}")
         if axis is None and axes != 1:
             raise NVFP4Error("positions with more than one axis need a Rope with axis")
-        ld = positions.stride(0) if positions.dim() == 2 and axes > 1 else tokens
-        return _Rope(positions.data_ptr(), ld, f.data_ptr(), _ptr(axis), axes, 2 * f.shape[0], int(self.interleaved))
+        return _ROPE(positions.data_ptr(), positions.stride(0) if axes > 1 else tokens, f.data_ptr(),
+                     0 if axis is None else axis.data_ptr(), axes, 2 * f.shape[0], int(self.interleaved))
 
 
 def _heads_of(x: torch.Tensor, tokens: int, head_dim: int, device: torch.device, what: str):
     """(heads, row stride, head stride) of [tokens, heads * head_dim] or [tokens, heads, head_dim]."""
-    if x.dim() == 3:
-        if x.shape[0] != tokens or x.shape[2] != head_dim or x.shape[1] == 0 or x.stride(2) != 1:
-            raise NVFP4Error(f"{what} must be [{tokens}, heads, {head_dim}] with contiguous heads, got {list(x.shape)}")
-        _on(x, device, what)
-        heads, head = x.shape[1], x.stride(1) if x.shape[1] > 1 else head_dim
-        return heads, x.stride(0) if tokens > 1 else (heads - 1) * head + head_dim, head
-    if x.dim() != 2 or x.shape[1] == 0 or x.shape[1] % head_dim != 0:
-        raise NVFP4Error(f"{what} must be [{tokens}, heads * {head_dim}], got {list(x.shape)}")
-    return x.shape[1] // head_dim, _row_stride(x, tokens, x.shape[1], device, what), head_dim
+    shape, stride = x.shape, x.stride()
+    if x.device != device:
+        raise NVFP4Error(f"{what} must live on {device}, got {x.device}")
+    if len(shape) == 2:
+        heads, rest = divmod(shape[1], head_dim)
+        if shape[0] == tokens and heads > 0 and rest == 0 and stride[1] == 1:
+            return heads, stride[0] if tokens > 1 else shape[1], head_dim
+    elif len(shape) == 3 and shape[0] == tokens and shape[1] > 0 and shape[2] == head_dim and stride[2] == 1:
+        heads = shape[1]
+        head = stride[1] if heads > 1 else head_dim
+        return heads, stride[0] if tokens > 1 else (heads - 1) * head + head_dim, head
+    raise NVFP4Error(f"{what} must be [{tokens}, heads * {head_dim}] or [{tokens}, heads, {head_dim}] with contiguous heads, "
+                     f"got {list(shape)}")
 
 
 def _head_rows(x, out, weight, tokens: int, head_dim: int, dtype, device: torch.device, what: str):
     if x is None:
         return None
-    if out is None or out.shape != x.shape or x.dtype != dtype or out.dtype != dtype:
+    if out is None or x.dtype is not dtype or out.dtype is not dtype or out.shape != x.shape:
         raise NVFP4Error(f"{what} and its output must share shape and dtype, queries and keys one dtype")
     heads, ld, head = _heads_of(x, tokens, head_dim, device, what)
-    _, ld_o, head_o = _heads_of(out, tokens, head_dim, device, what + "_out")
+    _, ld_o, head_o = _heads_of(out, tokens, head_dim, device, what)
+    w = 0
     if weight is not None:
         if weight.dtype is not torch.float32 or weight.shape != (head_dim,) or not weight.is_contiguous():
             raise NVFP4Error(f"the weight of {what} must be a contiguous float32 [{head_dim}] tensor")
-        _on(weight, device, f"the weight of {what}")
-    return ctypes.byref(_HeadRows(x.data_ptr(), ld, head, out.data_ptr(), ld_o, head_o, _ptr(weight), heads))
+        if weight.device != device:
+            raise NVFP4Error(f"the weight of {what} must live on {device}")
+        w = weight.data_ptr()
+    return _HEAD_ROWS(x.data_ptr(), ld, head, out.data_ptr(), ld_o, head_o, w, heads)
 
 
 def nvfp4_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None, k_out: torch.Tensor | None,
@@ -829,26 +826,44 @@ def nvfp4_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: to
     lead = q if q is not None else k
     if lead is None:
         raise NVFP4Error("one of q and k is needed")
-    tokens, device = lead.shape[0], lead.device
+    tokens, device, dtype = lead.shape[0], lead.device, lead.dtype
     if device.type != "cuda":
         raise NVFP4Error("q and k must live on a GPU")
+    if head_dim < 1:
+        raise NVFP4Error("head_dim must be 64, 128 or 256")
     dt = _dtype_code(lead)
     if (rope is None) != (positions is None):
         raise NVFP4Error("rope and positions come together")
-    hq = _head_rows(q, q_out, q_weight, tokens, head_dim, lead.dtype, device, "q")
-    hk = _head_rows(k, k_out, k_weight, tokens, head_dim, lead.dtype, device, "k")
-    r = None if rope is None else ctypes.byref(rope.descriptor(positions, tokens, device))
+    hq = _head_rows(q, q_out, q_weight, tokens, head_dim, dtype, device, "q")
+    hk = _head_rows(k, k_out, k_weight, tokens, head_dim, dtype, device, "k")
+    r = None if rope is None else rope.descriptor(positions, tokens, device)
     _check(_call_on(device, stream, load().nvfp4_qk_norm_rope, hq, hk, dt, tokens, head_dim, eps, weight_offset, r),
            "nvfp4_qk_norm_rope")
 
 
-def _per_sequence(t: torch.Tensor | None, n: int, dtype, device: torch.device, what: str):
+def _per_sequence(t: torch.Tensor | None, n: int, dtype, device: torch.device, what: str) -> int:
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise NVFP4Error(f"{what} must be a contiguous {str(dtype)[6:]} [{n}] tensor")
-    _on(t, device, what)
+    if t.device != device:
+        raise NVFP4Error(f"{what} must live on {device}, got {t.device}")
     return t.data_ptr()
+
+
+def _state_stride(states: torch.Tensor, shape: tuple, dtype, device: torch.device, what: str) -> int:
+    """Elements from one state to the next of a pool [n > 0, *shape] whose states are contiguous."""
+    full, stride, want = states.shape, states.stride(), 1
+    ok = states.dtype is dtype and len(full) == len(shape) + 1 and full[1:] == shape and full[0] > 0
+    if ok:
+        for n, by in zip(reversed(shape), reversed(stride)):
+            ok = ok and (by == want or n == 1)
+            want *= n
+    if not ok:
+        raise NVFP4Error(f"{what} must be {str(dtype)[6:]} [n, {', '.join(map(str, shape))}], each state contiguous")
+    if states.device != device:
+        raise NVFP4Error(f"{what} must live on {device}, got {states.device}")
+    return stride[0] if full[0] > 1 else want
 
 
 def nvfp4_causal_conv(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, batch: int, starts: torch.Tensor | None = None,
@@ -872,20 +887,16 @@ def nvfp4_causal_conv(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, ba
         raise NVFP4Error("y must have x's dtype")
     n_states = ld_state = 0
     if state is not None:
-        if state.dtype != x.dtype or state.dim() != 3 or state.shape[1:] != (width - 1, channels) \
-                or state.shape[0] == 0 or not state[0].is_contiguous():
-            raise NVFP4Error(f"state must be [n_states, {width - 1}, {channels}] of x's dtype, each state contiguous")
-        _on(state, device, "state")
+        ld_state = _state_stride(state, (width - 1, channels), x.dtype, device, "state")
         n_states = state.shape[0]
-        ld_state = state.stride(0) if n_states > 1 else (width - 1) * channels
     elif slots is not None or fresh is not None:
         raise NVFP4Error("slots and fresh need a state")
     i32 = torch.int32
-    c = _Conv(x.data_ptr(), ld_x, y.data_ptr(), ld_y, weight.data_ptr(), _per_sequence(bias, channels, torch.float32, device, "bias"),
-              tokens, channels, batch, width, int(silu), _per_sequence(starts, batch + 1, i32, device, "starts"), _ptr(state),
-              n_states, ld_state, _per_sequence(slots, batch, i32, device, "slots"),
+    c = _CONV(x.data_ptr(), ld_x, y.data_ptr(), ld_y, weight.data_ptr(), _per_sequence(bias, channels, torch.float32, device, "bias"),
+              tokens, channels, batch, width, int(silu), _per_sequence(starts, batch + 1, i32, device, "starts"),
+              0 if state is None else state.data_ptr(), n_states, ld_state, _per_sequence(slots, batch, i32, device, "slots"),
               _per_sequence(fresh, batch, torch.uint8, device, "fresh"))
-    _check(_call_on(device, stream, load().nvfp4_causal_conv, ctypes.byref(c), _dtype_code(x)), "nvfp4_causal_conv")
+    _check(_call_on(device, stream, load().nvfp4_causal_conv, c, _dtype_code(x)), "nvfp4_causal_conv")
 
 
 def nvfp4_gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, g: torch.Tensor, o: torch.Tensor,
@@ -900,22 +911,16 @@ def nvfp4_gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torc
     rows, device, dt = q.shape[0], q.device, _dtype_code(q)
     if device.type != "cuda":
         raise NVFP4Error("q must live on a GPU")
-    batch = rows // q_len
-    if any(t.dtype != q.dtype for t in (k, v, beta, g)):
+    batch, dtype, kw, vw = rows // q_len, q.dtype, k_heads * 128, v_heads * 128
+    if k.dtype is not dtype or v.dtype is not dtype or beta.dtype is not dtype or g.dtype is not dtype:
         raise NVFP4Error("q, k, v, beta and g must share one dtype")
-    ins = []
-    for name, t, width in (("q", q, k_heads * 128), ("k", k, k_heads * 128), ("v", v, v_heads * 128), ("beta", beta, v_heads),
-                           ("g", g, v_heads)):
-        ins += [t.data_ptr(), _row_stride(t, rows, width, device, name)]
-    ld_o = _row_stride(o, rows, v_heads * 128, device, "o")
-    if states.dtype is not torch.float32 or states.dim() != 4 or states.shape[1:] != (v_heads, 128, 128) \
-            or states.shape[0] > 0 and not states[0].is_contiguous():
-        raise NVFP4Error(f"states must be float32 [n_states, {v_heads}, 128, 128], each state contiguous")
-    _on(states, device, "states")
-    ld_s = states.stride(0) if states.shape[0] > 1 else v_heads * 16384
-    _check(_call_on(device, stream, load().nvfp4_gdn_step, ctypes.byref(_GdnInputs(*ins)), dt, batch, q_len, k_heads, v_heads,
-                    int(normalize_qk), states.data_ptr(), states.shape[0], ld_s,
-                    _per_sequence(slots, batch, torch.int32, device, "slots"),
+    ins = _GDN_INPUTS(q.data_ptr(), _row_stride(q, rows, kw, device, "q"), k.data_ptr(), _row_stride(k, rows, kw, device, "k"),
+                      v.data_ptr(), _row_stride(v, rows, vw, device, "v"), beta.data_ptr(),
+                      _row_stride(beta, rows, v_heads, device, "beta"), g.data_ptr(), _row_stride(g, rows, v_heads, device, "g"))
+    ld_o = _row_stride(o, rows, vw, device, "o")
+    ld_s = _state_stride(states, (v_heads, 128, 128), torch.float32, device, "states")
+    _check(_call_on(device, stream, load().nvfp4_gdn_step, ins, dt, batch, q_len, k_heads, v_heads, int(normalize_qk),
+                    states.data_ptr(), states.shape[0], ld_s, _per_sequence(slots, batch, torch.int32, device, "slots"),
                     _per_sequence(fresh, batch, torch.uint8, device, "fresh"), o.data_ptr(), _dtype_code(o), ld_o),
            "nvfp4_gdn_step")
 
@@ -1136,7 +1141,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, head_dim: int, positions: tor
                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
                  weight_offset: float = 0.0):
     """(queries, keys), normed per head and rotated, as new contiguous tensors."""
-    q_out, k_out = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    q_out, k_out = (torch.empty_like(x, memory_format=torch.contiguous_format) for x in (q, k))
     nvfp4_qk_norm_rope(q, k, q_out, k_out, head_dim, positions, rope, q_weight, k_weight, eps, weight_offset)
     return q_out, k_out
 

@@ -88,7 +88,7 @@ __device__ inline int64_t start_of(const nvfp4_conv& c, int64_t each, int64_t b)
 
 template <int DT, int W>
 __global__ __launch_bounds__(kElemThreads) void causal_conv_kernel(const nvfp4_conv c, int64_t each, int run, int64_t threads) {
-  constexpr int kBytes = DT == NVFP4_DTYPE_BF16 ? 16 : 32, kOld = W - 1;
+  constexpr int kBytes = DT == NVFP4_DTYPE_BF16 ? 16 : 32, kOld = W - 1, kAhead = 4;
   const int64_t id = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
   if (id >= threads) return;
   const int64_t chunks = c.channels / 8, chunk = id % chunks;
@@ -155,8 +155,8 @@ __global__ __launch_bounds__(kElemThreads) void causal_conv_kernel(const nvfp4_c
 #pragma unroll
       for (int j = 0; j < kOld; ++j) Eight<DT>::load(x + (t - kOld + j) * ldx).floats(in[j]);
     }
-    for (; t < end; ++t) {
-      Eight<DT>::load(x + t * ldx).floats(in[W - 1]);
+    auto token = [&](const Eight<DT>& now, int64_t at) {
+      now.floats(in[W - 1]);
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -165,31 +165,94 @@ __global__ __launch_bounds__(kElemThreads) void causal_conv_kernel(const nvfp4_c
         for (int j = 0; j < W; ++j) u = fmaf(w[e][j], in[j][e], u);
         v[e] = c.silu ? silu(u) : u;
       }
-      Eight<DT>::of(v).stream(y + t * ldy);
+      Eight<DT>::of(v).stream(y + at * ldy);
 #pragma unroll
       for (int j = 0; j < kOld; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) in[j][e] = in[j + 1][e];
+    };
+    for (; t + kAhead <= end; t += kAhead) {
+      Eight<DT> now[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) now[u] = Eight<DT>::load(x + (t + u) * ldx);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) token(now[u], t + u);
     }
+    for (; t < end; ++t) token(Eight<DT>::load(x + t * ldx), t);
   }
 }
 
-template <int DT>
+// One token of each sequence: a thread per sequence and 8 channels.  Nothing
+// waits for the slot but the state itself.
+template <int DT, int W>
+__global__ __launch_bounds__(kElemThreads) void causal_conv_step_kernel(const nvfp4_conv c) {
+  constexpr int kBytes = DT == NVFP4_DTYPE_BF16 ? 16 : 32, kOld = W - 1;
+  const int64_t id = (int64_t)blockIdx.x * kElemThreads + threadIdx.x;
+  const int64_t chunks = c.channels / 8, b = id / chunks, chunk = id - b * chunks;
+  if (b >= c.batch) return;
+  const int64_t slot = c.state == nullptr ? -1 : c.slots != nullptr ? (int64_t)c.slots[b] : b;
+  const bool fresh = c.fresh != nullptr && c.fresh[b] != 0;
+  const Eight<DT> now = Eight<DT>::load((const uint8_t*)c.x + b * c.ld_x * (kBytes / 8) + chunk * kBytes);
+  float w[8 * W], bias[8];
+#pragma unroll
+  for (int i = 0; i < 8 * W; i += 4) {
+    const float4 f = reinterpret_cast<const float4*>(c.weight + chunk * 8 * W)[i / 4];
+    w[i] = f.x; w[i + 1] = f.y; w[i + 2] = f.z; w[i + 3] = f.w;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bias[e] = c.bias != nullptr ? c.bias[chunk * 8 + e] : 0.0f;
+  const bool kept = slot >= 0 && slot < c.n_states;
+  uint8_t* st = (uint8_t*)c.state + slot * c.ld_state * (kBytes / 8) + chunk * kBytes;
+  Eight<DT> old[kOld] = {};
+  if (kept && !fresh) {
+#pragma unroll
+    for (int j = 0; j < kOld; ++j) old[j] = Eight<DT>::load(st + j * chunks * kBytes);
+  }
+  float in[W][8], v[8];
+#pragma unroll
+  for (int j = 0; j < kOld; ++j) old[j].floats(in[j]);
+  now.floats(in[kOld]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float u = bias[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) u = fmaf(w[e * W + j], in[j][e], u);
+    v[e] = c.silu ? silu(u) : u;
+  }
+  Eight<DT>::of(v).stream((uint8_t*)c.y + b * c.ld_y * (kBytes / 8) + chunk * kBytes);
+  if (kept) {
+#pragma unroll
+    for (int j = 0; j < kOld; ++j) (j + 1 < kOld ? old[j + 1] : now).store(st + j * chunks * kBytes);
+  }
+}
+
+template <int DT, int W>
 void launch(const nvfp4_conv& c, hipStream_t s) {
   const int64_t each = c.tokens / c.batch, chunks = c.channels / 8;
-  const int run = c.tokens == c.batch ? 1 : 16;
-  const int64_t threads = (c.tokens + run - 1) / run * chunks;
+  const bool step = c.starts == nullptr && each == 1;
+  // Longer runs read fewer inputs twice, shorter ones keep more threads busy.  Measured, bf16, us with runs of 4, 8, 16, 32
+  // (C = 10240 unless said): 64 rows 8.3, 8.7, 11.9, 18.5; 512 rows 11.3, 11.0, 13.5, 19.9; 2048 rows 28.2, 24.7, 22.7,
+  // 26.3; 31500 rows of 1024 37.3, 33.0, 32.7, 33.3; 8192 rows 110, 88, 79, 81; 31500 rows 417, 332, 293, 269 (4.8 TB/s).
+  const int64_t places = c.tokens * chunks;
+  const int run = places >= (int64_t)1 << 25 ? 32 : places >= 1 << 21 ? 16 : places >= 1 << 19 ? 8 : 4;
+  const int64_t threads = step ? places : (c.tokens + run - 1) / run * chunks;
   const unsigned grid = (unsigned)((threads + kElemThreads - 1) / kElemThreads);
-  if (c.width == 2) causal_conv_kernel<DT, 2><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
-  else if (c.width == 3) causal_conv_kernel<DT, 3><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
-  else causal_conv_kernel<DT, 4><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
+  if (step) causal_conv_step_kernel<DT, W><<<grid, kElemThreads, 0, s>>>(c);
+  else causal_conv_kernel<DT, W><<<grid, kElemThreads, 0, s>>>(c, each, run, threads);
+}
+
+template <int DT>
+void launch_width(const nvfp4_conv& c, hipStream_t s) {
+  if (c.width == 2) launch<DT, 2>(c, s);
+  else if (c.width == 3) launch<DT, 3>(c, s);
+  else launch<DT, 4>(c, s);
 }
 
 }  // namespace
 
 hipError_t launch_causal_conv(const nvfp4_conv& c, int dtype, hipStream_t s) {
-  if (dtype == NVFP4_DTYPE_BF16) launch<NVFP4_DTYPE_BF16>(c, s);
-  else launch<NVFP4_DTYPE_F32>(c, s);
+  if (dtype == NVFP4_DTYPE_BF16) launch_width<NVFP4_DTYPE_BF16>(c, s);
+  else launch_width<NVFP4_DTYPE_F32>(c, s);
   return hipGetLastError();
 }
 

@@ -195,7 +195,7 @@ int nvfp4_qk_norm_rope(const nvfp4_head_rows* q, const nvfp4_head_rows* k, int d
     if ((st = check_rope(rope, tokens, head_dim)) != NVFP4_OK) return st;
     a.rope = *rope;
   }
-  if (norm && (!(eps > 0.0f) || !isfinite(eps) || !isfinite(weight_offset))) return NVFP4_ERR_VALUE;
+  if (norm && (!(eps >= 0x1p-126f) || !isfinite(eps) || !isfinite(weight_offset))) return NVFP4_ERR_VALUE;
   if (tokens == 0) return NVFP4_OK;
   a.dtype = dtype;
   a.head_dim = head_dim;

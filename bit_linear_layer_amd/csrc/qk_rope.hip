@@ -3,16 +3,19 @@
 //     (z_i, z_j) -> (z_i cos - z_j sin, z_j cos + z_i sin) for the pairs (i, j),
 // each result rounded once.  Bound: HBM (every element read and written once).
 //
-// A workgroup takes one token and a share of its heads.  A head's elements lie
-// in head_dim / 8 neighbouring lanes, 16 bytes (bf16) each: the sum of squares
-// stays in those lanes, and the partner of a pair i, i + rotary_dim / 2 is
-// the same element of the lane rotary_dim / 16 away.  The token's sines and
-// cosines (at most 128 pairs) are computed once per workgroup, while the rows' loads
-// are in flight: angle / 2 pi in float64, its distance to the nearest integer,
-// and sincospi of that in float32 -- a float32 product of a far position would be
-// off by whole turns.
+// A workgroup takes a few tokens, all of their heads or a share of them.  A head's
+// elements lie in head_dim / 8 neighbouring lanes, 16 bytes (bf16) each: the sum of
+// squares stays in those lanes, and the partner of a pair i, i + rotary_dim / 2 is
+// the same element of the lane rotary_dim / 16 away.  The tokens' sines and
+// cosines are computed first, one a thread, while the first rows' loads are in
+// flight: angle / 2 pi in float64, its distance to the nearest integer, and
+// sincospi of that in float32 -- a float32 product of a far position would be off by
+// whole turns.  They are kept in LDS for each element, the sine with the sign of
+// its place in the pair, so that a result is z c + partner s without a choice.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "device_util.h"
 #include "e4m3.h"
@@ -24,6 +27,7 @@ namespace nvfp4 {
 namespace {
 
 using namespace dev;
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 template <int DT>
 __device__ inline void store8(uint8_t* p, const float v[8]) {
@@ -35,91 +39,143 @@ __device__ inline void store8(uint8_t* p, const float v[8]) {
   }
 }
 
-// Rows (token, head) of queries and keys in one line: heads 0 .. hq - 1 are
-// queries, the rest keys.  share: head slots of one workgroup.
-template <int DT, int D>
-__global__ __launch_bounds__(kElemThreads) void qk_norm_rope_kernel(const RopeArgs a, int share) {
-  constexpr int kLanes = D / 8, kSlots = kElemThreads / kLanes, kSize = DT == NVFP4_DTYPE_BF16 ? 2 : 4;
-  __shared__ float cs[D / 2], sn[D / 2];
-  const int64_t t = blockIdx.x;
-  const int part = threadIdx.x & (kLanes - 1), slot = threadIdx.x / kLanes;
-  const int heads = a.rows[0].heads + a.rows[1].heads;
-  const int h_end = min(heads, (int)(blockIdx.y + 1) * share);
-  const int half = a.rope.rotary_dim / 2;
-
-  int h = blockIdx.y * share + slot;
-  float v[8];
-  auto load = [&]() {
-    const bool key = h >= a.rows[0].heads;
-    const nvfp4_head_rows& r = a.rows[key];
-    load8<DT>((const uint8_t*)r.x + (t * r.ld_x + (int64_t)(h - (key ? a.rows[0].heads : 0)) * r.head_x + part * 8) * kSize, v);
+// The sum over the L lanes of a head, in all of them.
+template <int L>
+__device__ inline float head_sum(float v) {
+  auto add = [&](auto ctrl) {
+    v += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), decltype(ctrl)::value, 0xF, 0xF, true));
   };
-  if (h < h_end) load();
-  if ((int)threadIdx.x < half) {
-    const int i = threadIdx.x;
+  add(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  add(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  add(std::integral_constant<int, 0x141>{});  // 7 - lane of 8: the other four
+  if constexpr (L >= 16) add(std::integral_constant<int, 0x140>{});  // 15 - lane of 16: the other eight
+  if constexpr (L >= 32) v += __shfl_xor(v, 16);
+  return v;
+}
+
+constexpr int kTable = 1024;  // entries of the sines' and of the cosines' table: tokens * rotary_dim
+
+// Rows are (token, head), queries' heads first, then keys'.  A workgroup has `tokens`
+// tokens and of their rows `passes` times as many as it holds at once.
+template <int DT, int D>
+__global__ __launch_bounds__(kElemThreads) void qk_norm_rope_kernel(const RopeArgs a, int tokens, int passes) {
+  constexpr int kLanes = D / 8, kSlots = kElemThreads / kLanes, kSize = DT == NVFP4_DTYPE_BF16 ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) float cs[kTable], sn[kTable], weights[2][D];
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  const int part = threadIdx.x & (kLanes - 1), slot = threadIdx.x / kLanes;
+  const int hq = a.rows[0].heads, heads = hq + a.rows[1].heads;
+  const int n = (int)min((int64_t)tokens, a.tokens - t0) * heads;  // rows of these tokens
+  const int dim = a.rope.rotary_dim, half = dim / 2;
+
+  float v[8], next[8];
+  struct Row {
+    int token, head;
+    bool key, there;
+  };
+  auto row_of = [&](int pass) {
+    const int row = pass * kSlots + slot;
+    Row r;
+    r.there = row < n;
+    r.token = row / heads;
+    const int h = row - r.token * heads;
+    r.key = h >= hq;
+    r.head = r.key ? h - hq : h;
+    return r;
+  };
+  auto load = [&](const Row& r) {
+    const uint8_t* x = (const uint8_t*)(r.key ? a.rows[1].x : a.rows[0].x);
+    const int64_t ld = r.key ? a.rows[1].ld_x : a.rows[0].ld_x, hd = r.key ? a.rows[1].head_x : a.rows[0].head_x;
+    if (r.there) load8<DT>(x + ((t0 + r.token) * ld + r.head * hd + part * 8) * kSize, next);
+  };
+  const int first = blockIdx.y * passes, last = min(first + passes, (n + kSlots - 1) / kSlots);
+  Row row = row_of(first);
+  load(row);
+  const bool norm_q = a.rows[0].weight != nullptr, norm_k = a.rows[1].weight != nullptr;
+  for (int i = threadIdx.x; i < D; i += kElemThreads) {
+    if (norm_q) weights[0][i] = a.rows[0].weight[i] + a.weight_offset;
+    if (norm_k) weights[1][i] = a.rows[1].weight[i] + a.weight_offset;
+  }
+  for (int e = threadIdx.x; e < tokens * half; e += kElemThreads) {
+    const int k = e / half, i = e - k * half;
+    const int64_t t = min(t0 + k, a.tokens - 1);
     const int axis = a.rope.axis != nullptr ? min((int)a.rope.axis[i], a.rope.axes - 1) : 0;
     const double turn = (double)a.rope.positions[axis * a.rope.ld_positions + t] * (double)a.rope.inv_freq[i] * 0.15915494309189533577;
     float sine, cosine;
     sincospif(2.0f * (float)(turn - rint(turn)), &sine, &cosine);
-    cs[i] = cosine;
-    sn[i] = sine;
+    const int p = k * dim + (a.rope.interleaved ? 2 * i : i), q = a.rope.interleaved ? p + 1 : p + half;
+    cs[p] = cs[q] = cosine;
+    sn[p] = -sine;
+    sn[q] = sine;
   }
   __syncthreads();
-  for (; h < h_end; h += kSlots) {
-    const bool key = h >= a.rows[0].heads;
-    const nvfp4_head_rows& r = a.rows[key];
-    if (r.weight != nullptr) {
+  const bool turned = part * 8 < dim;
+  const int partner = (threadIdx.x & (63 & ~(kLanes - 1))) + (!turned ? part : part * 8 < half ? part + half / 8 : part - half / 8);
+  for (int pass = first; pass < last; ++pass) {
+    const Row now = row;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = next[e];
+    if (pass + 1 < last) {
+      row = row_of(pass + 1);
+      load(row);
+    }
+    if (now.key ? norm_k : norm_q) {
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+      // within one ulp; the sum is at least eps, a normal number
+      const float f = __builtin_amdgcn_rsqf(head_sum<kLanes>(sum) * (1.0f / D) + a.eps);
+      const floatx4* w = reinterpret_cast<const floatx4*>(&weights[now.key][part * 8]);
 #pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-      const float f = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * f * (r.weight[part * 8 + e] + a.weight_offset);
+      for (int e = 0; e < 8; ++e) v[e] *= f * w[e / 4][e % 4];
     }
-    if (a.rope.interleaved) {
-      if (part * 8 < 2 * half) {
+    if (dim > 0) {
+      const floatx4* c = reinterpret_cast<const floatx4*>(&cs[turned ? now.token * dim + part * 8 : 0]);
+      const floatx4* s = reinterpret_cast<const floatx4*>(&sn[turned ? now.token * dim + part * 8 : 0]);
+      float other[8];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float c = cs[part * 4 + e / 2], s = sn[part * 4 + e / 2], x = v[e], y = v[e + 1];
-          v[e] = x * c - y * s;
-          v[e + 1] = y * c + x * s;
-        }
-      }
-    } else if (half > 0) {
-      const bool first = part * 8 < half, second = !first && part * 8 < 2 * half;
-      const int from = first ? part + half / 8 : second ? part - half / 8 : part;
-      const int at = first ? part * 8 : second ? part * 8 - half : 0;
+      for (int e = 0; e < 8; ++e) other[e] = a.rope.interleaved ? v[e ^ 1] : __shfl(v[e], partner);
+      if (turned) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float other = __shfl(v[e], (threadIdx.x & (63 & ~(kLanes - 1))) + from);
-        const float c = cs[at + e], s = first ? -sn[at + e] : sn[at + e];
-        if (first || second) v[e] = v[e] * c + other * s;
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], c[e / 4][e % 4], other[e] * s[e / 4][e % 4]);
       }
     }
-    store8<DT>((uint8_t*)r.out + (t * r.ld_out + (int64_t)(h - (key ? a.rows[0].heads : 0)) * r.head_out + part * 8) * kSize, v);
-    const int keep = h;
-    h += kSlots;
-    if (h < h_end) load();
-    h = keep;
+    if (now.there) {
+      uint8_t* out = (uint8_t*)(now.key ? a.rows[1].out : a.rows[0].out);
+      const int64_t ld = now.key ? a.rows[1].ld_out : a.rows[0].ld_out, hd = now.key ? a.rows[1].head_out : a.rows[0].head_out;
+      store8<DT>(out + ((t0 + now.token) * ld + now.head * hd + part * 8) * kSize, v);
+    }
   }
 }
 
-template <int DT>
+template <int DT, int D>
 void launch(const RopeArgs& a, hipStream_t s) {
-  const int heads = a.rows[0].heads + a.rows[1].heads;
-  const dim3 grid((unsigned)a.tokens, 1);
-  if (a.head_dim == 64) qk_norm_rope_kernel<DT, 64><<<grid, kElemThreads, 0, s>>>(a, heads);
-  else if (a.head_dim == 128) qk_norm_rope_kernel<DT, 128><<<grid, kElemThreads, 0, s>>>(a, heads);
-  else qk_norm_rope_kernel<DT, 256><<<grid, kElemThreads, 0, s>>>(a, heads);
+  constexpr int kSlots = kElemThreads / (D / 8);
+  const int heads = a.rows[0].heads + a.rows[1].heads, dim = a.rope.rotary_dim;
+  // Passes of a workgroup: few calls' worth of rows keep all CUs busy one by one; many share the tables' work and the
+  // start.  Measured, us, one token and one pass | 1, 2, 4, 8 tokens a workgroup: bf16, 32 + 8 heads of 128, 256 tokens 4.5 |
+  // 5.4, 7.1, 10.9; 2048 tokens 14.5 | 12.7, 11.9, 14.1; 16384 tokens 118 | 89, 76, 73.5, 73.4 (4.6 TB/s); 24 + 4 of 256 153 |
+  // 110, 95.5, 103, 121; 16 + 4 of 64 31 | 32, 25, 20, 19; float32, 8192 tokens of 32 + 8 of 128 83 | 68, 71, 78.
+  const int64_t total = a.tokens * heads / kSlots;
+  const int want = total < 1024 ? 1 : DT == NVFP4_DTYPE_F32 ? 3 : total < 16384 ? 5 : 8;
+  const int tokens = max(1, min(want * kSlots / heads, dim > 0 ? kTable / dim : 8));
+  const int all = (tokens * heads + kSlots - 1) / kSlots;
+  const int passes = min(all, max(want, 1 + (all - 1) / 60000));  // the grid's second size stays below 2^16
+  const dim3 grid((unsigned)((a.tokens + tokens - 1) / tokens), (unsigned)((all + passes - 1) / passes));
+  qk_norm_rope_kernel<DT, D><<<grid, kElemThreads, 0, s>>>(a, tokens, passes);
+}
+
+template <int DT>
+void launch_dim(const RopeArgs& a, hipStream_t s) {
+  if (a.head_dim == 64) launch<DT, 64>(a, s);
+  else if (a.head_dim == 128) launch<DT, 128>(a, s);
+  else launch<DT, 256>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t s) {
-  if (a.dtype == NVFP4_DTYPE_BF16) launch<NVFP4_DTYPE_BF16>(a, s);
-  else launch<NVFP4_DTYPE_F32>(a, s);
+  if (a.dtype == NVFP4_DTYPE_BF16) launch_dim<NVFP4_DTYPE_BF16>(a, s);
+  else launch_dim<NVFP4_DTYPE_F32>(a, s);
   return hipGetLastError();
 }
 

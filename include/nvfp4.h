@@ -687,7 +687,7 @@ typedef struct {
  *   token lie together (head >= head_dim, ld >= (heads - 1) * head + head_dim)
  *   or the tokens of a head do (ld >= head_dim, head >= (tokens - 1) * ld +
  *   head_dim); a stride that is not used is not looked at.
- *   eps       finite and > 0 (read where there is a weight).
+ *   eps       finite and >= 2^-126 (read where there is a weight).
  * One launch.  tokens = 0 is a valid call that does nothing.
  */
 int nvfp4_qk_norm_rope(const nvfp4_head_rows* q, const nvfp4_head_rows* k, int dtype, int64_t tokens, int head_dim,

@@ -135,7 +135,7 @@ def test_axis_values_beyond_the_axes_and_bad_plans():
     rng = np.random.default_rng(4)
     x = torch.from_numpy(rng.standard_normal((9, 2 * 64))).float().to(DEV)
     rope, freq, _ = rope_of(64, 1, False, rng)
-    rope.axis = torch.arange(32, device=DEV).to(torch.uint8) * 8
+    rope = nv.Rope(rope.inv_freq, torch.arange(32, device=DEV).to(torch.uint8) * 8)
     pos = torch.from_numpy(rng.integers(0, 5000, (2, 9))).to(DEV)
     got, _ = nv.qk_norm_rope(x, x, 64, pos, rope)
     close(got, x, 64, positions=pos.cpu().numpy(), inv_freq=freq, axis=rope.axis.cpu().numpy())
@@ -150,8 +150,11 @@ def test_axis_values_beyond_the_axes_and_bad_plans():
     refused(positions=pos.cpu())
     refused(positions=None)
     refused(rope=nv.Rope(rope.inv_freq))
-    refused(rope=nv.Rope(rope.inv_freq.double(), rope.axis))
-    refused(rope=nv.Rope(rope.inv_freq, rope.axis[:31]))
+    for args in ((rope.inv_freq.double(), rope.axis), (rope.inv_freq, rope.axis[:31]), (rope.inv_freq, rope.axis.int()),
+                 (rope.inv_freq, rope.axis.cpu()), (rope.inv_freq[::2], None), (rope.inv_freq.view(2, 16), None)):
+        with pytest.raises(nv.NVFP4Error):
+            nv.Rope(*args)
+    refused(rope=nv.Rope(rope.inv_freq.cpu(), rope.axis.cpu()))
     refused(rope=nv.Rope(rope.inv_freq[:31], rope.axis[:31]))
     refused(q_weight=torch.ones(63, device=DEV))
     refused(q_weight=torch.ones(64, device=DEV).double())

@@ -2,8 +2,6 @@
 convolution and the gated delta rule's next tokens, at the C ABI and in the
 binding (CPU only: every call here is refused before any HIP call, or has
 nothing to do)."""
-import ctypes
-
 import pytest
 import torch
 
@@ -13,8 +11,9 @@ FAKE = 1 << 20
 BIG = 1 << 62
 
 
-def ref(x):
-    return None if x is None else ctypes.byref(x)
+def pack(f, *values):
+    """The struct's bytes, for what its integers hold; a NULL pointer is None."""
+    return f(*[0 if v is None else v for v in values])
 
 
 # ------------------------------------------------------------ 8-bit layers
@@ -22,19 +21,19 @@ def ref(x):
 def fp8(**kw):
     a = dict(codes=FAKE, scales=FAKE, rows=5, cols=272, ldc=272, lds=3, block=1)
     a.update(kw)
-    return nv._FP8(a["codes"], a["scales"], a["rows"], a["cols"], a["ldc"], a["lds"], a["block"])
+    return pack(nv._FP8, a["codes"], a["scales"], a["rows"], a["cols"], a["ldc"], a["lds"], a["block"])
 
 
 def quantize(q=None, x=FAKE, dt=0, ld=272, flags=0):
-    return nv.load().nvfp4_fp8_quantize(x, dt, ld, ref(q or fp8()), flags, None)
+    return nv.load().nvfp4_fp8_quantize(x, dt, ld, q or fp8(), flags, None)
 
 
 def gemm(a=None, w=None, out=FAKE, dt=0, ld=130, ws=FAKE, wsb=1 << 30):
-    return nv.load().nvfp4_fp8_gemm(ref(a or fp8()), ref(w or fp8(rows=130, block=128)), out, dt, ld, ws, wsb, None)
+    return nv.load().nvfp4_fp8_gemm(a or fp8(), w or fp8(rows=130, block=128), out, dt, ld, ws, wsb, None)
 
 
 def linear(w=None, x=FAKE, dt=0, rows=5, ld=272, out=FAKE, odt=0, ldo=130, ws=FAKE, wsb=1 << 30):
-    return nv.load().nvfp4_fp8_linear(x, dt, rows, ld, ref(w or fp8(rows=130, block=128)), out, odt, ldo, ws, wsb, None)
+    return nv.load().nvfp4_fp8_linear(x, dt, rows, ld, w or fp8(rows=130, block=128), out, odt, ldo, ws, wsb, None)
 
 
 MATRICES = [
@@ -101,23 +100,23 @@ def test_linear_workspace():
 def rows_of(**kw):
     a = dict(x=FAKE, ld=512, head=128, out=FAKE, ldo=512, heado=128, w=FAKE, heads=4)
     a.update(kw)
-    return nv._HeadRows(a["x"], a["ld"], a["head"], a["out"], a["ldo"], a["heado"], a["w"], a["heads"])
+    return pack(nv._HEAD_ROWS, a["x"], a["ld"], a["head"], a["out"], a["ldo"], a["heado"], a["w"], a["heads"])
 
 
 def turn(**kw):
     a = dict(pos=FAKE, ld=10, freq=FAKE, axis=FAKE, axes=3, dim=64, inter=0)
     a.update(kw)
-    return nv._Rope(a["pos"], a["ld"], a["freq"], a["axis"], a["axes"], a["dim"], a["inter"])
+    return pack(nv._ROPE, a["pos"], a["ld"], a["freq"], a["axis"], a["axes"], a["dim"], a["inter"])
 
 
 def rope(q=None, k=None, dt=0, tokens=10, dim=128, eps=1e-6, offset=0.0, r=None, none=False):
     q = None if none else q or rows_of()
-    return nv.load().nvfp4_qk_norm_rope(ref(q), ref(k), dt, tokens, dim, eps, offset, ref(r), None)
+    return nv.load().nvfp4_qk_norm_rope(q, k, dt, tokens, dim, eps, offset, r, None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(none=True), -1), (dict(dt=5), -3), (dict(dim=96), -2), (dict(tokens=-1), -2), (dict(tokens=1 << 24), -11),
-    (dict(eps=0.0), -12), (dict(eps=-1.0), -12), (dict(eps=float("nan")), -12), (dict(eps=float("inf")), -12),
+    (dict(eps=0.0), -12), (dict(eps=-1.0), -12), (dict(eps=1e-39), -12), (dict(eps=float("nan")), -12), (dict(eps=float("inf")), -12),
     (dict(offset=float("nan")), -12),
     (dict(tokens=0, q=rows_of(x=None, out=None), r=turn(pos=None, freq=None)), 0),
 ])
@@ -149,9 +148,9 @@ def conv(dt=0, none=False, **kw):
     a = dict(x=FAKE, ldx=64, y=2 * FAKE, ldy=64, w=FAKE, bias=FAKE, tokens=12, channels=64, batch=3, width=4, silu=1, starts=FAKE,
              state=FAKE, n=5, lds=192, slots=FAKE, fresh=FAKE)
     a.update(kw)
-    c = nv._Conv(a["x"], a["ldx"], a["y"], a["ldy"], a["w"], a["bias"], a["tokens"], a["channels"], a["batch"], a["width"],
+    c = pack(nv._CONV, a["x"], a["ldx"], a["y"], a["ldy"], a["w"], a["bias"], a["tokens"], a["channels"], a["batch"], a["width"],
                  a["silu"], a["starts"], a["state"], a["n"], a["lds"], a["slots"], a["fresh"])
-    return nv.load().nvfp4_causal_conv(None if none else ctypes.byref(c), dt, None)
+    return nv.load().nvfp4_causal_conv(None if none else c, dt, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -173,8 +172,8 @@ def test_bad_convolution(kw, status):
 def step(dt=0, odt=0, batch=3, q_len=2, hk=2, hv=4, states=FAKE, n=5, lds=4 * 16384, slots=FAKE, o=FAKE, ldo=512, none=False, **kw):
     a = dict(q=FAKE, ldq=256, k=FAKE, ldk=256, v=FAKE, ldv=512, beta=FAKE, ldb=4, g=FAKE, ldg=4)
     a.update(kw)
-    i = nv._GdnInputs(a["q"], a["ldq"], a["k"], a["ldk"], a["v"], a["ldv"], a["beta"], a["ldb"], a["g"], a["ldg"])
-    return nv.load().nvfp4_gdn_step(None if none else ctypes.byref(i), dt, batch, q_len, hk, hv, 1, states, n, lds, slots, None, o,
+    i = pack(nv._GDN_INPUTS, a["q"], a["ldq"], a["k"], a["ldk"], a["v"], a["ldv"], a["beta"], a["ldb"], a["g"], a["ldg"])
+    return nv.load().nvfp4_gdn_step(None if none else i, dt, batch, q_len, hk, hv, 1, states, n, lds, slots, None, o,
                                     odt, ldo, None)
 
 
