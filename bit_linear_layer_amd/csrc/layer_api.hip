@@ -125,7 +125,7 @@ int nvfp4_fp8_quantize(const void* x, int x_dtype, int64_t ld_x, const nvfp4_fp8
   const bool pow2 = flags == NVFP4_FP8_SCALE_POW2;
   if (q->block_rows == 1)
     return status_from_hip(launch_fp8_quantize_rows(x, x_dtype, q->rows, q->cols, ld_x, m, pow2, (hipStream_t)stream));
-  if ((q->rows + 127) / 128 * pieces_of(q->cols) >= kGridLimit) return NVFP4_ERR_RANGE;
+  if ((q->rows + 127) / 128 * pieces_of(q->cols) >= kGridLimit / 4) return NVFP4_ERR_RANGE;  // workgroups of 1024 threads
   return status_from_hip(launch_fp8_quantize_blocks(x, x_dtype, q->rows, q->cols, ld_x, m, pow2, (hipStream_t)stream));
 }
 
