@@ -112,6 +112,7 @@ struct Ring {
   static constexpr int CW = TN / 64, CX = TM / 64;           // copies of every wave
   static constexpr int XR = TM / 8 % 8;                      // waves that copy one more group of activation rows
   static constexpr int kBase = CW + CX;
+  static constexpr int kHint = TM == 16 ? 2 : 0;
   static constexpr int kStage = kW + kX + NS * 256;
   static_assert(WN * WM == 8 && TN % 64 == 0 && 128 % TN == 0 && XR + NS <= 8 && D * kStage <= 160 * 1024, "the copies' shares");
   static_assert((D - 2) * (kBase + 1) < 64, "vmcnt's range");
@@ -140,56 +141,48 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
   const int q = lane >> 3, piece = ((lane & 7) ^ q) * 16;
   const int ldw = (int)p.w.ld_codes, lda = (int)p.a.ld_codes;
   constexpr int kNowhere = (int)0x80000000;
-  struct Cursor {
-    int tile, block;
-    int64_t step;
-    i32x4 rw, rx;
-    const float* sa;
-  } at;
-  auto enter = [&](int tile) __attribute__((always_inline)) {
-    const int n0 = tile / tiles_m * T::TN, m0 = tile % tiles_m * T::TM;
-    at.rw = buffer_rsrc(p.w.codes + (int64_t)n0 * ldw, (uint32_t)(min(T::TN, p.N - n0) * ldw));
-    at.rx = buffer_rsrc(p.a.codes + (int64_t)m0 * lda, (uint32_t)(min(T::TM, p.M - m0) * lda));
-    at.sa = p.a.scales + (int64_t)min(m0 + max(wave - (8 - T::NS), 0) * 64 + lane, p.M - 1) * p.a.scale_row;
+  int tile = (int)(mine.first / blocks), block = (int)(mine.first - (int64_t)tile * blocks);
+  const int steps = (int)(mine.last - mine.first);
+  // the copies' place in the line, D - 1 steps ahead of the products'
+  int to_tile = tile, to_block = block, to_step = 0;
+  i32x4 rw, rx;
+  const float* sa;
+  auto enter = [&]() __attribute__((always_inline)) {
+    const int tn = to_tile / tiles_m, n0 = tn * T::TN, m0 = (to_tile - tn * tiles_m) * T::TM;
+    rw = buffer_rsrc(p.w.codes + (int64_t)n0 * ldw, (uint32_t)(min(T::TN, p.N - n0) * ldw));
+    rx = buffer_rsrc(p.a.codes + (int64_t)m0 * lda, (uint32_t)(min(T::TM, p.M - m0) * lda));
+    sa = p.a.scales + (int64_t)min(m0 + max(wave - (8 - T::NS), 0) * 64 + lane, p.M - 1) * p.a.scale_row;
   };
   auto copy = [&](uint8_t* stage) __attribute__((always_inline)) {
-    const int k = at.block * 128;
+    const int k = to_block * 128;
     const bool there = k + piece < p.K;
 #pragma unroll
     for (int c = 0; c < T::CW; ++c)
-      llvm_amdgcn_raw_buffer_load_lds(at.rw, (lds_u32_ptr)(stage + (wave * T::CW + c) * 1024), 16,
-                                      there ? ((wave * T::CW + c) * 8 + q) * ldw + piece : kNowhere, k, 0, 0);
+      llvm_amdgcn_raw_buffer_load_lds(rw, (lds_u32_ptr)(stage + (wave * T::CW + c) * 1024), 16,
+                                      there ? ((wave * T::CW + c) * 8 + q) * ldw + piece : kNowhere, k, 0, T::kHint);
 #pragma unroll
     for (int c = 0; c < T::CX; ++c)
-      llvm_amdgcn_raw_buffer_load_lds(at.rx, (lds_u32_ptr)(stage + T::kW + (wave * T::CX + c) * 1024), 16,
+      llvm_amdgcn_raw_buffer_load_lds(rx, (lds_u32_ptr)(stage + T::kW + (wave * T::CX + c) * 1024), 16,
                                       there ? ((wave * T::CX + c) * 8 + q) * lda + piece : kNowhere, k, 0, 0);
     if (wave < T::XR)
-      llvm_amdgcn_raw_buffer_load_lds(at.rx, (lds_u32_ptr)(stage + T::kW + (8 * T::CX + wave) * 1024), 16,
+      llvm_amdgcn_raw_buffer_load_lds(rx, (lds_u32_ptr)(stage + T::kW + (8 * T::CX + wave) * 1024), 16,
                                       there ? ((8 * T::CX + wave) * 8 + q) * lda + piece : kNowhere, k, 0, 0);
     if (wave >= 8 - T::NS)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(at.sa + (int64_t)at.block * p.a.scale_block),
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(sa + (int64_t)to_block * p.a.scale_block),
                                        (lds_u32_ptr)(stage + T::kW + T::kX + (wave - (8 - T::NS)) * 256), 4, 0, 0);
-  };
-  auto advance = [&]() __attribute__((always_inline)) {  // behind the last step the last one is copied again
-    if (at.step + 1 < mine.last) {
-      ++at.step;
-      if (++at.block == blocks) {
-        at.block = 0;
-        enter(++at.tile);
+    if (to_step + 1 < steps) {  // behind the last step the last one is copied again
+      ++to_step;
+      if (++to_block == blocks) {
+        to_block = 0;
+        ++to_tile;
+        enter();
       }
     }
   };
 
-  int tile = (int)(mine.first / blocks), block = (int)(mine.first - (int64_t)tile * blocks);
-  at.tile = tile;
-  at.block = block;
-  at.step = mine.first;
-  enter(tile);
+  enter();
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) {
-    copy(smem + d * T::kStage);
-    advance();
-  }
+  for (int d = 0; d < D - 1; ++d) copy(smem + d * T::kStage);
   floatx4 acc[FN][FM];
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -202,15 +195,21 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
   const bool vec = p.ld_out % 4 == 0 && (uintptr_t)p.out % (OUT == NVFP4_DTYPE_BF16 ? 8 : 16) == 0;
   int begun = block, stage = 0;  // begun: the tile's first block of this workgroup
   const bool extra = wave < T::XR || wave >= 8 - T::NS;
-  for (int64_t step = mine.first; step < mine.last; ++step) {
-    const int n0 = tile / tiles_m * T::TN, m0 = tile % tiles_m * T::TM;
-    const auto* sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)(n0 / 128) * p.w.scale_row);
-    const float s = sw[block * p.w.scale_block];
+  int n0, m0;
+  const __attribute__((address_space(4))) float* sw;
+  auto begin_tile = [&]() __attribute__((always_inline)) {
+    const int tn = tile / tiles_m;
+    n0 = tn * T::TN;
+    m0 = (tile - tn * tiles_m) * T::TM;
+    sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)(n0 / 128) * p.w.scale_row);
+  };
+  begin_tile();
+  float next_s = sw[block * p.w.scale_block];
+  for (int step = 0; step < steps; ++step) {
     if (extra) wait_vmem<(D - 2) * (T::kBase + 1)>();
     else wait_vmem<(D - 2) * T::kBase>();
     barrier_lds();
-    copy(smem + (stage == 0 ? D - 1 : stage - 1) * T::kStage);
-    advance();
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the barrier's lgkmcnt(0) again, seen by the compiler's own wait insertion
     const uint8_t* st = smem + stage * T::kStage;
     auto frag = [&](int row) __attribute__((always_inline)) {
       Frag f;
@@ -218,23 +217,35 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
       for (int h = 0; h < 2; ++h) f.p[h] = *reinterpret_cast<const u32x4*>(st + row * 128 + (((lg + 4 * h) ^ key) << 4));
       return f;
     };
-    Frag w[FN];
+    Frag w[FN], x[FM];
+    float sc[FM];
 #pragma unroll
     for (int i = 0; i < FN; ++i) w[i] = frag((wn * FN + i) * 16 + li);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const Frag x = frag(T::TN + (wm * FM + j) * 16 + li);
-      const float sc = *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + j) * 16 + li) * 4) * s;
+    for (int j = 0; j < FM; ++j) x[j] = frag(T::TN + (wm * FM + j) * 16 + li);
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const floatx4 t = block_product<EXACT>(w[i], x);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], sc, acc[i][j][r]);
-      }
-    }
+    for (int j = 0; j < FM; ++j) sc[j] = *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + j) * 16 + li) * 4);
+    __builtin_amdgcn_sched_barrier(0);
+    copy(smem + (stage == 0 ? D - 1 : stage - 1) * T::kStage);
+    __builtin_amdgcn_sched_barrier(0);
+    const float s = next_s;
     stage = stage == D - 1 ? 0 : stage + 1;
     ++block;
-    if (block == blocks || step + 1 == mine.last) {
+    const bool ends = block == blocks || step + 1 == steps;
+    floatx4 t[FN][FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) t[i][j] = block_product<EXACT>(w[i], x[j]);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      sc[j] *= s;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[i][j][r], sc[j], acc[i][j][r]);
+    }
+    if (ends) {
       if (block == blocks && begun == 0) {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
@@ -256,7 +267,9 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
       clear();
       begun = block = 0;
       ++tile;
+      if (step + 1 < steps) begin_tile();
     }
+    if (step + 1 < steps) next_s = sw[block * p.w.scale_block];
   }
   wait_vmem<0>();  // no copy may land after the workgroup's LDS is given away
 }
