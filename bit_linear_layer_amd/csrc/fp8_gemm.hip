@@ -145,17 +145,21 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
   const int steps = (int)(mine.last - mine.first);
   // the copies' place in the line, D - 1 steps ahead of the products'
   int to_tile = tile, to_block = block, to_step = 0;
-  i32x4 rw, rx;
+  i32x4 rw;
+  const uint8_t* xa;
+  uint32_t x_bytes;
   const float* sa;
   auto enter = [&]() __attribute__((always_inline)) {
     const int tn = to_tile / tiles_m, n0 = tn * T::TN, m0 = (to_tile - tn * tiles_m) * T::TM;
     rw = buffer_rsrc(p.w.codes + (int64_t)n0 * ldw, (uint32_t)(min(T::TN, p.N - n0) * ldw));
-    rx = buffer_rsrc(p.a.codes + (int64_t)m0 * lda, (uint32_t)(min(T::TM, p.M - m0) * lda));
+    xa = p.a.codes + (int64_t)m0 * lda;
+    x_bytes = (uint32_t)(min(T::TM, p.M - m0) * lda);
     sa = p.a.scales + (int64_t)min(m0 + max(wave - (8 - T::NS), 0) * 64 + lane, p.M - 1) * p.a.scale_row;
   };
   auto copy = [&](uint8_t* stage) __attribute__((always_inline)) {
     const int k = to_block * 128;
     const bool there = k + piece < p.K;
+    const i32x4 rx = buffer_rsrc(xa + to_block * p.a.code_block, x_bytes);
 #pragma unroll
     for (int c = 0; c < T::CW; ++c)
       llvm_amdgcn_raw_buffer_load_lds(rw, (lds_u32_ptr)(stage + (wave * T::CW + c) * 1024), 16,
@@ -163,10 +167,10 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
 #pragma unroll
     for (int c = 0; c < T::CX; ++c)
       llvm_amdgcn_raw_buffer_load_lds(rx, (lds_u32_ptr)(stage + T::kW + (wave * T::CX + c) * 1024), 16,
-                                      there ? ((wave * T::CX + c) * 8 + q) * lda + piece : kNowhere, k, 0, 0);
+                                      there ? ((wave * T::CX + c) * 8 + q) * lda + piece : kNowhere, 0, 0, 0);
     if (wave < T::XR)
       llvm_amdgcn_raw_buffer_load_lds(rx, (lds_u32_ptr)(stage + T::kW + (8 * T::CX + wave) * 1024), 16,
-                                      there ? ((8 * T::CX + wave) * 8 + q) * lda + piece : kNowhere, k, 0, 0);
+                                      there ? ((8 * T::CX + wave) * 8 + q) * lda + piece : kNowhere, 0, 0, 0);
     if (wave >= 8 - T::NS)
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(sa + (int64_t)to_block * p.a.scale_block),
                                        (lds_u32_ptr)(stage + T::kW + T::kX + (wave - (8 - T::NS)) * 256), 4, 0, 0);
@@ -226,17 +230,18 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
 #pragma unroll
     for (int j = 0; j < FM; ++j) sc[j] = *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + j) * 16 + li) * 4);
     __builtin_amdgcn_sched_barrier(0);
-    copy(smem + (stage == 0 ? D - 1 : stage - 1) * T::kStage);
-    __builtin_amdgcn_sched_barrier(0);
     const float s = next_s;
-    stage = stage == D - 1 ? 0 : stage + 1;
-    ++block;
-    const bool ends = block == blocks || step + 1 == steps;
     floatx4 t[FN][FM];
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
       for (int i = 0; i < FN; ++i) t[i][j] = block_product<EXACT>(w[i], x[j]);
+    __builtin_amdgcn_sched_barrier(0);
+    copy(smem + (stage == 0 ? D - 1 : stage - 1) * T::kStage);  // behind the products, which run on while a copy waits to go out
+    __builtin_amdgcn_sched_barrier(0);
+    stage = stage == D - 1 ? 0 : stage + 1;
+    ++block;
+    const bool ends = block == blocks || step + 1 == steps;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       sc[j] *= s;
@@ -352,7 +357,7 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
 
   // copies: lane l brings piece l % 8 of row l / 8 of a group of 8 rows
   const i32x4 rw = buffer_rsrc(p.w.codes + (int64_t)n0 * p.w.ld_codes, (uint32_t)(T::TN * p.w.ld_codes));
-  const i32x4 rx = buffer_rsrc(p.a.codes + (int64_t)m0 * p.a.ld_codes, (uint32_t)(T::TM * p.a.ld_codes));
+  const i32x4 rx = buffer_rsrc(p.a.codes + (int64_t)m0 * p.a.ld_codes, (uint32_t)(T::TM * p.a.ld_codes));  // code_block is 128
   const int q = lane >> 3;
   int vw[T::CW], vx[T::CX];
   int pw[2];                              // the piece, by the parity of the group of rows
@@ -567,7 +572,7 @@ size_t fp8_gemm_workspace(int64_t m) {
 }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
-  if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 224) {
+  if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 224 && g.a.code_block == 128) {
     return launch_pipe<8, 7, 2, 2>(g, 0, g.N, s);
   }
   switch (ring_tokens(g.M)) {

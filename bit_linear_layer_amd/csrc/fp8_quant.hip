@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kElemThreads) void fp8_quantize_rows_kernel(const u
       const Divider d(__uint_as_float(top), pow2);
       const uint2 w = any ? d.codes_any(v) : d.codes(v);
       if (there[u]) {
-        store_stream8(q.codes + rr[u] * q.ld_codes + bb[u] * 128 + part * 8, w.x, w.y);
+        store_stream8(q.codes + rr[u] * q.ld_codes + bb[u] * q.code_block + part * 8, w.x, w.y);
         if (part == 0) q.scales[rr[u] * q.scale_row + bb[u] * q.scale_block] = d.s;
       }
     }

@@ -9,12 +9,13 @@
 
 namespace nvfp4 {
 
-// E4M3 codes with a float32 scale per block: the scale of (row, block b) is at
-// scales[row * scale_row + b * scale_block], rows counted in block_rows.
+// E4M3 codes with a float32 scale per block: the 128 codes of (row, block b)
+// begin at codes[row * ld_codes + b * code_block], its scale is at
+// scales[row * scale_row + b * scale_block] (rows counted in block_rows).
 struct Fp8Mat {
   uint8_t* codes;
   float* scales;
-  int64_t ld_codes, scale_row, scale_block;
+  int64_t ld_codes, code_block, scale_row, scale_block;
 };
 
 hipError_t launch_fp8_quantize_rows(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, const Fp8Mat& q,
