@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_util.h"
 #include "layer_ops.h"
 
@@ -93,7 +95,7 @@ __device__ inline void store4(void* out, int64_t at, const floatx4& v, int left,
 // Products with few tokens, or of too few tiles to fill the chip: bound by the
 // weight's bytes up to about 200 tokens.  256 workgroups of 8 waves, one per CU, share the
 // line of all (tile, block of 128) steps evenly, tile by tile; a workgroup's copies
-// run D - 1 steps ahead of its products, across the ends of tiles, so that the
+// run D steps ahead of its products, across the ends of tiles, so that the
 // stream from memory never drains.  A tile whose steps lie in one workgroup is stored; of one that a
 // cut divides each workgroup leaves its float32 sums in the workspace, and
 // fp8_join_kernel adds them in the order of the blocks: the result depends on the sizes only.
@@ -102,8 +104,8 @@ __device__ inline void store4(void* out, int64_t at, const floatx4& v, int left,
 // bytes each, 16-byte pieces XOR-swizzled by the row so that fragment reads are free of bank
 // conflicts) and the activations' scales, all by LDS DMA.  Rows behind the last
 // and pieces behind K lie behind the descriptors' ranges: such lanes write zeros.
-// One barrier per step certifies its stage and frees the one before, into which the
-// copies D - 1 steps ahead then go.
+// One barrier per step certifies the next step's stage and frees its own, whose fragments
+// are in registers by then: the copies D steps ahead go there.
 template <int FN, int FM, int WN, int WM, int D>
 struct Ring {
   static constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
@@ -115,7 +117,7 @@ struct Ring {
   static constexpr int kHint = TM == 16 ? 2 : 0;
   static constexpr int kStage = kW + kX + NS * 256;
   static_assert(WN * WM == 8 && TN % 64 == 0 && 128 % TN == 0 && XR + NS <= 8 && D * kStage <= 160 * 1024, "the copies' shares");
-  static_assert((D - 2) * (kBase + 1) < 64, "vmcnt's range");
+  static_assert((D - 1) * (kBase + 1) < 64, "vmcnt's range");
 };
 
 constexpr int kRingGroups = 256;
@@ -143,7 +145,7 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
   constexpr int kNowhere = (int)0x80000000;
   int tile = (int)(mine.first / blocks), block = (int)(mine.first - (int64_t)tile * blocks);
   const int steps = (int)(mine.last - mine.first);
-  // the copies' place in the line, D - 1 steps ahead of the products'
+  // the copies' place in the line, D steps ahead of the products'
   int to_tile = tile, to_block = block, to_step = 0;
   i32x4 rw;
   const uint8_t* xa;
@@ -186,7 +188,7 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
 
   enter();
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) copy(smem + d * T::kStage);
+  for (int d = 0; d < D; ++d) copy(smem + d * T::kStage);
   floatx4 acc[FN][FM];
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -199,6 +201,12 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
   const bool vec = p.ld_out % 4 == 0 && (uintptr_t)p.out % (OUT == NVFP4_DTYPE_BF16 ? 8 : 16) == 0;
   int begun = block, stage = 0;  // begun: the tile's first block of this workgroup
   const bool extra = wave < T::XR || wave >= 8 - T::NS;
+  auto landed = [&](auto sets) __attribute__((always_inline)) {  // all but the last `sets` steps' copies, in every wave
+    if (extra) wait_vmem<decltype(sets)::value * (T::kBase + 1)>();
+    else wait_vmem<decltype(sets)::value * T::kBase>();
+    barrier_lds();
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the barrier's lgkmcnt(0) again, seen by the compiler's own wait insertion
+  };
   int n0, m0;
   const __attribute__((address_space(4))) float* sw;
   auto begin_tile = [&]() __attribute__((always_inline)) {
@@ -209,47 +217,63 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
   };
   begin_tile();
   float next_s = sw[block * p.w.scale_block];
+  auto frag = [&](const uint8_t* st, int row) __attribute__((always_inline)) {
+    Frag f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) f.p[h] = *reinterpret_cast<const u32x4*>(st + row * 128 + (((lg + 4 * h) ^ key) << 4));
+    return f;
+  };
+  auto scale_at = [&](const uint8_t* st, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + j) * 16 + li) * 4);
+  };
+  Frag w[FN], x[FM];
+  float sc[FM];
+  landed(std::integral_constant<int, D - 1>{});
+#pragma unroll
+  for (int i = 0; i < FN; ++i) w[i] = frag(smem, (wn * FN + i) * 16 + li);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) x[j] = frag(smem, T::TN + (wm * FM + j) * 16 + li);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) sc[j] = scale_at(smem, j);
+  // A step's fragments are in registers when it begins; the next step's are read beside its products, each
+  // activation fragment into the place of the one just used.
   for (int step = 0; step < steps; ++step) {
-    if (extra) wait_vmem<(D - 2) * (T::kBase + 1)>();
-    else wait_vmem<(D - 2) * T::kBase>();
-    barrier_lds();
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the barrier's lgkmcnt(0) again, seen by the compiler's own wait insertion
-    const uint8_t* st = smem + stage * T::kStage;
-    auto frag = [&](int row) __attribute__((always_inline)) {
-      Frag f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) f.p[h] = *reinterpret_cast<const u32x4*>(st + row * 128 + (((lg + 4 * h) ^ key) << 4));
-      return f;
-    };
-    Frag w[FN], x[FM];
-    float sc[FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i) w[i] = frag((wn * FN + i) * 16 + li);
-#pragma unroll
-    for (int j = 0; j < FM; ++j) x[j] = frag(T::TN + (wm * FM + j) * 16 + li);
-#pragma unroll
-    for (int j = 0; j < FM; ++j) sc[j] = *reinterpret_cast<const float*>(st + T::kW + T::kX + ((wm * FM + j) * 16 + li) * 4);
-    __builtin_amdgcn_sched_barrier(0);
+    landed(std::integral_constant<int, D - 2>{});
     const float s = next_s;
-    floatx4 t[FN][FM];
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-      for (int i = 0; i < FN; ++i) t[i][j] = block_product<EXACT>(w[i], x[j]);
-    __builtin_amdgcn_sched_barrier(0);
-    copy(smem + (stage == 0 ? D - 1 : stage - 1) * T::kStage);  // behind the products, which run on while a copy waits to go out
-    __builtin_amdgcn_sched_barrier(0);
-    stage = stage == D - 1 ? 0 : stage + 1;
-    ++block;
-    const bool ends = block == blocks || step + 1 == steps;
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      sc[j] *= s;
+    const int next_stage = stage == D - 1 ? 0 : stage + 1;
+    const uint8_t* nst = smem + next_stage * T::kStage;
+    Frag next_w[FN];
+    float now_sc[FM];
+    floatx4 t[2][FN];
+    auto add = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[i][j][r], sc[j], acc[i][j][r]);
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[j & 1][i][r], now_sc[j], acc[i][j][r]);
+    };
+#pragma unroll
+    for (int j = 0; j < FM; ++j) now_sc[j] = sc[j] * s;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) t[j & 1][i] = block_product<EXACT>(w[i], x[j]);
+      if (j == 0) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) next_w[i] = frag(nst, (wn * FN + i) * 16 + li);
+      }
+      x[j] = frag(nst, T::TN + (wm * FM + j) * 16 + li);
+      sc[j] = scale_at(nst, j);
+      if (j == 0) copy(smem + stage * T::kStage);  // every wave has this step's fragments
+      if (j > 0) add(j - 1);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    add(FM - 1);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) w[i] = next_w[i];
+    stage = next_stage;
+    ++block;
+    const bool ends = block == blocks || step + 1 == steps;
     if (ends) {
       if (block == blocks && begun == 0) {
 #pragma unroll
@@ -535,7 +559,7 @@ hipError_t launch_pipe(const Fp8GemmArgs& g, int n_lo, int n_hi, hipStream_t s) 
 template <int FN, int FM, int WN, int WM, int D, bool EXACT, int OUT>
 hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
   using T = Ring<FN, FM, WN, WM, D>;
-  static_assert(T::TN * T::TM <= 128 * 128, "a partial tile's room in the workspace");
+  static_assert(T::TN * T::TM <= 128 * 224, "a partial tile's room in the workspace");
   const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (g.N + T::TN - 1) / T::TN, blocks = (g.K + 127) / 128;
   const int64_t tiles = (int64_t)tiles_m * tiles_n, steps = tiles * blocks;
   const int groups = (int)(steps < kRingGroups ? steps : kRingGroups);
@@ -565,10 +589,10 @@ int ring_tokens(int64_t m) {
 
 }  // namespace
 
-// Two partial tiles of each workgroup.  Never less for more tokens, so that one workspace serves smaller calls too.
+// Two partial tiles of each workgroup.  More tokens never need less, so that one workspace serves smaller calls too.
 size_t fp8_gemm_workspace(int64_t m) {
   const int tm = ring_tokens(m);
-  return (size_t)kRingGroups * 2 * 128 * (tm < 128 ? tm : 128) * sizeof(float);
+  return (size_t)kRingGroups * 2 * 128 * tm * sizeof(float);
 }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
@@ -580,7 +604,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
     case 32: return launch_ring<1, 2, 8, 1, 7>(g, ws, s);
     case 64: return launch_ring<1, 4, 8, 1, 6>(g, ws, s);
     case 128: return launch_ring<2, 4, 4, 2, 4>(g, ws, s);
-    default: return launch_ring<1, 7, 4, 2, 4>(g, ws, s);
+    default: return launch_ring<2, 7, 4, 2, 3>(g, ws, s);
   }
 }
 

@@ -592,7 +592,7 @@ enum {
 int nvfp4_fp8_quantize(const void* x, int x_dtype, int64_t ld_x, const nvfp4_fp8_tensor* q, int flags, void* stream);
 
 /* Bytes of device workspace nvfp4_fp8_gemm needs for a->rows rows (any
- * weight): 4 MB up to 16 rows, 32 MB at most.  0 for a number it does not take. */
+ * weight): 4 MB up to 16 rows, 59 MB at most.  0 for a number it does not take. */
 size_t nvfp4_fp8_gemm_workspace_bytes(int64_t rows);
 
 /*

@@ -89,7 +89,7 @@ def test_linear_workspace():
     assert linear(wsb=f(5, 272) - 1) == -8
     f = nv.nvfp4_fp8_gemm_workspace_bytes
     sizes = [f(n) for n in (0, 1, 16, 17, 64, 128, 129, 5000, (1 << 31) - 1)]
-    assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] <= 1 << 25 and f(-1) == 0 and f(1 << 31) == 0
+    assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] < 59e6 and f(-1) == 0 and f(1 << 31) == 0
     assert gemm(wsb=f(5) - 1) == -8
     with pytest.raises(nv.NVFP4Error):
         nv.fp8_linear_workspace(5, 100, "cpu")
