@@ -595,10 +595,19 @@ size_t fp8_gemm_workspace(int64_t m) {
   return (size_t)kRingGroups * 2 * 128 * tm * sizeof(float);
 }
 
+// In steps (a block of a tile, about 1.5 us either way) of the busiest workgroup: whole waves of 256 x 224 tiles against
+// an even share of 128 x 224 tiles, whose partial sums and join cost as much as 9 steps.  Measured, us, shared | whole tiles:
+// 224 x 34816 x 5120 97 | 76; 300 x 5120 x 5120 36 | 60; 448 x 5120 x 17408 73 | 188; 672 x 5120 x 5120 45 | 61; 1024 x 5120 x
+// 5120 62 | 61; 1024 x 34816 x 5120 323 | 221.
+bool fp8_gemm_shares(const Fp8GemmArgs& g) {
+  if (g.out_dtype != NVFP4_DTYPE_BF16 || g.M <= 128) return true;
+  const int64_t blocks = (g.K + 127) / 128, tiles_m = (g.M + 223) / 224;
+  const int64_t waves = (tiles_m * ((g.N + 255) / 256) + 255) / 256;
+  return waves * blocks > tiles_m * ((g.N + 127) / 128) * blocks / kRingGroups + 9;
+}
+
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
-  if (g.out_dtype == NVFP4_DTYPE_BF16 && g.M > 224 && g.a.code_block == 128) {
-    return launch_pipe<8, 7, 2, 2>(g, 0, g.N, s);
-  }
+  if (!fp8_gemm_shares(g)) return launch_pipe<8, 7, 2, 2>(g, 0, g.N, s);
   switch (ring_tokens(g.M)) {
     case 16: return launch_ring<1, 1, 8, 1, 8>(g, ws, s);
     case 32: return launch_ring<1, 2, 8, 1, 7>(g, ws, s);

@@ -76,10 +76,9 @@ int check_product(int64_t m, int64_t n, int64_t k, void* out, int out_dtype, int
   return NVFP4_OK;
 }
 
-// The workspace of nvfp4_fp8_linear: the product's, then codes, then scales [pieces, rows].  Codes of few rows as [pieces,
-// rows, 128], so that what a tile reads of one block of columns lies together (64 x 34816 x 5120 47 -> 42.5 us, 200 x 5120 x
-// 17408 54 -> 53), of more as [rows, 128 pieces] (8192 x 5120 x 17408: 715 us so, 722 with blocks together).
-constexpr int64_t kTogether = 224;
+// The workspace of nvfp4_fp8_linear: the product's, then codes, then scales [pieces, rows].  Codes as [pieces, rows, 128]
+// where the product is shared out in small steps, so that what a step reads lies together (64 x 34816 x 5120 47 -> 42.5 us,
+// 200 x 5120 x 17408 54 -> 53), else as [rows, 128 pieces] (8192 x 5120 x 17408: 715 us so, 722 the other way).
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 int check_heads(const nvfp4_head_rows* r, int64_t tokens, int head_dim, int esz) {
@@ -172,7 +171,8 @@ int nvfp4_fp8_linear(const void* x, int x_dtype, int64_t rows, int64_t ld_x, con
   if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
   uint8_t* codes = (uint8_t*)workspace + up16((int64_t)fp8_gemm_workspace(rows));
   const int64_t wide = pieces_of(w->cols) * 128;
-  g.a = Fp8Mat{codes, (float*)(codes + rows * wide), rows <= kTogether ? 128 : wide, rows <= kTogether ? rows * 128 : 128, 1, rows};
+  const bool together = fp8_gemm_shares(g);
+  g.a = Fp8Mat{codes, (float*)(codes + rows * wide), together ? 128 : wide, together ? rows * 128 : 128, 1, rows};
   const hipError_t e = launch_fp8_quantize_rows(x, x_dtype, rows, w->cols, ld_x, g.a, false, (hipStream_t)stream);
   if (e != hipSuccess) return status_from_hip(e);
   return status_from_hip(launch_fp8_gemm(g, (float*)workspace, (hipStream_t)stream));

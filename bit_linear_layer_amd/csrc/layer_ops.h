@@ -31,6 +31,8 @@ struct Fp8GemmArgs {
   int M, N, K;
 };
 size_t fp8_gemm_workspace(int64_t m);  // bytes for products of up to 2^31 columns with m tokens
+// Whether the product is shared out in small steps; then a.code_block may be any, else it is 128.
+bool fp8_gemm_shares(const Fp8GemmArgs& g);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s);
 
 struct RopeArgs {

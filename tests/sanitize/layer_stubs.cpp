@@ -28,6 +28,7 @@ hipError_t launch_fp8_quantize_blocks(const void*, int, int64_t rows, int64_t co
   return record(rows, cols, q.ld_codes, q.scale_block);
 }
 size_t fp8_gemm_workspace(int64_t m) { return (m <= 16 ? 1 : 8) << 22; }
+bool fp8_gemm_shares(const Fp8GemmArgs& g) { return g.M <= 128; }
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float*, hipStream_t) { return record(g.M, g.N, g.K, g.ld_out); }
 hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t) { return record(a.tokens, a.rows[0].heads, a.rows[1].heads, a.rope.rotary_dim); }
 hipError_t launch_causal_conv(const nvfp4_conv& c, int, hipStream_t) { return record(c.tokens, c.channels, c.batch, c.width); }

@@ -130,7 +130,8 @@ def test_product(m, n, k, out_dtype):
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
-@pytest.mark.parametrize("m,n,k", [(1, 34816, 1024), (9, 5120, 5120), (40, 5120, 8192), (150, 2048, 17408), (1030, 1300, 1024), (2048, 2560, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 34816, 1024), (9, 5120, 5120), (40, 5120, 8192), (150, 2048, 17408), (1030, 1300, 1024), (2048, 2560, 512), (200, 17000, 400),
+                                   (500, 5120, 1200), (700, 12900, 272)])
 def test_product_of_large_operands(m, n, k, out_dtype):
     say(f"fp8 gemm large {m}x{n}x{k} {out_dtype}")
     a, w = operands(np.random.default_rng(m + n), m, n, k)
@@ -199,7 +200,7 @@ def test_bytes_behind_the_columns_do_not_matter(m):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("m,n,k", [(1, 512, 272), (4, 5120, 5120), (16, 130, 2064), (17, 300, 1024), (90, 640, 1040), (700, 1024, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 512, 272), (4, 5120, 5120), (16, 130, 2064), (17, 300, 1024), (90, 640, 1040), (700, 1024, 512), (150, 1030, 4112), (180, 20000, 528), (1500, 5120, 272)])
 def test_linear_is_quantize_and_product(m, n, k, dtype):
     say(f"fp8 linear {m}x{n}x{k} {dtype}")
     rng = np.random.default_rng(m + k)
