@@ -782,14 +782,12 @@ class Rope:
                      0 if axis is None else axis.data_ptr(), axes, 2 * f.shape[0], int(self.interleaved))
 
 
-def _heads_of(x: torch.Tensor, tokens: int, head_dim: int, device: torch.device, what: str):
+def _heads_of(x: torch.Tensor, tokens: int, head_dim: int, what: str):
     """(heads, row stride, head stride) of [tokens, heads * head_dim] or [tokens, heads, head_dim]."""
     shape, stride = x.shape, x.stride()
-    if x.device != device:
-        raise NVFP4Error(f"{what} must live on {device}, got {x.device}")
     if len(shape) == 2:
-        heads, rest = divmod(shape[1], head_dim)
-        if shape[0] == tokens and heads > 0 and rest == 0 and stride[1] == 1:
+        heads = shape[1] // head_dim
+        if shape[0] == tokens and heads > 0 and heads * head_dim == shape[1] and stride[1] == 1:
             return heads, stride[0] if tokens > 1 else shape[1], head_dim
     elif len(shape) == 3 and shape[0] == tokens and shape[1] > 0 and shape[2] == head_dim and stride[2] == 1:
         heads = shape[1]
@@ -804,8 +802,10 @@ def _head_rows(x, out, weight, tokens: int, head_dim: int, dtype, device: torch.
         return None
     if out is None or x.dtype is not dtype or out.dtype is not dtype or out.shape != x.shape:
         raise NVFP4Error(f"{what} and its output must share shape and dtype, queries and keys one dtype")
-    heads, ld, head = _heads_of(x, tokens, head_dim, device, what)
-    _, ld_o, head_o = _heads_of(out, tokens, head_dim, device, what)
+    if x.device != device or out.device != device:
+        raise NVFP4Error(f"{what} and its output must live on {device}")
+    heads, ld, head = _heads_of(x, tokens, head_dim, what)
+    _, ld_o, head_o = _heads_of(out, tokens, head_dim, what)
     w = 0
     if weight is not None:
         if weight.dtype is not torch.float32 or weight.shape != (head_dim,) or not weight.is_contiguous():
@@ -851,19 +851,16 @@ def _per_sequence(t: torch.Tensor | None, n: int, dtype, device: torch.device, w
     return t.data_ptr()
 
 
-def _state_stride(states: torch.Tensor, shape: tuple, dtype, device: torch.device, what: str) -> int:
-    """Elements from one state to the next of a pool [n > 0, *shape] whose states are contiguous."""
-    full, stride, want = states.shape, states.stride(), 1
-    ok = states.dtype is dtype and len(full) == len(shape) + 1 and full[1:] == shape and full[0] > 0
-    if ok:
-        for n, by in zip(reversed(shape), reversed(stride)):
-            ok = ok and (by == want or n == 1)
-            want *= n
-    if not ok:
+def _state_stride(states: torch.Tensor, shape: tuple, dense: tuple, dtype, device: torch.device, what: str) -> int:
+    """Elements from one state to the next of a pool [n > 0, *shape] whose
+    states are contiguous, with the strides ``dense``."""
+    full, stride = states.shape, states.stride()
+    if states.dtype is not dtype or full[1:] != shape or full[0] < 1 \
+            or stride[1:] != dense and any(n > 1 and by != want for n, by, want in zip(shape, stride[1:], dense)):
         raise NVFP4Error(f"{what} must be {str(dtype)[6:]} [n, {', '.join(map(str, shape))}], each state contiguous")
     if states.device != device:
         raise NVFP4Error(f"{what} must live on {device}, got {states.device}")
-    return stride[0] if full[0] > 1 else want
+    return stride[0] if full[0] > 1 else shape[0] * dense[0]
 
 
 def nvfp4_causal_conv(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, batch: int, starts: torch.Tensor | None = None,
@@ -887,7 +884,7 @@ def nvfp4_causal_conv(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, ba
         raise NVFP4Error("y must have x's dtype")
     n_states = ld_state = 0
     if state is not None:
-        ld_state = _state_stride(state, (width - 1, channels), x.dtype, device, "state")
+        ld_state = _state_stride(state, (width - 1, channels), (channels, 1), x.dtype, device, "state")
         n_states = state.shape[0]
     elif slots is not None or fresh is not None:
         raise NVFP4Error("slots and fresh need a state")
@@ -918,7 +915,7 @@ def nvfp4_gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torc
                       v.data_ptr(), _row_stride(v, rows, vw, device, "v"), beta.data_ptr(),
                       _row_stride(beta, rows, v_heads, device, "beta"), g.data_ptr(), _row_stride(g, rows, v_heads, device, "g"))
     ld_o = _row_stride(o, rows, vw, device, "o")
-    ld_s = _state_stride(states, (v_heads, 128, 128), torch.float32, device, "states")
+    ld_s = _state_stride(states, (v_heads, 128, 128), (16384, 128, 1), torch.float32, device, "states")
     _check(_call_on(device, stream, load().nvfp4_gdn_step, ins, dt, batch, q_len, k_heads, v_heads, int(normalize_qk),
                     states.data_ptr(), states.shape[0], ld_s, _per_sequence(slots, batch, torch.int32, device, "slots"),
                     _per_sequence(fresh, batch, torch.uint8, device, "fresh"), o.data_ptr(), _dtype_code(o), ld_o),

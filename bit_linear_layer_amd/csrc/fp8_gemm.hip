@@ -322,11 +322,19 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const Fp8GemmArgs p, int 
   if (g0 == g1) return;  // stored as it was finished
   const int e = blockIdx.y * 256 + threadIdx.x;
   if (e >= T::TN * T::TM / 4) return;
-  floatx4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int g = g0; g <= g1; ++g) {
-    const bool begins = Share(steps, groups, g).first <= lo;
-    sum += *reinterpret_cast<const floatx4*>(partial + ((int64_t)g * 2 + begins) * (T::TN * T::TM) + e * 4);
+  // only the tile's first workgroup may have begun it
+  const floatx4* at = reinterpret_cast<const floatx4*>(partial) + e;
+  constexpr int kSlot = T::TN * T::TM / 4, kAhead = 4;
+  floatx4 sum = at[((int64_t)g0 * 2 + (Share(steps, groups, g0).first <= lo)) * kSlot];
+  int g = g0 + 1;
+  for (; g + kAhead <= g1 + 1; g += kAhead) {
+    floatx4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = at[(int64_t)(g + u) * 2 * kSlot];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) sum += v[u];
   }
+  for (; g <= g1; ++g) sum += at[(int64_t)g * 2 * kSlot];
   const int lane = e & 63, f = e >> 6, j = f % FM, i = f / FM % FN, wave = f / (FM * FN);
   const int m = tile % tiles_m * T::TM + (wave % WM * FM + j) * 16 + (lane & 15);
   const int n = tile / tiles_m * T::TN + (wave / WM * FN + i) * 16 + 4 * (lane >> 4);
@@ -562,7 +570,11 @@ hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
   static_assert(T::TN * T::TM <= 128 * 224, "a partial tile's room in the workspace");
   const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (g.N + T::TN - 1) / T::TN, blocks = (g.K + 127) / 128;
   const int64_t tiles = (int64_t)tiles_m * tiles_n, steps = tiles * blocks;
-  const int groups = (int)(steps < kRingGroups ? steps : kRingGroups);
+  // At least 4 steps a workgroup, where a tile has them: fewer sums to join.  Measured, us with at least 1, 2, 4, 8:
+  // 1 x 1024 x 5120 11.0, 9.4, 8.5, 9.2; 40 x 2048 x 2048 12.8, 10.4, 9.9, 10.6; 128 x 1024 x 5120 18.5, 15.1, 12.5, 13.2;
+  // 200 x 1024 x 5120 24.0, 20.3, 16.8, 17.8; 77 x 1000 x 2064 float32 12.7, 11.1, 11.8, 15.5.
+  const int64_t want = tiles > steps / 4 ? tiles : steps / 4;
+  const int groups = (int)(want < kRingGroups ? want : kRingGroups);
   const auto fn = fp8_ring_kernel<FN, FM, WN, WM, D, EXACT, OUT>;
   hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, D * T::kStage);
   if (e != hipSuccess) return e;
