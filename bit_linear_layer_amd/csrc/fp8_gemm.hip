@@ -497,6 +497,12 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
         if (i == 1) x[(t + 1) & 1] = t < FM - 1 ? read_x(st, t + 1) : read_x(nst, 0);
         tmp[n % (kLag + 1)] = block_product<false>(w[i], x[t & 1]);
         if (n >= kLag) add(n - kLag);
+        // the next block's scales: early enough that nothing waits for them
+        if (t == 1 && i == 2) next_sw = sw[min(b + 1, blocks - 1) * p.w.scale_block];
+        if (t == FM - 1 && i == 0) {
+#pragma unroll
+          for (int j = 0; j < FM; ++j) next_sc[j] = read_s(nst, j);
+        }
         if (t == FM - 1) w[i] = read_w(nst, i);
         const int c = i - 1;
         if (c >= 0 && c < x_hi - x_lo) copy_x(t < 3 ? b + 1 : b + 2, x_lo + c);
@@ -506,14 +512,11 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
       __builtin_amdgcn_sched_barrier(0);
       if (t == FM - 1) {
 #pragma unroll
-        for (int j = 0; j < FM; ++j) next_sc[j] = read_s(nst, j);
-#pragma unroll
         for (int o = FM * FN - kLag; o < FM * FN; ++o) add(o);
 #pragma unroll
         for (int j = 0; j < FM; ++j) next_sc[j] *= next_sw;
       }
       if (t == 1) {
-        next_sw = sw[min(b + 1, blocks - 1) * p.w.scale_block];
         barrier_lds();
         __builtin_amdgcn_s_waitcnt(0xC07F);  // the barrier's lgkmcnt(0) again, seen by the compiler's own wait insertion
       }
