@@ -10,7 +10,8 @@
 // one activation scale per 16-token tile and stores its columns side by side.
 //
 // Two products (block_product):
-//   bf16 output     v_mfma_scale_f32_16x16x128_f8f6f4 with unit scales.  The
+//   bf16 output     v_mfma_f32_16x16x128_f8f6f4 (the builtin with scale operands
+//                   0 is the form without scales: 2 % faster than unit scales).  The
 //                   instruction cuts the products of 8 neighbouring k to
 //                   multiples of 2^-13 of the largest's power of two before it
 //                   adds them (measured); 1.5e-5 of a normally distributed result,
@@ -93,7 +94,9 @@ __device__ inline void store4(void* out, int64_t at, const floatx4& v, int left,
 }
 
 // Products with few tokens, or of too few tiles to fill the chip: bound by the
-// weight's bytes up to about 200 tokens.  256 workgroups of 8 waves, one per CU, share the
+// weight's bytes up to about 64 tokens, beyond by the copies into LDS.  Measured, with the join: 3 x 34816 x 5120 36 us
+// (5.0 TB/s), 16 x 5120 x 17408 25, 64 x 34816 x 5120 51, 200 x 5120 x 17408 48 -- the copies alone take 34, the
+// products alone 36, the join 9.  Tiles of 64 columns at 224 tokens: 53 instead of 41 before the join.  256 workgroups of 8 waves, one per CU, share the
 // line of all (tile, block of 128) steps evenly, tile by tile; a workgroup's copies
 // run D steps ahead of its products, across the ends of tiles, so that the
 // stream from memory never drains.  A tile whose steps lie in one workgroup is stored; of one that a
@@ -114,7 +117,9 @@ struct Ring {
   static constexpr int CW = TN / 64, CX = TM / 64;           // copies of every wave
   static constexpr int XR = TM / 8 % 8;                      // waves that copy one more group of activation rows
   static constexpr int kBase = CW + CX;
-  static constexpr int kHint = TM == 16 ? 2 : 0;
+  // Non-temporal weights.  Measured, us, without | with: 3 x 34816 x 5120 42.3 | 37.8, 16 x 5120 x 17408 26.2 | 25.6, 32 x 34816 x
+  // 5120 47.4 | 46.3, 64 x 34816 x 5120 55.6 | 59.8, 128 x 34816 x 5120 69.3 | 73.1, 200 x 5120 x 17408 47.0 | 50.4.
+  static constexpr int kHint = TM <= 32 ? 2 : 0;
   static constexpr int kStage = kW + kX + NS * 256;
   static_assert(WN * WM == 8 && TN % 64 == 0 && 128 % TN == 0 && XR + NS <= 8 && D * kStage <= 160 * 1024, "the copies' shares");
   static_assert((D - 1) * (kBase + 1) < 64, "vmcnt's range");
@@ -343,10 +348,17 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const Fp8GemmArgs p, int 
 }
 
 // Large products.  WN x WM = 4 waves, one per SIMD; a wave owns FN * 16
-// columns x FM * 16 tokens (256 x 256 tiles: 128 x 128, 256 accumulators a
+// columns x FM * 16 tokens (256 x 224 tiles: 128 x 112, 224 accumulators a
 // lane).  Per block of 128 a wave reads FN + FM fragments of 2 KB from LDS for FN * FM
 // matrix instructions of 32 cycles; each instruction's four fmas (out += scale *
-// tmp) run two instructions later, beside the matrix unit.
+// tmp) run three instructions later, beside the matrix unit.
+//
+// Bound: the matrix unit with the fmas beside it.  Measured, 8192 x 5120 x 17408: 633-646 us, 2.2-2.3 PFLOP/s (8192 x
+// 34816 x 5120 2.17, 8192^3 2.21), at a clock of 1.9 GHz under this load; the same instructions and fmas from registers
+// alone reach 3.1, a library product with a single scale 2.06 at this size and 2.7 at 8192^3.  Other forms at this
+// size, in the version where this one took 659: 256 x 256 tiles 732 (their sums no longer fit beside the fragments in the
+// vector registers and are moved to and fro), two waves per SIMD with half the accumulators each 704 (twice the
+// LDS reads).
 //
 // LDS holds two stages of a block: weight rows, activation rows (128 bytes each),
 // the tile's activation scales; all three come by LDS DMA.  16-byte pieces are
@@ -421,7 +433,8 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(sa + (int64_t)min(b, blocks - 1) * p.a.scale_block),
                                      (lds_u32_ptr)(smem + (b & 1) * T::kStage + T::kW + T::kX + srow * 4), 4, 0, 0);
   };
-  const auto* sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)((n0 + wn * FN * 16) / 128) * p.w.scale_row);
+  // a wave whose columns all lie behind the last takes the last block's scales
+  const auto* sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)(min(n0 + wn * FN * 16, p.N - 1) / 128) * p.w.scale_row);
 
   // fragments: weight row (i, a = lane % 16) is column (i / 2) * 32 + (a / 4) * 8 + (i % 2) * 4 + a % 4 of the wave, so that a
   // lane's results of fragments 2 i and 2 i + 1 are 8 neighbouring columns

@@ -116,7 +116,7 @@ def close(out, a, w, extra=0.0):
     assert bad.size == 0, f"{len(bad)} of {err.size} outside, first {bad[:3].tolist()}: {[(err[i, j], tol[i, j]) for i, j in bad[:3]]}"
 
 
-SHAPES = [(1, 1, 16), (4, 384, 6400), (16, 200, 17408), (30, 640, 3600), (100, 130, 6400), (130, 130, 9984), (224, 128, 16384), (225, 192, 400), (1, 128, 128), (2, 130, 144), (3, 1000, 272), (5, 4096, 1040), (15, 64, 4096), (16, 129, 2064), (17, 257, 128),
+SHAPES = [(1, 1, 16), (300, 300, 16), (129, 70, 128), (240, 256, 144), (1000, 40, 272), (130, 1, 16), (4, 384, 6400), (16, 200, 17408), (30, 640, 3600), (100, 130, 6400), (130, 130, 9984), (224, 128, 16384), (225, 192, 400), (1, 128, 128), (2, 130, 144), (3, 1000, 272), (5, 4096, 1040), (15, 64, 4096), (16, 129, 2064), (17, 257, 128),
           (33, 100, 640), (64, 512, 1024), (65, 384, 2064), (77, 1000, 400), (128, 128, 128), (129, 640, 256), (200, 1111, 912),
           (257, 513, 384), (300, 256, 3200), (511, 1280, 512)]
 
