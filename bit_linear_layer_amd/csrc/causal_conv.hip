@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kElemThreads) void causal_conv_kernel(const nvfp4_c
 }
 
 // One token of each sequence: a thread per sequence and 8 channels.  Nothing
-// waits for the slot but the state itself.
+// waits for the slot but the state itself.  64 sequences of 10240 channels: 5.8 us, the general kernel 8.3.
 template <int DT, int W>
 __global__ __launch_bounds__(kElemThreads) void causal_conv_step_kernel(const nvfp4_conv c) {
   constexpr int kBytes = DT == NVFP4_DTYPE_BF16 ? 16 : 32, kOld = W - 1;
@@ -229,11 +229,11 @@ __global__ __launch_bounds__(kElemThreads) void causal_conv_step_kernel(const nv
 template <int DT, int W>
 void launch(const nvfp4_conv& c, hipStream_t s) {
   const int64_t each = c.tokens / c.batch, chunks = c.channels / 8;
-  const bool step = c.starts == nullptr && each == 1;
   // Longer runs read fewer inputs twice, shorter ones keep more threads busy.  Measured, bf16, us with runs of 4, 8, 16, 32
   // (C = 10240 unless said): 64 rows 8.3, 8.7, 11.9, 18.5; 512 rows 11.3, 11.0, 13.5, 19.9; 2048 rows 28.2, 24.7, 22.7,
   // 26.3; 31500 rows of 1024 37.3, 33.0, 32.7, 33.3; 8192 rows 110, 88, 79, 81; 31500 rows 417, 332, 293, 269 (4.8 TB/s).
   const int64_t places = c.tokens * chunks;
+  const bool step = c.starts == nullptr && each == 1 && places < (int64_t)1 << 31;  // its threads fit a grid
   const int run = places >= (int64_t)1 << 25 ? 32 : places >= 1 << 21 ? 16 : places >= 1 << 19 ? 8 : 4;
   const int64_t threads = step ? places : (c.tokens + run - 1) / run * chunks;
   const unsigned grid = (unsigned)((threads + kElemThreads - 1) / kElemThreads);

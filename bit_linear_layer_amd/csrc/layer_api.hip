@@ -62,7 +62,8 @@ int check_product(int64_t m, int64_t n, int64_t k, void* out, int out_dtype, int
   if (n <= 0) return NVFP4_ERR_SHAPE;
   if (ld_out < n) return NVFP4_ERR_STRIDE;
   if (ld_out >= kIndexLimit || m >= kSizeLimit / ld_out) return NVFP4_ERR_RANGE;
-  // the smallest tiles: 32 columns of all tokens up to 64, 64 x 64 above
+  // every tile is larger (16 to 224 tokens x 128 columns, 256 x 224): grids stay below 2^32 threads, and a tile's last row and
+  // column inside 32 bits
   if ((m <= 64 ? (n + 31) / 32 : (n + 63) / 64 * ((m + 63) / 64)) >= kGridLimit) return NVFP4_ERR_RANGE;
   if (m == 0) return NVFP4_OK;
   if (out == nullptr) return NVFP4_ERR_NULL;
@@ -102,7 +103,7 @@ int check_heads(const nvfp4_head_rows* r, int64_t tokens, int head_dim, int esz)
 int check_rope(const nvfp4_rope* r, int64_t tokens, int head_dim) {
   if (r->rotary_dim < 16 || r->rotary_dim > head_dim || r->rotary_dim % 16 != 0 || r->axes < 1 || r->axes > 255)
     return NVFP4_ERR_SHAPE;
-  if (r->ld_positions < tokens) return NVFP4_ERR_STRIDE;
+  if (r->ld_positions < tokens && r->ld_positions != 0) return NVFP4_ERR_STRIDE;
   if (r->ld_positions >= kSizeLimit) return NVFP4_ERR_RANGE;
   if (tokens == 0) return NVFP4_OK;
   if (r->positions == nullptr || r->inv_freq == nullptr) return NVFP4_ERR_NULL;

@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kElemThreads) void qk_norm_rope_kernel(const RopeAr
   const int n = (int)min((int64_t)tokens, a.tokens - t0) * heads;  // rows of these tokens
   const int dim = a.rope.rotary_dim, half = dim / 2;
 
-  float v[8], next[8];
+  float v[8], next[8] = {};
   struct Row {
     int token, head;
     bool key, there;

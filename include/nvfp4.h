@@ -601,7 +601,8 @@ size_t nvfp4_fp8_gemm_workspace_bytes(int64_t rows);
  * (out = A W^T), a = activations [M, K] (block_rows 1), w = weight [N, K]
  * (block_rows 128).
  *   out   DEVICE [M, ld_out] of out_dtype (bf16: round to nearest even),
- *         ld_out >= N elements.
+ *         ld_out >= N elements, below 2^31; M * ld_out < 2^40.
+ * N < 2^29 - 31 for M <= 64, above that ceil(N / 64) * ceil(M / 64) < 2^24.
  * Sums over a block and over blocks are float32.  With out_dtype F32 the
  * products are exact (codes as fp16 on the matrix unit) and the result is within
  * (K / 128 + 136) 2^-23 sum |a w| of the exact one.  With BF16 the 8-bit matrix
@@ -656,10 +657,11 @@ typedef struct {
  * The rotation of a head's first rotary_dim dimensions, in rotary_dim / 2
  * pairs: (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0.  Pair
  * i turns by the angle positions[axis[i] * ld_positions + t] * inv_freq[i].
- *   positions  DEVICE int64 [axes, ld_positions], ld_positions >= tokens:
- *              one axis for text, three (time, height, width) for images and
- *              video.  Angles are formed in 64 bits: far positions keep
- *              float32's precision (below 2^31 times inv_freq <= 1).
+ *   positions  DEVICE int64 [axes, ld_positions], ld_positions >= tokens, or 0
+ *              where all axes share one row: one axis for text, three (time,
+ *              height, width) for images and video.  Angles are formed in 64
+ *              bits: far positions keep float32's precision (below 2^31 times
+ *              inv_freq <= 1).
  *   inv_freq   DEVICE float32 [rotary_dim / 2].
  *   axis       DEVICE uint8 [rotary_dim / 2], the axis of each pair; NULL:
  *              axis 0.  A value beyond axes - 1 counts as axes - 1.

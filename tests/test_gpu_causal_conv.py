@@ -89,6 +89,27 @@ def test_uniform_batches_without_starts_slots_or_states(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_next_tokens_of_a_padded_batch(width, dtype):
+    """One row a sequence without starts: places without a state, fresh ones, strides, a pool with more states than places."""
+    say(f"conv next tokens W={width} {dtype}")
+    rng = np.random.default_rng(20 + width)
+    for n, silu in ((1, True), (7, False), (33, True)):
+        wide, w, b, pool = inputs(rng, n, 72, width, dtype, n + 4)
+        w, b = w[:40].contiguous(), b[:40].contiguous()
+        x, state = wide[:, 16:56], pool[:, :, :40].contiguous()
+        slots, fresh = rng.permutation(n + 4)[:n], rng.integers(0, 2, n)
+        if n > 4:
+            slots[[0, 2, 4]] = -1, n + 4, -2 ** 31
+            fresh[0], fresh[2] = 0, 1
+        before, out = state.clone(), torch.full((n, 64), -7.0, dtype=dtype, device=DEV)
+        nv.nvfp4_causal_conv(x, w, out[:, 8:48], n, None, b, silu, state, torch.from_numpy(slots).int().to(DEV),
+                             torch.from_numpy(fresh).to(torch.uint8).to(DEV))
+        check(x, w, out[:, 8:48], np.arange(n + 1), b, silu, before, state, slots, fresh)
+        assert bool((out[:, :8] == -7).all()) and bool((out[:, 48:] == -7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_a_prompt_in_chunks_and_single_tokens(dtype):
     """The same rows as one call, as chunks and token by token: the same bits, and the same state at the end."""
     say(f"conv chunks {dtype}")

@@ -140,6 +140,9 @@ def test_axis_values_beyond_the_axes_and_bad_plans():
     got, _ = nv.qk_norm_rope(x, x, 64, pos, rope)
     close(got, x, 64, positions=pos.cpu().numpy(), inv_freq=freq, axis=rope.axis.cpu().numpy())
 
+    shared = pos[:1].expand(2, 9)  # one row for all axes
+    assert torch.equal(nv.qk_norm_rope(x, x, 64, shared, rope)[0], nv.qk_norm_rope(x, x, 64, shared.contiguous(), rope)[0])
+
     def refused(**kw):
         a = dict(positions=pos, rope=rope)
         a.update(kw)
