@@ -96,6 +96,8 @@ int check_heads(const nvfp4_head_rows* r, int64_t tokens, int head_dim, int esz)
   }
   if (tokens == 0) return NVFP4_OK;
   if (r->x == nullptr || r->out == nullptr) return NVFP4_ERR_NULL;
+  // in place every element is read by the thread that writes it
+  if (r->x == r->out && ((tokens > 1 && r->ld_x != r->ld_out) || (r->heads > 1 && r->head_x != r->head_out))) return NVFP4_ERR_STRIDE;
   if (!aligned(r->x, 16) || !aligned(r->out, 16) || !aligned(r->weight, 4)) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
 }

@@ -76,8 +76,8 @@ __global__ __launch_bounds__(kElemThreads) void qk_norm_rope_kernel(const RopeAr
     const int row = pass * kSlots + slot;
     Row r;
     r.there = row < n;
-    r.token = row / heads;
-    const int h = row - r.token * heads;
+    r.token = r.there ? row / heads : 0;  // its place in the tables
+    const int h = r.there ? row - r.token * heads : 0;
     r.key = h >= hq;
     r.head = r.key ? h - hq : h;
     return r;

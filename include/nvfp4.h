@@ -641,7 +641,7 @@ int nvfp4_fp8_linear(const void* x, int x_dtype, int64_t rows, int64_t ld_x, con
  * element (t, h, d) at x[t * ld_x + h * head_x + d], its result at
  * out[t * ld_out + h * head_out + d], so that a projection's columns, heads
  * interleaved with something else among them, are taken as they are.  out may
- * be x with the same strides.
+ * be x with the same strides (others are refused); else they must not overlap.
  *   weight  DEVICE float32 [head_dim], or NULL: no norm.
  */
 typedef struct {

@@ -134,6 +134,18 @@ def test_bad_heads(kw, status):
     assert rope(k=rows_of(**kw)) == status and rope(none=True, k=rows_of(**kw)) == status
 
 
+def test_in_place_only_with_the_same_strides():
+    for kw in (dict(ldo=640), dict(ldo=640, heado=136), dict(ld=1280, heado=144, ldo=1280)):
+        assert rope(q=rows_of(**kw)) == -4
+    assert rope(tokens=1, q=rows_of(heado=136, ldo=640)) == -4
+    # strides that are not used differ: the next check is reached
+    assert rope(tokens=1, q=rows_of(ldo=640, w=FAKE + 2)) == -5 and rope(q=rows_of(heads=1, heado=1024, w=FAKE + 2)) == -5
+
+
+def test_one_row_of_positions_for_all_axes():
+    assert rope(r=turn(ld=0, freq=FAKE + 2)) == -5 and rope(r=turn(ld=1)) == -4 and rope(r=turn(ld=-1)) == -4
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(pos=None), -1), (dict(freq=None), -1), (dict(dim=0), -2), (dict(dim=8), -2), (dict(dim=72), -2), (dict(dim=144), -2),
     (dict(axes=0), -2), (dict(axes=256), -2), (dict(ld=9), -4), (dict(ld=1 << 50), -11), (dict(pos=FAKE + 4), -5), (dict(freq=FAKE + 2), -5),
