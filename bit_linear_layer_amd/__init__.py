@@ -29,13 +29,14 @@ __all__ = [
     "FP8Tensor", "empty_fp8", "nvfp4_fp8_quantize", "nvfp4_fp8_gemm", "nvfp4_fp8_linear", "nvfp4_fp8_gemm_workspace_bytes",
     "nvfp4_fp8_linear_workspace_bytes", "fp8_gemm_workspace",
     "fp8_quantize", "fp8_gemm", "fp8_linear", "fp8_linear_workspace", "Rope", "nvfp4_qk_norm_rope", "qk_norm_rope",
-    "nvfp4_causal_conv", "causal_conv", "nvfp4_gdn_step", "gdn_step", "FP8_SCALE_F32", "FP8_SCALE_POW2",
+    "nvfp4_causal_conv", "causal_conv", "nvfp4_gdn_step", "gdn_step", "FP8_SCALE_F32", "FP8_SCALE_POW2", "FP8_CUT_SUMS",
     "DTYPE_BF16", "DTYPE_F32", "SCALE_DYNAMIC", "SCALE_STATIC", "AMAX_PRECOMPUTED", "MAX_SEGMENTS",
 ]
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 SCALE_DYNAMIC, SCALE_STATIC, AMAX_PRECOMPUTED = 0, 1, 2
 FP8_SCALE_F32, FP8_SCALE_POW2 = 0, 1
+FP8_CUT_SUMS = 0x100
 MAX_SEGMENTS = 16
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4.so")
@@ -724,12 +725,15 @@ def _space(workspace: torch.Tensor, device: torch.device):
     return workspace.data_ptr(), workspace.nbytes
 
 
-def nvfp4_fp8_gemm(a: FP8Tensor, w: FP8Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
-    """C ``nvfp4_fp8_gemm``: out[M, N] = A W^T, a by rows, w by blocks of 128 rows."""
+def nvfp4_fp8_gemm(a: FP8Tensor, w: FP8Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None,
+                   cut_sums: bool = False) -> None:
+    """C ``nvfp4_fp8_gemm``: out[M, N] = A W^T, a by rows, w by blocks of 128
+    rows.  cut_sums: ``NVFP4_FP8_CUT_SUMS``, faster and less exact (bf16 only)."""
     da, dw, device = a.descriptor(), w.descriptor(), w.codes.device
     _on(a.codes, device, "a")
     ld = _row_stride(out, a.rows, w.rows, device, "out")
-    _check(_call_on(device, stream, load().nvfp4_fp8_gemm, da, dw, out.data_ptr(), _dtype_code(out), ld,
+    _check(_call_on(device, stream, load().nvfp4_fp8_gemm, da, dw, out.data_ptr(),
+                    _dtype_code(out) | (FP8_CUT_SUMS if cut_sums else 0), ld,
                     *_space(workspace, device)), "nvfp4_fp8_gemm")
 
 
@@ -738,16 +742,18 @@ def nvfp4_fp8_linear_workspace_bytes(rows: int, cols: int) -> int:
     return int(load().nvfp4_fp8_linear_workspace_bytes(rows, cols))
 
 
-def nvfp4_fp8_linear(x: torch.Tensor, w: FP8Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+def nvfp4_fp8_linear(x: torch.Tensor, w: FP8Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None,
+                     cut_sums: bool = False) -> None:
     """C ``nvfp4_fp8_linear``: x [rows, w.cols] (bf16 or float32) quantized by
-    rows and multiplied with w into out [rows, w.rows]."""
+    rows and multiplied with w into out [rows, w.rows]; cut_sums as for
+    ``nvfp4_fp8_gemm``."""
     d, device = w.descriptor(), w.codes.device
     if x.dim() != 2:
         raise NVFP4Error(f"x must be [rows, {w.cols}], got {list(x.shape)}")
     rows = x.shape[0]
     ld_x, ld_o = _row_stride(x, rows, w.cols, device, "x"), _row_stride(out, rows, w.rows, device, "out")
     _check(_call_on(device, stream, load().nvfp4_fp8_linear, x.data_ptr(), _dtype_code(x), rows, ld_x, d, out.data_ptr(),
-                    _dtype_code(out), ld_o, *_space(workspace, device)), "nvfp4_fp8_linear")
+                    _dtype_code(out) | (FP8_CUT_SUMS if cut_sums else 0), ld_o, *_space(workspace, device)), "nvfp4_fp8_linear")
 
 
 @dataclass(frozen=True)
@@ -1108,10 +1114,11 @@ def fp8_gemm_workspace(rows: int, device="cuda") -> torch.Tensor:
 
 
 def fp8_gemm(a: FP8Tensor, w: FP8Tensor, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
-             workspace: torch.Tensor | None = None) -> torch.Tensor:
+             workspace: torch.Tensor | None = None, cut_sums: bool = False) -> torch.Tensor:
+    """A W^T (see ``nvfp4_fp8_gemm``)."""
     ws = workspace if workspace is not None else fp8_gemm_workspace(a.rows, a.codes.device)
     o = out if out is not None else torch.empty((a.rows, w.rows), dtype=out_dtype, device=a.codes.device)
-    nvfp4_fp8_gemm(a, w, o, ws)
+    nvfp4_fp8_gemm(a, w, o, ws, cut_sums=cut_sums)
     return o
 
 
@@ -1124,13 +1131,13 @@ def fp8_linear_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
 
 
 def fp8_linear(x: torch.Tensor, w: FP8Tensor, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
-               workspace: torch.Tensor | None = None) -> torch.Tensor:
+               workspace: torch.Tensor | None = None, cut_sums: bool = False) -> torch.Tensor:
     """x [rows, w.cols] through the E4M3 layer w (see ``nvfp4_fp8_linear``)."""
     if x.dim() != 2:
         raise NVFP4Error(f"x must be [rows, {w.cols}], got {list(x.shape)}")
     ws = workspace if workspace is not None else fp8_linear_workspace(x.shape[0], w.cols, x.device)
     o = out if out is not None else torch.empty((x.shape[0], w.rows), dtype=out_dtype, device=x.device)
-    nvfp4_fp8_linear(x, w, o, ws)
+    nvfp4_fp8_linear(x, w, o, ws, cut_sums=cut_sums)
     return o
 
 

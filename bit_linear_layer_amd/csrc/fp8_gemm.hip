@@ -9,15 +9,11 @@
 // a lane then holds one token (lane % 16) and four consecutive columns, needs
 // one activation scale per 16-token tile and stores its columns side by side.
 //
-// Two products (block_product):
-//   bf16 output     v_mfma_f32_16x16x128_f8f6f4 (the builtin with scale operands
-//                   0 is the form without scales: 2 % faster than unit scales).  The
-//                   instruction cuts the products of 8 neighbouring k to
-//                   multiples of 2^-13 of the largest's power of two before it
-//                   adds them (measured); 1.5e-5 of a normally distributed result,
-//                   against 1.7e-3 for the output's own rounding.
-//   float32 output  codes converted to fp16 (exact), four 16x16x32 fp16
-//                   instructions, exact products and float32 sums.
+// Products are exact and sums float32: the codes become fp16 (exact) and go through
+// four 16x16x32 fp16 instructions a block.  The 8-bit matrix instructions (16x16x128 and
+// 16x16x32 alike) cut the products of 8 neighbouring k to multiples of 2^-13 of the
+// largest's power of two before they add them (measured): a small sum of
+// large products loses up to 2^-10 of their magnitudes, so they are used only where the caller allows it.
 // Which k meets which inside a block is free as long as both operands agree: lane
 // group g = lane / 16 takes the 16-byte pieces g and g + 4 of its row.
 #include <hip/hip_runtime.h>
@@ -50,22 +46,14 @@ struct Frag {
   u32x4 p[2];
 };
 
+// The s-th quarter of a fragment as an operand of the matrix instruction.
+__device__ inline half8 quarter(const Frag& f, int s) { return half_of(f.p[s >> 1][2 * (s & 1)], f.p[s >> 1][2 * (s & 1) + 1]); }
+
 // The 16 x 16 sums over one block of 128.
-template <bool EXACT>
 __device__ inline floatx4 block_product(const Frag& w, const Frag& x) {
   floatx4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (EXACT) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(half_of(w.p[s >> 1][2 * (s & 1)], w.p[s >> 1][2 * (s & 1) + 1]),
-                                                 half_of(x.p[s >> 1][2 * (s & 1)], x.p[s >> 1][2 * (s & 1) + 1]), c, 0, 0, 0);
-  } else {
-    const i32x8 a = {(int)w.p[0][0], (int)w.p[0][1], (int)w.p[0][2], (int)w.p[0][3],
-                     (int)w.p[1][0], (int)w.p[1][1], (int)w.p[1][2], (int)w.p[1][3]};
-    const i32x8 b = {(int)x.p[0][0], (int)x.p[0][1], (int)x.p[0][2], (int)x.p[0][3],
-                     (int)x.p[1][0], (int)x.p[1][1], (int)x.p[1][2], (int)x.p[1][3]};
-    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-  }
+  for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(quarter(w, s), quarter(x, s), c, 0, 0, 0);
   return c;
 }
 
@@ -134,7 +122,7 @@ struct Share {
       : first(steps * g / groups), last(steps * (g + 1) / groups) {}
 };
 
-template <int FN, int FM, int WN, int WM, int D, bool EXACT, int OUT>
+template <int FN, int FM, int WN, int WM, int D, int OUT>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __restrict__ partial) {
   using T = Ring<FN, FM, WN, WM, D>;
@@ -262,7 +250,7 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
     for (int j = 0; j < FM; ++j) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < FN; ++i) t[j & 1][i] = block_product<EXACT>(w[i], x[j]);
+      for (int i = 0; i < FN; ++i) t[j & 1][i] = block_product(w[i], x[j]);
       if (j == 0) {
 #pragma unroll
         for (int i = 0; i < FN; ++i) next_w[i] = frag(nst, (wn * FN + i) * 16 + li);
@@ -347,7 +335,230 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const Fp8GemmArgs p, int 
   if (m < p.M) store4<OUT>(p.out, (int64_t)m * p.ld_out + n, sum, p.N - n, vec);
 }
 
-// Large products.  WN x WM = 4 waves, one per SIMD; a wave owns FN * 16
+// Large products: a workgroup has a whole tile of 256 columns x 224 tokens, 8 waves in 4 x 2, two to a SIMD; a wave owns 64
+// columns x 112 tokens (112 accumulators a lane).  Per block of 128 it reads 4 + 7 fragments of 2 KB from LDS, converts
+// them (176 instructions) and issues 4 * 7 * 4 matrix instructions of 16 cycles and 112 fmas (out += scale * sum).
+//
+// Bound: the matrix unit, the vector instructions beside it and the power limit.  Measured, 8192 x 5120 x 17408: 1175 us,
+// 1.24 PFLOP/s at 1.95 GHz (a library bf16 product reaches 1.27 at 8192^3); with the copies left out 980, the fmas
+// 1078, the conversions 1160, the matrix instructions 789.  The same instructions from registers alone reach 1.7.
+//
+// LDS holds two stages of a block: weight rows, activation rows (128 bytes each),
+// the tile's activation scales; all three come by LDS DMA.  16-byte pieces are
+// XOR-swizzled by the row, in the copies' addresses, so that the reads are free of
+// bank conflicts.  Rows behind the last and pieces behind K lie behind the descriptors'
+// ranges: such lanes write zeros.
+//
+// The weight's fragments stay in registers, as fp16, over a block.  A step (j, n) is two products with one quarter (32 k)
+// of the activation fragment j; beside them stand fmas of the two products before, half a conversion of
+// fragment j + 1 and reads of j + 2, so that no instruction waits for the one before it.  Reads are thus ahead
+// by more than a fragment, and in the middle of the last but one every wave has read all that it needs of the
+// stage.  The one barrier of a block stands there: it frees the stage for the block two on, and certifies the next
+// block's, whose weight fragments replace the present ones beside the last products.  A block's 8 copies a
+// wave are spread over 32 steps: all at once they hold up the instructions behind them (60 tiles of 40 blocks: 118 us, so 105).
+struct Tile {
+  static constexpr int FN = 4, FM = 7, WN = 4, WM = 2;
+  static constexpr int TN = FN * WN * 16, TM = FM * WM * 16;
+  static constexpr int kW = TN * 128, kX = TM * 128, kStage = kW + kX + 1024;
+  // 1 KB copies of every wave; the first four waves bring one more group of activation rows, the others the scales
+  static constexpr int CW = TN / 64, CX = TM / 64;
+  static_assert(TM / 8 % 8 == 4 && TM <= 256, "the copies' shares");
+};
+
+template <int OUT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void fp8_tile_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n) {
+  using T = Tile;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+  const int n0 = tn * T::TN, m0 = tm * T::TM;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave / T::WM, wm = wave % T::WM, li = lane & 15, lg = lane >> 4;
+  const int blocks = (p.K + 127) / 128;
+
+  // copies: lane l brings piece l % 8 (swizzled) of row l / 8 of a group of 8 rows
+  const int ldw = (int)p.w.ld_codes, lda = (int)p.a.ld_codes;
+  const i32x4 rw = buffer_rsrc(p.w.codes + (int64_t)n0 * ldw, (uint32_t)(min(T::TN, p.N - n0) * ldw));
+  const uint8_t* xa = p.a.codes + (int64_t)m0 * lda;
+  const uint32_t x_bytes = (uint32_t)(min(T::TM, p.M - m0) * lda);
+  const float* sa = p.a.scales + (int64_t)min(m0 + max(wave - 4, 0) * 64 + lane, p.M - 1) * p.a.scale_row;
+  constexpr int kNowhere = (int)0x80000000;
+  constexpr int kCopies = T::CW + T::CX + 1;
+  // the c-th copy of a wave's share of block b; behind the last block the last one is copied again, so that the waits need no branches
+  auto copy = [&](int b, int c) __attribute__((always_inline)) {
+    int l = lane;
+    asm volatile("" : "+v"(l));  // the offsets are worked out anew: kept over the loop they would cost registers that it lacks
+    const int q = l >> 3, g = c < T::CW ? wave * T::CW + c : c < T::CW + T::CX ? wave * T::CX + c - T::CW : 8 * T::CX + wave;
+    uint8_t* to = smem + (b & 1) * T::kStage;
+    const int last = min(b, blocks - 1), k = last * 128;
+    if (c < T::CW) {
+      const int piece = ((l & 7) ^ ((q & 3) + 4 * (c & 1))) * 16;  // by the row and the parity of the group of rows
+      llvm_amdgcn_raw_buffer_load_lds(rw, (lds_u32_ptr)(to + g * 1024), 16, k + piece < p.K ? (g * 8 + q) * ldw + piece : kNowhere, k, 0, 0);
+    } else if (c < kCopies - 1 || wave < 4) {
+      const int piece = ((l & 7) ^ q) * 16;
+      llvm_amdgcn_raw_buffer_load_lds(buffer_rsrc(xa + last * p.a.code_block, x_bytes), (lds_u32_ptr)(to + T::kW + g * 1024), 16,
+                                      k + piece < p.K ? (g * 8 + q) * lda + piece : kNowhere, 0, 0, 0);
+    } else {
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(sa + (int64_t)last * p.a.scale_block),
+                                       (lds_u32_ptr)(to + T::kW + T::kX + (wave - 4) * 256), 4, 0, 0);
+    }
+  };
+  // a wave whose columns all lie behind the last takes the last block's scales
+  const auto* sw = (const __attribute__((address_space(4))) float*)(p.w.scales + (int64_t)(min(n0 + wn * 64, p.N - 1) / 128) * p.w.scale_row);
+
+  // fragments: weight row (i, a = lane % 16) is column (i / 2) * 32 + (a / 4) * 8 + (i % 2) * 4 + a % 4 of the wave, so that a
+  // lane's results of fragments 2 i and 2 i + 1 are 8 neighbouring columns
+  const int wbase = (wn * 64 + (li >> 2) * 8 + (li & 3)) * 128, xbase = T::kW + (wm * T::FM * 16 + li) * 128;
+  const int sbase = T::kW + T::kX + (wm * T::FM * 16 + li) * 4;
+  int piece[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) piece[h] = ((lg + 4 * h) ^ (li & 7)) << 4;
+  // half h of a fragment: the operands of quarters 2 h and 2 h + 1
+  auto read_w = [&](const uint8_t* st, int i, int h) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(st + wbase + piece[h] + (i >> 1) * 4096 + (i & 1) * 512);
+  };
+  auto read_x = [&](const uint8_t* st, int j, int h) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(st + xbase + piece[h] + j * 2048);
+  };
+  auto read_s = [&](const uint8_t* st, int j) __attribute__((always_inline)) { return *reinterpret_cast<const float*>(st + sbase + j * 64); };
+  auto quarter = [&](const u32x4& half, int s) __attribute__((always_inline)) { return half_of(half[2 * (s & 1)], half[2 * (s & 1) + 1]); };
+
+#pragma unroll
+  for (int c = 0; c < kCopies; ++c) copy(0, c);
+#pragma unroll
+  for (int c = 0; c < 3; ++c) copy(1, c);
+  wait_vmem<3>();
+  barrier_lds();
+  floatx4 acc[T::FN][T::FM], t[2][2];
+  half8 hw[T::FN][4], hx[4];
+#pragma unroll
+  for (int i = 0; i < T::FN; ++i) {
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) hw[i][s] = quarter(read_w(smem, i, s >> 1), s);
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) hx[s] = quarter(read_x(smem, 0, s >> 1), s);
+  t[1][0] = t[1][1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 x[2] = {read_x(smem, 1, 0), read_x(smem, 1, 1)};  // of the fragment after hx
+  float sx = read_s(smem, 0), sc = 0.0f, s_now = sw[0];   // sc: the scale of the sums in t
+  for (int b = 0; b < blocks; ++b) {
+    const uint8_t* st = smem + (b & 1) * T::kStage;
+    const uint8_t* nst = smem + ((b + 1) & 1) * T::kStage;
+    const float s_next = sw[min(b + 1, blocks - 1) * p.w.scale_block];
+    u32x4 w[2];
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) {
+      half8 next[4];
+      const float s_prev = sc;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {  // products of fragments 2 P and 2 P + 1 with quarter s
+        const int P = n >> 2, s = n & 3, i = 2 * P;
+        __builtin_amdgcn_sched_barrier(0);
+        if (j == T::FM - 2 && n == 4) {
+          wait_vmem<0>();
+          barrier_lds();
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // the barrier's lgkmcnt(0) again, seen by the compiler's own wait insertion
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          t[P][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hw[i + u][s], hx[s], s == 0 ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : t[P][u], 0, 0, 0);
+        // the two fragments before
+        const int jp = P == 1 ? j : j == 0 ? T::FM - 1 : j - 1, ip = P == 1 ? 0 : 2;
+        if (s > 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e * 3 / 8 == s - 1) acc[ip + (e >> 2)][jp][e & 3] = fmaf(t[1 - P][e >> 2][e & 3], P == 1 ? sc : s_prev, acc[ip + (e >> 2)][jp][e & 3]);
+          if (s == 3) asm volatile("" : "+v"(acc[ip][jp]), "+v"(acc[ip + 1][jp]));  // here, not where the compiler would sink them to
+        }
+        // half a quarter of the next fragment
+        {
+          const uint32_t c = x[n >> 2][n & 3];
+          const half2v lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false), hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, true);
+          const int e = (n & 1) * 4;
+          next[n >> 1][e] = lo[0];
+          next[n >> 1][e + 1] = lo[1];
+          next[n >> 1][e + 2] = hi[0];
+          next[n >> 1][e + 3] = hi[1];
+        }
+        // the copies, one in four steps: the freed stage's first three, then the other stage's remaining five
+        if (j == T::FM - 2 && n == 5) copy(b + 2, 0);
+        if (j == T::FM - 1 && (n == 1 || n == 5)) copy(b + 2, n == 1 ? 1 : 2);
+        if (j < 3 && (n == 1 || n == 5) && 2 * j + n / 5 < 5) copy(b + 1, 3 + 2 * j + n / 5);
+        if (n == 0) {
+          sc = sx * s_now;
+          sx = j < T::FM - 1 ? read_s(st, j + 1) : read_s(nst, 0);
+        }
+        if (n == 4) x[0] = j < T::FM - 2 ? read_x(st, j + 2, 0) : read_x(nst, j + 2 - T::FM, 0);
+        if (n == 7) x[1] = j < T::FM - 2 ? read_x(st, j + 2, 1) : read_x(nst, j + 2 - T::FM, 1);
+        if (j == T::FM - 2 && n == 7) w[0] = read_w(nst, 0, 0), w[1] = read_w(nst, 1, 0);
+        if (j == T::FM - 1) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) hw[i + u][s] = quarter(w[u], s);
+          if ((s & 1) && n < 7) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) w[u] = read_w(nst, n == 3 ? 2 + u : i + u, n == 3 ? 0 : 1);
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) hx[s] = next[s];
+    }
+    s_now = s_next;
+  }
+  wait_vmem<0>();  // no copy may land after the workgroup's LDS is given away
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[2 + u][T::FM - 1][r] = fmaf(t[1][u][r], sc, acc[2 + u][T::FM - 1][r]);
+
+  const bool vec = p.ld_out % 8 == 0 && (uintptr_t)p.out % 16 == 0;
+#pragma unroll
+  for (int j = 0; j < T::FM; ++j) {
+    const int m = m0 + (wm * T::FM + j) * 16 + li;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int i = 0; i < T::FN; i += 2) {
+      const int n = n0 + wn * 64 + (i / 2) * 32 + lg * 8;
+      const floatx4 u = acc[i][j], v = acc[i + 1][j];
+      if constexpr (OUT == NVFP4_DTYPE_BF16) {
+        uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + (int64_t)m * p.ld_out + n;
+        if (vec && n + 8 <= p.N) {
+          store_stream16(o, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          continue;
+        }
+      }
+      store4<OUT>(p.out, (int64_t)m * p.ld_out + n, u, p.N - n, vec);
+      store4<OUT>(p.out, (int64_t)m * p.ld_out + n + 4, v, p.N - n - 4, vec);
+    }
+  }
+}
+
+template <int OUT>
+hipError_t launch_tiles(const Fp8GemmArgs& g, hipStream_t s) {
+  using T = Tile;
+  const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (g.N + T::TN - 1) / T::TN;
+  const auto fn = fp8_tile_kernel<OUT>;
+  const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * T::kStage);
+  if (e != hipSuccess) return e;
+  fn<<<(unsigned)tiles_m * (unsigned)tiles_n, 512, 2 * T::kStage, s>>>(g, tiles_m, tiles_n);
+  return hipGetLastError();
+}
+
+// Large products whose caller allows the 8-bit matrix instruction (the builtin with scale operands 0 is the form without
+// scales: 2 % faster than unit scales).
+__device__ inline floatx4 product_8bit(const Frag& w, const Frag& x) {
+  const i32x8 a = {(int)w.p[0][0], (int)w.p[0][1], (int)w.p[0][2], (int)w.p[0][3],
+                   (int)w.p[1][0], (int)w.p[1][1], (int)w.p[1][2], (int)w.p[1][3]};
+  const i32x8 b = {(int)x.p[0][0], (int)x.p[0][1], (int)x.p[0][2], (int)x.p[0][3],
+                   (int)x.p[1][0], (int)x.p[1][1], (int)x.p[1][2], (int)x.p[1][3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
+// WN x WM = 4 waves, one per SIMD; a wave owns FN * 16
 // columns x FM * 16 tokens (256 x 224 tiles: 128 x 112, 224 accumulators a
 // lane).  Per block of 128 a wave reads FN + FM fragments of 2 KB from LDS for FN * FM
 // matrix instructions of 32 cycles; each instruction's four fmas (out += scale *
@@ -389,12 +600,12 @@ struct Pipe {
 
 template <int FN, int FM, int WN, int WM>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
+void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n) {
   using T = Pipe<FN, FM, WN, WM>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   int tm, tn;
   tile_of(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-  const int n0 = n_lo + tn * T::TN, m0 = tm * T::TM;
+  const int n0 = tn * T::TN, m0 = tm * T::TM;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / WM, wm = wave % WM, li = lane & 15, lg = lane >> 4;
   const int blocks = (p.K + 127) / 128;
@@ -508,7 +719,7 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
         __builtin_amdgcn_sched_barrier(0);
         const int n = t * FN + i;
         if (i == 1) x[(t + 1) & 1] = t < FM - 1 ? read_x(st, t + 1) : read_x(nst, 0);
-        tmp[n % (kLag + 1)] = block_product<false>(w[i], x[t & 1]);
+        tmp[n % (kLag + 1)] = product_8bit(w[i], x[t & 1]);
         if (n >= kLag) add(n - kLag);
         // the next block's scales: early enough that nothing waits for them
         if (t == 1 && i == 2) next_sw = sw[min(b + 1, blocks - 1) * p.w.scale_block];
@@ -568,19 +779,17 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, int n_lo) {
 }
 
 template <int FN, int FM, int WN, int WM>
-hipError_t launch_pipe(const Fp8GemmArgs& g, int n_lo, int n_hi, hipStream_t s) {
+hipError_t launch_pipe(const Fp8GemmArgs& g, hipStream_t s) {
   using T = Pipe<FN, FM, WN, WM>;
-  Fp8GemmArgs h = g;
-  h.N = n_hi;
-  const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (n_hi - n_lo + T::TN - 1) / T::TN;
+  const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (g.N + T::TN - 1) / T::TN;
   const auto fn = fp8_pipe_kernel<FN, FM, WN, WM>;
   const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * T::kStage);
   if (e != hipSuccess) return e;
-  fn<<<(unsigned)tiles_m * (unsigned)tiles_n, 256, 2 * T::kStage, s>>>(h, tiles_m, tiles_n, n_lo);
+  fn<<<(unsigned)tiles_m * (unsigned)tiles_n, 256, 2 * T::kStage, s>>>(g, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
-template <int FN, int FM, int WN, int WM, int D, bool EXACT, int OUT>
+template <int FN, int FM, int WN, int WM, int D, int OUT>
 hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
   using T = Ring<FN, FM, WN, WM, D>;
   static_assert(T::TN * T::TM <= 128 * 224, "a partial tile's room in the workspace");
@@ -591,7 +800,7 @@ hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
   // 200 x 1024 x 5120 24.0, 20.3, 16.8, 17.8; 77 x 1000 x 2064 float32 12.7, 11.1, 11.8, 15.5.
   const int64_t want = tiles > steps / 4 ? tiles : steps / 4;
   const int groups = (int)(want < kRingGroups ? want : kRingGroups);
-  const auto fn = fp8_ring_kernel<FN, FM, WN, WM, D, EXACT, OUT>;
+  const auto fn = fp8_ring_kernel<FN, FM, WN, WM, D, OUT>;
   hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, D * T::kStage);
   if (e != hipSuccess) return e;
   fn<<<groups, 512, D * T::kStage, s>>>(g, tiles_m, tiles_n, ws);
@@ -602,8 +811,8 @@ hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
 
 template <int FN, int FM, int WN, int WM, int D>
 hipError_t launch_ring(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
-  return g.out_dtype == NVFP4_DTYPE_BF16 ? launch_ring_as<FN, FM, WN, WM, D, false, NVFP4_DTYPE_BF16>(g, ws, s)
-                                         : launch_ring_as<FN, FM, WN, WM, D, true, NVFP4_DTYPE_F32>(g, ws, s);
+  return g.out_dtype == NVFP4_DTYPE_BF16 ? launch_ring_as<FN, FM, WN, WM, D, NVFP4_DTYPE_BF16>(g, ws, s)
+                                         : launch_ring_as<FN, FM, WN, WM, D, NVFP4_DTYPE_F32>(g, ws, s);
 }
 
 // Tokens of the ring kernel's tiles.
@@ -623,19 +832,29 @@ size_t fp8_gemm_workspace(int64_t m) {
   return (size_t)kRingGroups * 2 * 128 * tm * sizeof(float);
 }
 
-// In steps (a block of a tile, about 1.5 us either way) of the busiest workgroup: whole waves of 256 x 224 tiles against
-// an even share of 128 x 224 tiles, whose partial sums and join cost as much as 9 steps.  Measured, us, shared | whole tiles:
-// 224 x 34816 x 5120 97 | 76; 300 x 5120 x 5120 36 | 60; 448 x 5120 x 17408 73 | 188; 672 x 5120 x 5120 45 | 61; 1024 x 5120 x
-// 5120 62 | 61; 1024 x 34816 x 5120 323 | 221.
-bool fp8_gemm_shares(const Fp8GemmArgs& g) {
-  if (g.out_dtype != NVFP4_DTYPE_BF16 || g.M <= 128) return true;
+// By the steps (a block of a tile) of the busiest workgroup: 2 us each for an even share of 128 x 224 tiles, whose partial
+// sums and join cost 10 more, against whole 256 x 224 tiles with 2.6 to 2.9 us a step, or 1.55 with the 8-bit instruction.
+// Measured, us, shared | whole | whole with the 8-bit instruction: 224 x 34816 x 5120 108 | 126 | 76; 512 x 5120 x 5120 51 | 105
+// | -; 448 x 5120 x 17408 95 | 370 | 188; 1024 x 5120 x 5120 78 | 108 | 61; 1024 x 34816 x 5120 432 | 344 | 214; 2048 x 5120 x
+// 17408 400 | 349 | 205; 8192 x 5120 x 17408 1467 | 1175 | 640-668.
+namespace {
+enum class Form { kRing, kTile, kPipe };
+Form form_of(const Fp8GemmArgs& g) {
+  if (g.M <= 128) return Form::kRing;
   const int64_t blocks = (g.K + 127) / 128, tiles_m = (g.M + 223) / 224;
-  const int64_t waves = (tiles_m * ((g.N + 255) / 256) + 255) / 256;
-  return waves * blocks > tiles_m * ((g.N + 127) / 128) * blocks / kRingGroups + 9;
+  const int64_t whole = (tiles_m * ((g.N + 255) / 256) + 255) / 256 * blocks;
+  const int64_t shared = tiles_m * ((g.N + 127) / 128) * blocks / kRingGroups;
+  if (g.cut_sums && whole * 3 <= shared * 4 + 20) return Form::kPipe;
+  return whole * 3 <= shared * 2 + 10 ? Form::kTile : Form::kRing;
 }
+}  // namespace
+
+bool fp8_gemm_shares(const Fp8GemmArgs& g) { return form_of(g) != Form::kPipe; }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
-  if (!fp8_gemm_shares(g)) return launch_pipe<8, 7, 2, 2>(g, 0, g.N, s);
+  const Form form = form_of(g);
+  if (form == Form::kPipe) return launch_pipe<8, 7, 2, 2>(g, s);
+  if (form == Form::kTile) return g.out_dtype == NVFP4_DTYPE_BF16 ? launch_tiles<NVFP4_DTYPE_BF16>(g, s) : launch_tiles<NVFP4_DTYPE_F32>(g, s);
   switch (ring_tokens(g.M)) {
     case 16: return launch_ring<1, 1, 8, 1, 8>(g, ws, s);
     case 32: return launch_ring<1, 2, 8, 1, 7>(g, ws, s);

@@ -57,12 +57,15 @@ int check_fp8(const nvfp4_fp8_tensor* t, Fp8Mat& out) {
 
 // The sizes and the output of a product (a's and w's matrices already checked).
 int check_product(int64_t m, int64_t n, int64_t k, void* out, int out_dtype, int64_t ld_out, Fp8GemmArgs& g) {
+  g.cut_sums = (out_dtype & NVFP4_FP8_CUT_SUMS) != 0;
+  out_dtype &= ~NVFP4_FP8_CUT_SUMS;
   const int esz = elem_size(out_dtype);
   if (esz == 0) return NVFP4_ERR_DTYPE;
+  if (g.cut_sums && out_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_FLAGS;
   if (n <= 0) return NVFP4_ERR_SHAPE;
   if (ld_out < n) return NVFP4_ERR_STRIDE;
   if (ld_out >= kIndexLimit || m >= kSizeLimit / ld_out) return NVFP4_ERR_RANGE;
-  // every tile is larger (16 to 224 tokens x 128 columns, 256 x 224): grids stay below 2^32 threads, and a tile's last row and
+  // every tile is larger (16 to 224 tokens x 128 columns, 224 x 256): grids stay below 2^32 threads, and a tile's last row and
   // column inside 32 bits
   if ((m <= 64 ? (n + 31) / 32 : (n + 63) / 64 * ((m + 63) / 64)) >= kGridLimit) return NVFP4_ERR_RANGE;
   if (m == 0) return NVFP4_OK;
@@ -77,9 +80,9 @@ int check_product(int64_t m, int64_t n, int64_t k, void* out, int out_dtype, int
   return NVFP4_OK;
 }
 
-// The workspace of nvfp4_fp8_linear: the product's, then codes, then scales [pieces, rows].  Codes as [pieces, rows, 128]
-// where the product is shared out in small steps, so that what a step reads lies together (64 x 34816 x 5120 47 -> 42.5 us,
-// 200 x 5120 x 17408 54 -> 53), else as [rows, 128 pieces] (8192 x 5120 x 17408: 715 us so, 722 the other way).
+// The workspace of nvfp4_fp8_linear: the product's, then codes, then scales [pieces, rows].  Codes as [pieces, rows, 128],
+// so that what a step reads lies together (with the 8-bit instruction 64 x 34816 x 5120 took 47 us instead of 42.5 the other
+// way), or as [rows, 128 pieces] where the product needs that.
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 int check_heads(const nvfp4_head_rows* r, int64_t tokens, int head_dim, int esz) {

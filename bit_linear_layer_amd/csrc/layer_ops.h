@@ -29,9 +29,10 @@ struct Fp8GemmArgs {
   int64_t ld_out;
   int out_dtype;
   int M, N, K;
+  bool cut_sums;  // the 8-bit matrix instructions are allowed
 };
 size_t fp8_gemm_workspace(int64_t m);  // bytes for products of up to 2^31 columns with m tokens
-// Whether the product is shared out in small steps; then a.code_block may be any, else it is 128.
+// Whether the product reads a's blocks wherever they lie; else a.code_block has to be 128.
 bool fp8_gemm_shares(const Fp8GemmArgs& g);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, float* ws, hipStream_t s);
 

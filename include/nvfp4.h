@@ -580,6 +580,17 @@ enum {
 };
 
 /*
+ * May be ORed into out_dtype (bf16 only) of nvfp4_fp8_gemm and nvfp4_fp8_linear:
+ * products large enough for it use the 8-bit matrix instructions, at up to 1.8
+ * times the speed.  These cut the products of 8 neighbouring k to multiples of
+ * 2^-13 of the largest's power of two before they add them: an error of up to
+ * 2^-10 of the sum of their magnitudes, 1.5e-5 of the result on normally
+ * distributed data (bf16's own rounding is 1.7e-3), but more of a result
+ * that is small because large products cancel.
+ */
+enum { NVFP4_FP8_CUT_SUMS = 0x100 };
+
+/*
  * nvfp4_fp8_quantize -- x [q->rows, q->cols] (bf16 or float32, row stride ld_x
  * elements, rows 16-byte aligned) into q, whose codes and scales are written.
  * Bit for bit: amax = the largest magnitude among the block's finite
@@ -603,14 +614,11 @@ size_t nvfp4_fp8_gemm_workspace_bytes(int64_t rows);
  *   out   DEVICE [M, ld_out] of out_dtype (bf16: round to nearest even),
  *         ld_out >= N elements, below 2^31; M * ld_out < 2^40.
  * N < 2^29 - 31 for M <= 64, above that ceil(N / 64) * ceil(M / 64) < 2^24.
- * Sums over a block and over blocks are float32.  With out_dtype F32 the
- * products are exact (codes as fp16 on the matrix unit) and the result is within
- * (K / 128 + 136) 2^-23 sum |a w| of the exact one.  With BF16 the 8-bit matrix
- * instructions are used, which cut the products of 8 neighbouring k to
- * multiples of 2^-13 of the largest's power of two before they add them: up
- * to 2^-10 of the sum of their magnitudes more, 1.5e-5 of the result on normally
- * distributed data, where bf16's own rounding is 1.7e-3.  A NaN code reaches
- * its row (a) or column (w) only.
+ * Products are exact (codes as fp16 on the matrix unit), sums over a block and
+ * over blocks are float32, and the result is rounded once: within
+ * (K / 128 + 136) 2^-23 sum |a w| of the exact one before that rounding, unless
+ * the caller allows less (NVFP4_FP8_CUT_SUMS).  A NaN code reaches its row (a)
+ * or column (w) only.
  * The product of two scales is a float32: below 2^-126 it loses bits.
  *   workspace DEVICE, >= nvfp4_fp8_gemm_workspace_bytes(M) bytes, 16-byte
  *             aligned, contents arbitrary; calls that may overlap in time need
