@@ -57,6 +57,58 @@ __device__ inline floatx4 block_product(const Frag& w, const Frag& x) {
   return c;
 }
 
+// Where the product of two scales is beyond float32's range, sums that are not large still are not: 0 gives 0, and 2^-18
+// times 2^140 gives 2^122.  Such a product leaves an infinity or NaN in the sums, so that the loops over blocks need not
+// look for it; a wave that finds one in its sums over blocks [b0, b1) works out anew, from memory, the tokens with such scales.
+// Both scales are at least 1 there, so that 2^-64 of each is exact.
+// m: the wave's first token; w_row(i): the lane's row of weight fragment i; n: one of the wave's columns.
+template <int FN, int FM, typename Rows>
+__device__ inline void mend_large_scales(const Fp8GemmArgs& p, floatx4 (&acc)[FN][FM], int b0, int b1, int m, int n, Rows w_row) {
+  float any = 0.0f;
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) any = fmaf(acc[i][j][r], 0.0f, any);
+  if (__ballot(any != 0.0f) == 0) return;  // NaN
+  const int li = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
+  const float* sw = p.w.scales + (int64_t)(min(n, p.N - 1) / 128) * p.w.scale_row;
+  auto load = [&](const Fp8Mat& q, int row, int b) {
+    Frag f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = (lg + 4 * h) * 16;
+      f.p[h] = u32x4{0u, 0u, 0u, 0u};
+      if (b * 128 + at < p.K) f.p[h] = *reinterpret_cast<const u32x4*>(q.codes + (int64_t)row * q.ld_codes + b * q.code_block + at);
+    }
+    return f;
+  };
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int row = min(m + j * 16 + li, p.M - 1);
+    const float* sx = p.a.scales + (int64_t)row * p.a.scale_row;
+    bool mine = false;
+    for (int b = b0; b < b1; ++b) mine = mine || __builtin_isinf(sx[b * p.a.scale_block] * sw[b * p.w.scale_block]);
+    if (__ballot(mine) == 0) continue;
+    floatx4 sum[FN] = {};
+    for (int b = b0; b < b1; ++b) {
+      const float u = sx[b * p.a.scale_block], v = sw[b * p.w.scale_block], s = u * v;
+      const bool inf = __builtin_isinf(s);
+      const float sc = inf ? (u * 0x1p-64f) * (v * 0x1p-64f) : s, up = inf ? 0x1p64f : 1.0f;
+      const Frag x = load(p.a, row, b);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const floatx4 t = block_product(load(p.w, min(w_row(i), p.N - 1), b), x);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[i][r] = fmaf(t[r] * sc * up, up, sum[i][r]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[i][j] = mine ? sum[i] : acc[i][j];
+  }
+}
+
 // Four consecutive columns of one row; vec: the row's address allows one store.
 template <int OUT>
 __device__ inline void store4(void* out, int64_t at, const floatx4& v, int left, bool vec) {
@@ -268,6 +320,7 @@ void fp8_ring_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n, float* __res
     ++block;
     const bool ends = block == blocks || step + 1 == steps;
     if (ends) {
+      mend_large_scales(p, acc, begun, block, m0 + wm * FM * 16, n0, [&](int i) { return n0 + (wn * FN + i) * 16 + li; });
       if (block == blocks && begun == 0) {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
@@ -514,6 +567,8 @@ void fp8_tile_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n) {
   for (int u = 0; u < 2; ++u)
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[2 + u][T::FM - 1][r] = fmaf(t[1][u][r], sc, acc[2 + u][T::FM - 1][r]);
+  mend_large_scales(p, acc, 0, blocks, m0 + wm * T::FM * 16, n0 + wn * 64,
+                    [&](int i) { return n0 + wn * 64 + (i >> 1) * 32 + (li >> 2) * 8 + (i & 1) * 4 + (li & 3); });
 
   const bool vec = p.ld_out % 8 == 0 && (uintptr_t)p.out % 16 == 0;
 #pragma unroll
@@ -755,6 +810,8 @@ void fp8_pipe_kernel(const Fp8GemmArgs p, int tiles_m, int tiles_n) {
     if constexpr (FM % 2 == 1) x[0] = x[1];
   }
   wait_vmem<0>();  // no copy may land after the workgroup's LDS is given away
+  mend_large_scales(p, acc, 0, blocks, m0 + wm * FM * 16, n0 + wn * FN * 16,
+                    [&](int i) { return n0 + wn * FN * 16 + (i >> 1) * 32 + (li >> 2) * 8 + (i & 1) * 4 + (li & 3); });
 
   const bool vec = p.ld_out % 8 == 0 && (uintptr_t)p.out % 16 == 0;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out);

@@ -619,7 +619,8 @@ size_t nvfp4_fp8_gemm_workspace_bytes(int64_t rows);
  * (K / 128 + 136) 2^-23 sum |a w| of the exact one before that rounding, unless
  * the caller allows less (NVFP4_FP8_CUT_SUMS).  A NaN code reaches its row (a)
  * or column (w) only.
- * The product of two scales is a float32: below 2^-126 it loses bits.
+ * The product of two scales is a float32: below 2^-126 it loses bits.  Beyond
+ * float32's range it counts as it is: a block whose sum is 0 adds 0.
  *   workspace DEVICE, >= nvfp4_fp8_gemm_workspace_bytes(M) bytes, 16-byte
  *             aligned, contents arbitrary; calls that may overlap in time need
  *             one each.
