@@ -88,19 +88,21 @@ int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 int check_heads(const nvfp4_head_rows* r, int64_t tokens, int head_dim, int esz) {
   if (r->heads < 1 || r->heads > 4096) return NVFP4_ERR_SHAPE;
   const int64_t unit = 16 / esz, most = kIndexLimit;
-  const int64_t lds[2] = {r->ld_x, r->ld_out}, hds[2] = {r->head_x, r->head_out};
+  // a stride that is not used counts as 0
+  const bool rows = tokens > 1, several = r->heads > 1;
+  const int64_t lds[2] = {rows ? r->ld_x : 0, rows ? r->ld_out : 0}, hds[2] = {several ? r->head_x : 0, several ? r->head_out : 0};
   for (int i = 0; i < 2; ++i) {
     if (lds[i] < 0 || hds[i] < 0 || lds[i] % unit != 0 || hds[i] % unit != 0) return NVFP4_ERR_STRIDE;
     if (lds[i] >= most || hds[i] >= most) return NVFP4_ERR_RANGE;
     // no two (token, head) places may overlap: the heads of a token lie together, or the tokens of a head do
-    const bool by_token = (r->heads == 1 || hds[i] >= head_dim) && (tokens <= 1 || lds[i] >= (r->heads - 1) * hds[i] + head_dim);
-    const bool by_head = (tokens <= 1 || lds[i] >= head_dim) && (r->heads == 1 || hds[i] >= (tokens - 1) * lds[i] + head_dim);
+    const bool by_token = (!several || hds[i] >= head_dim) && (!rows || lds[i] >= (r->heads - 1) * hds[i] + head_dim);
+    const bool by_head = (!rows || lds[i] >= head_dim) && (!several || hds[i] >= (tokens - 1) * lds[i] + head_dim);
     if (!by_token && !by_head) return NVFP4_ERR_STRIDE;
   }
   if (tokens == 0) return NVFP4_OK;
   if (r->x == nullptr || r->out == nullptr) return NVFP4_ERR_NULL;
   // in place every element is read by the thread that writes it
-  if (r->x == r->out && ((tokens > 1 && r->ld_x != r->ld_out) || (r->heads > 1 && r->head_x != r->head_out))) return NVFP4_ERR_STRIDE;
+  if (r->x == r->out && (lds[0] != lds[1] || hds[0] != hds[1])) return NVFP4_ERR_STRIDE;
   if (!aligned(r->x, 16) || !aligned(r->out, 16) || !aligned(r->weight, 4)) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
 }
