@@ -368,10 +368,10 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const Fp8GemmArgs p, int 
   if (g0 == g1) return;  // stored as it was finished
   const int e = blockIdx.y * 256 + threadIdx.x;
   if (e >= T::TN * T::TM / 4) return;
-  // only the tile's first workgroup may have begun it
+  // g0 began the tile (its second slot), the others came to it from its middle (their first)
   const floatx4* at = reinterpret_cast<const floatx4*>(partial) + e;
   constexpr int kSlot = T::TN * T::TM / 4, kAhead = 4;
-  floatx4 sum = at[((int64_t)g0 * 2 + (Share(steps, groups, g0).first <= lo)) * kSlot];
+  floatx4 sum = at[((int64_t)g0 * 2 + 1) * kSlot];
   int g = g0 + 1;
   for (; g + kAhead <= g1 + 1; g += kAhead) {
     floatx4 v[kAhead];
@@ -861,7 +861,7 @@ hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
   hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, D * T::kStage);
   if (e != hipSuccess) return e;
   fn<<<groups, 512, D * T::kStage, s>>>(g, tiles_m, tiles_n, ws);
-  if ((e = hipGetLastError()) != hipSuccess || tiles % groups == 0) return e;  // whole tiles each: nothing to join
+  if ((e = hipGetLastError()) != hipSuccess || blocks == 1 || tiles % groups == 0) return e;  // whole tiles each: nothing to join
   fp8_join_kernel<FN, FM, WN, WM, D, OUT><<<dim3((unsigned)tiles, (T::TN * T::TM / 4 + 255) / 256), 256, 0, s>>>(g, tiles_m, groups, steps, ws);
   return hipGetLastError();
 }
