@@ -872,25 +872,27 @@ hipError_t launch_ring(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
                                          : launch_ring_as<FN, FM, WN, WM, D, NVFP4_DTYPE_F32>(g, ws, s);
 }
 
-// Tokens of the ring kernel's tiles.
+// Tokens of the ring kernel's tiles.  Above 128 by the tiles' number and the time of a step, 1.3 us for 128 tokens and 2.1 for 224.
+// Measured, us, 128 | 224: 200 x 5120 x 17408 62 | 57; 256 x 5120 x 17408 64 | 90; 384 x 5120 x 17408 91 | 96; 448 x 5120 x
+// 17408 112 | 97; 512 x 5120 x 17408 114 | 133; 224 x 5120 x 5120 28 | 30; 512 x 5120 x 5120 46 | 53; 640 x 5120 x 5120 53 | 55.
 int ring_tokens(int64_t m) {
   if (m <= 16) return 16;
   if (m <= 32) return 32;
   if (m <= 64) return 64;
   if (m <= 128) return 128;
-  return 224;
+  return (m + 127) / 128 * 5 < (m + 223) / 224 * 8 ? 128 : 224;
 }
 
 }  // namespace
 
 // Two partial tiles of each workgroup.  More tokens never need less, so that one workspace serves smaller calls too.
 size_t fp8_gemm_workspace(int64_t m) {
-  const int tm = ring_tokens(m);
+  const int tm = m <= 128 ? ring_tokens(m) : 224;
   return (size_t)kRingGroups * 2 * 128 * tm * sizeof(float);
 }
 
-// By the steps (a block of a tile) of the busiest workgroup: 2 us each for an even share of 128 x 224 tiles, whose partial
-// sums and join cost 10 more, against whole 256 x 224 tiles with 2.6 to 2.9 us a step, or 1.55 with the 8-bit instruction.
+// By the steps (a block of a tile) of the busiest workgroup: 1.3 or 2.1 us each for an even share of 128 x 128 or 128 x 224 tiles,
+// whose partial sums and join cost 10 more, against whole 256 x 224 tiles with 2.6 to 2.9 us a step, or 1.55 with the 8-bit instruction.
 // Measured, us, shared | whole | whole with the 8-bit instruction: 224 x 34816 x 5120 108 | 126 | 76; 512 x 5120 x 5120 51 | 105
 // | -; 448 x 5120 x 17408 95 | 370 | 188; 1024 x 5120 x 5120 78 | 108 | 61; 1024 x 34816 x 5120 432 | 344 | 214; 2048 x 5120 x
 // 17408 400 | 349 | 205; 8192 x 5120 x 17408 1467 | 1175 | 640-668.
@@ -898,11 +900,11 @@ namespace {
 enum class Form { kRing, kTile, kPipe };
 Form form_of(const Fp8GemmArgs& g) {
   if (g.M <= 128) return Form::kRing;
-  const int64_t blocks = (g.K + 127) / 128, tiles_m = (g.M + 223) / 224;
-  const int64_t whole = (tiles_m * ((g.N + 255) / 256) + 255) / 256 * blocks;
-  const int64_t shared = tiles_m * ((g.N + 127) / 128) * blocks / kRingGroups;
-  if (g.cut_sums && whole * 3 <= shared * 4 + 20) return Form::kPipe;
-  return whole * 3 <= shared * 2 + 10 ? Form::kTile : Form::kRing;
+  const int64_t blocks = (g.K + 127) / 128, tm = ring_tokens(g.M);
+  const int64_t whole = ((g.M + 223) / 224 * (((int64_t)g.N + 255) / 256) + 255) / 256 * blocks;
+  const int64_t shared = (g.M + tm - 1) / tm * (((int64_t)g.N + 127) / 128) * blocks / kRingGroups * (tm == 128 ? 5 : 8) + 40;
+  if (g.cut_sums && whole * 6 <= shared) return Form::kPipe;
+  return whole * 12 <= shared ? Form::kTile : Form::kRing;
 }
 }  // namespace
 
