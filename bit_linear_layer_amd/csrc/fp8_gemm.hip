@@ -1,7 +1,7 @@
 // Matrix product of E4M3 operands with a float32 scale per block of 128 columns
 // (activations: per row, weights: per 128 rows):
 //     out[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in b} a[m, k] w[n, k].
-// One block of 128 is the depth of one 16x16x128 matrix instruction, so a tile's
+// One block of 128 is the depth of four 16x16x32 matrix instructions, so a tile's
 // sum over a block comes out of the matrix unit by itself and enters the
 // running sum with one fma per output: out += (sa sw) tmp.
 //
@@ -134,9 +134,10 @@ __device__ inline void store4(void* out, int64_t at, const floatx4& v, int left,
 }
 
 // Products with few tokens, or of too few tiles to fill the chip: bound by the
-// weight's bytes up to about 64 tokens, beyond by the copies into LDS.  Measured, with the join: 3 x 34816 x 5120 36 us
-// (5.0 TB/s), 16 x 5120 x 17408 25, 64 x 34816 x 5120 51, 200 x 5120 x 17408 48 -- the copies alone take 34, the
-// products alone 36, the join 9.  Tiles of 64 columns at 224 tokens: 53 instead of 41 before the join.  256 workgroups of 8 waves, one per CU, share the
+// weight's bytes up to about 32 tokens, beyond by the copies into LDS and the conversions and products, in nearly equal
+// parts.  Measured, us, with the join | without the copies | without the products: 3 x 34816 x 5120 38 | 28 | 37; 16 x 5120 x
+// 17408 24 | 20 | 24; 32 x 34816 x 5120 44 | 36 | 43; 64 x 34816 x 5120 58 | 47 | 54; 128 x 34816 x 5120 74 | 63 | 68; 200 x 5120 x
+// 17408 57 | 51 | 47, the join 7.5 of them; 256 x 5120 x 17408 64 | 56 | 50.  256 workgroups of 8 waves, one per CU, share the
 // line of all (tile, block of 128) steps evenly, tile by tile; a workgroup's copies
 // run D steps ahead of its products, across the ends of tiles, so that the
 // stream from memory never drains.  A tile whose steps lie in one workgroup is stored; of one that a
@@ -157,8 +158,8 @@ struct Ring {
   static constexpr int CW = TN / 64, CX = TM / 64;           // copies of every wave
   static constexpr int XR = TM / 8 % 8;                      // waves that copy one more group of activation rows
   static constexpr int kBase = CW + CX;
-  // Non-temporal weights.  Measured, us, without | with: 3 x 34816 x 5120 42.3 | 37.8, 16 x 5120 x 17408 26.2 | 25.6, 32 x 34816 x
-  // 5120 47.4 | 46.3, 64 x 34816 x 5120 55.6 | 59.8, 128 x 34816 x 5120 69.3 | 73.1, 200 x 5120 x 17408 47.0 | 50.4.
+  // Non-temporal weights.  Measured, us, without | with: 3 x 34816 x 5120 43.2 | 38.2, 16 x 5120 x 17408 26.4 | 24.9, 32 x 34816 x
+  // 5120 48.7 | 43.6, 64 x 34816 x 5120 58.0 | 59.2, 128 x 34816 x 5120 74.8 | 76.0, 200 x 5120 x 17408 56.6 | 59.2.
   static constexpr int kHint = TM <= 32 ? 2 : 0;
   static constexpr int kStage = kW + kX + NS * 256;
   static_assert(WN * WM == 8 && TN % 64 == 0 && 128 % TN == 0 && XR + NS <= 8 && D * kStage <= 160 * 1024, "the copies' shares");
@@ -392,8 +393,8 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const Fp8GemmArgs p, int 
 // columns x 112 tokens (112 accumulators a lane).  Per block of 128 it reads 4 + 7 fragments of 2 KB from LDS, converts
 // them (176 instructions) and issues 4 * 7 * 4 matrix instructions of 16 cycles and 112 fmas (out += scale * sum).
 //
-// Bound: the matrix unit, the vector instructions beside it and the power limit.  Measured, 8192 x 5120 x 17408: 1175 us,
-// 1.24 PFLOP/s at 1.95 GHz (a library bf16 product reaches 1.27 at 8192^3); with the copies left out 980, the fmas
+// Bound: the matrix unit, the vector instructions beside it and the power limit.  Measured, 8192 x 5120 x 17408: 1175 us (1130
+// to 1290 from card to card), 1.24 PFLOP/s at 1.95 GHz (a library bf16 product reaches 1.27 at 8192^3); with the copies left out 980, the fmas
 // 1078, the conversions 1160, the matrix instructions 789.  The same instructions from registers alone reach 1.7.
 //
 // LDS holds two stages of a block: weight rows, activation rows (128 bytes each),
@@ -619,8 +620,8 @@ __device__ inline floatx4 product_8bit(const Frag& w, const Frag& x) {
 // matrix instructions of 32 cycles; each instruction's four fmas (out += scale *
 // tmp) run three instructions later, beside the matrix unit.
 //
-// Bound: the matrix unit with the fmas beside it.  Measured, 8192 x 5120 x 17408: 633-646 us, 2.2-2.3 PFLOP/s (8192 x
-// 34816 x 5120 2.17, 8192^3 2.21), at a clock of 1.9 GHz under this load; the same instructions and fmas from registers
+// Bound: the matrix unit with the fmas beside it.  Measured, 8192 x 5120 x 17408: 635-715 us from card to card, 2.0-2.3 PFLOP/s
+// (8192 x 34816 x 5120 1.9-2.2, 8192^3 1.9-2.2), at a clock of 1.9 GHz under this load; the same instructions and fmas from registers
 // alone reach 3.1, a library product with a single scale 2.06 at this size and 2.7 at 8192^3.  Other forms at this
 // size, in the version where this one took 659: 256 x 256 tiles 732 (their sums no longer fit beside the fragments in the
 // vector registers and are moved to and fro), two waves per SIMD with half the accumulators each 704 (twice the
@@ -853,8 +854,8 @@ hipError_t launch_ring_as(const Fp8GemmArgs& g, float* ws, hipStream_t s) {
   const int tiles_m = (g.M + T::TM - 1) / T::TM, tiles_n = (g.N + T::TN - 1) / T::TN, blocks = (g.K + 127) / 128;
   const int64_t tiles = (int64_t)tiles_m * tiles_n, steps = tiles * blocks;
   // At least 4 steps a workgroup, where a tile has them: fewer sums to join.  Measured, us with at least 1, 2, 4, 8:
-  // 1 x 1024 x 5120 11.0, 9.4, 8.5, 9.2; 40 x 2048 x 2048 12.8, 10.4, 9.9, 10.6; 128 x 1024 x 5120 18.5, 15.1, 12.5, 13.2;
-  // 200 x 1024 x 5120 24.0, 20.3, 16.8, 17.8; 77 x 1000 x 2064 float32 12.7, 11.1, 11.8, 15.5.
+  // 1 x 1024 x 5120 13.3, 11.8, 11.1, 11.4; 40 x 2048 x 2048 13.3, 11.3, 11.7, 13.9; 128 x 1024 x 5120 18.9, 16.2, 14.7, 16.8;
+  // 200 x 1024 x 5120 24.4, 21.3, 19.7, 23.1; 77 x 1000 x 2064 float32 13.3, 11.9, 12.5, 16.5.
   const int64_t want = tiles > steps / 4 ? tiles : steps / 4;
   const int groups = (int)(want < kRingGroups ? want : kRingGroups);
   const auto fn = fp8_ring_kernel<FN, FM, WN, WM, D, OUT>;
@@ -895,7 +896,7 @@ size_t fp8_gemm_workspace(int64_t m) {
 // whose partial sums and join cost 10 more, against whole 256 x 224 tiles with 2.6 to 2.9 us a step, or 1.55 with the 8-bit instruction.
 // Measured, us, shared | whole | whole with the 8-bit instruction: 224 x 34816 x 5120 108 | 126 | 76; 512 x 5120 x 5120 51 | 105
 // | -; 448 x 5120 x 17408 95 | 370 | 188; 1024 x 5120 x 5120 78 | 108 | 61; 1024 x 34816 x 5120 432 | 344 | 214; 2048 x 5120 x
-// 17408 400 | 349 | 205; 8192 x 5120 x 17408 1467 | 1175 | 640-668.
+// 17408 400 | 349 | 205; 8192 x 5120 x 17408 1467 | 1175 | 635-715.
 namespace {
 enum class Form { kRing, kTile, kPipe };
 Form form_of(const Fp8GemmArgs& g) {
